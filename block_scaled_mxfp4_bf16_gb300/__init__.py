@@ -21,7 +21,8 @@ __all__ = [
     "mxfp4_gemm_workspace_size", "mxfp4_workspace_init", "mxfp4_gemm", "mxfp4_gemm_host", "mxfp4_gemm_noalloc",
     "mxfp4_gemm_plan", "mxfp4_gemm_plan_model", "mxfp4_device_status", "mxfp4_selftest_timeout", "mxfp4_version",
     "PreparedCall", "prepare_gemm", "prepare_gemm_host", "TokenBlocks", "mxfp4_token_tile", "mxfp4_token_blocks_size",
-    "mxfp4_quantize_tokens", "mxfp4_gemm_tokens", "mxfp4_gemm_unpacked",
+    "mxfp4_quantize_tokens", "mxfp4_gemm_tokens", "mxfp4_gemm_unpacked", "mxfp4_gemv", "mxfp4_grouped_gemm",
+    "mxfp4_prepack_experts", "MoeRouting", "mxfp4_moe_route", "mxfp4_moe_combine",
 ]
 
 _LOCK = threading.Lock()
@@ -124,6 +125,22 @@ def load_library() -> ctypes.CDLL:
             L.mxfp4_call_run.restype = _int
             L.mxfp4_call_destroy.argtypes = [_vp]
             L.mxfp4_call_destroy.restype = None
+            L.mxfp4_gemv_workspace_size.argtypes = [_i64, _i64, _i64]
+            L.mxfp4_gemv_workspace_size.restype = _sz
+            L.mxfp4_gemv.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _sz, _vp]
+            L.mxfp4_gemv.restype = _int
+            L.mxfp4_grouped_gemm_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
+            L.mxfp4_grouped_gemm_workspace_size.restype = _sz
+            L.mxfp4_grouped_gemm.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64,
+                                             ctypes.c_uint, _vp, _sz, _vp]
+            L.mxfp4_grouped_gemm.restype = _int
+            L.mxfp4_moe_route_workspace_size.argtypes = [_i64, _i64]
+            L.mxfp4_moe_route_workspace_size.restype = _sz
+            L.mxfp4_moe_route.argtypes = [_vp, _int, _i64, _i64, _i64, _int, ctypes.c_uint, _vp, _vp, _vp, _vp, _vp,
+                                          _vp, _sz, _vp]
+            L.mxfp4_moe_route.restype = _int
+            L.mxfp4_moe_combine.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _int, _vp, _i64, _vp]
+            L.mxfp4_moe_combine.restype = _int
             _LIB = L
     return _LIB
 
@@ -585,3 +602,7 @@ def mxfp4_device_status(stream=None) -> int:
 
 def mxfp4_selftest_timeout(limit_us: int, stream=None) -> None:
     _check(load_library().mxfp4_selftest_timeout(limit_us, _stream(stream)), "mxfp4_selftest_timeout")
+
+
+from .moe import (MoeRouting, mxfp4_gemv, mxfp4_grouped_gemm, mxfp4_moe_combine, mxfp4_moe_route,  # noqa: E402
+                  mxfp4_prepack_experts)

@@ -16,7 +16,7 @@ __device__ uint32_t g_device_status;   // bit 0: a bounded wait gave up
 
 static thread_local int t_last_cuda_error = 0;
 
-static int cuda_fail(cudaError_t e) {
+int cuda_fail(cudaError_t e) {
     t_last_cuda_error = static_cast<int>(e);
     return MXFP4_ERR_CUDA;
 }
@@ -470,6 +470,7 @@ static int cached_plan(const DeviceInfo& di, int64_t M, int64_t N, int64_t K, in
 }
 
 static uint64_t g_wait_limit_ns = 1000000000ull;   // 1 s per bounded wait
+uint64_t wait_limit_ns() { return g_wait_limit_ns; }
 
 #ifdef MXFP4_TEST_HOOKS
 static void* g_token_dump = nullptr;   // test build only: see mxfp4_test_token_dump
@@ -627,7 +628,7 @@ const char* mxfp4_status_string(int status) {
 
 int mxfp4_last_cuda_error(void) { return t_last_cuda_error; }
 
-int mxfp4_version(void) { return 204; }
+int mxfp4_version(void) { return 205; }
 
 int mxfp4_quantize(const void* x, int64_t rows, int64_t K, int64_t ld, void* q, void* scales, void* stream) {
     if (rows < 0 || K < 0) return MXFP4_ERR_ARG;

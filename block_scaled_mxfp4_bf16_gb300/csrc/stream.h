@@ -1,0 +1,84 @@
+// Shared definitions of the streaming product over ragged groups (grouped GEMM and weight-only
+// product): group tiling, workspace layout, kernel arguments (not part of the public ABI).
+#pragma once
+#include "internal.h"
+
+namespace mxfp4 {
+
+constexpr int kMaxGroups = 1024;          // groups (experts) one launch can address
+constexpr int kStreamThreads = 384;       // warps 0-3: copies, MMAs, two spare; warps 4-11: epilogue
+constexpr int kStreamEpiThreads = 256;
+constexpr int kStreamMaxStages = 10;
+constexpr int kTerms = 8;                 // e2m1 terms an activation is expanded into (weight-only)
+
+// A group of n rows is cut into tiles_of(n) token tiles of tile_rows(n) rows (a multiple of 16,
+// the last tile holds the rest): equal tiles instead of full ones and a remainder, since a tile's
+// cost is its weight stream and does not shrink with its rows.
+__host__ __device__ inline int tiles_of(int n, int m_tile) { return (n + m_tile - 1) / m_tile; }
+__host__ __device__ inline int tile_rows(int n, int m_tile) {
+    const int t = tiles_of(n, m_tile);
+    return t ? ((n + t - 1) / t + 15) / 16 * 16 : 16;
+}
+// Token-block index of tile i of group g whose rows start at `begin`: distinct for every tile of
+// every group without a prefix sum over the groups (floor(begin / m_tile) grows by at least
+// tiles_of(n) - 1 from one group to the next, and g by one), and below stream_tile_bound.
+__host__ __device__ inline int tile_slot(int begin, int g, int i, int m_tile) { return begin / m_tile + g + i; }
+__host__ __device__ inline int64_t stream_tile_bound(int64_t rows, int64_t groups, int m_tile) {
+    return rows / m_tile + groups + 1;
+}
+
+struct StreamArgs {
+    const uint8_t* tblk;      // token blocks [tile slot][k_atoms][a_block]
+    const uint8_t* wblk;      // packed weights, group_bytes from one group to the next
+    size_t group_bytes;
+    const int32_t* offsets;   // [groups + 1], or null: one group of `rows` rows
+    uint16_t* c;
+    int64_t ldc;
+    float* partial;           // [2 * CTAs][128 * tokens per tile] fp32 partial sums of split units
+    uint32_t* counters;       // [CTAs + 1] arrivals per split unit, zero at the start
+    uint32_t* status;
+    int groups, rows, N;      // rows: token-block rows (grouped) or tokens * terms (weight-only)
+    int m_tile, nmc, n_tiles, k_atoms, stages;
+    int min_steps;            // fewest 256-K steps a split unit's share has
+    uint32_t a_block;
+    uint32_t tmem_cols;
+    uint64_t wait_limit_ns;
+};
+
+struct StreamPlan {
+    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, min_steps;
+    uint32_t a_block, tmem_cols;
+    size_t smem_bytes;
+    size_t off_counters, off_partial, ws_total;   // workspace: token blocks at 0
+};
+
+// Plan for `rows` token-block rows in `groups` groups; terms: 1 (grouped) or kTerms.
+int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count, StreamPlan* plan);
+
+// a [tokens, K] rows -> token blocks of the sorted rows: row r of the blocks is a[index ? index[r] : r].
+cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,
+                                   const int32_t* offsets, int groups, int rows, bool gated, const StreamPlan& plan,
+                                   uint8_t* blocks, uint32_t* counters, cudaStream_t s);
+// x [M, K] rows -> kTerms token-block rows per token.
+cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx, const StreamPlan& plan,
+                                uint8_t* blocks, uint32_t* counters, cudaStream_t s);
+cudaError_t launch_stream(const StreamPlan& plan, const StreamArgs& args, int terms, cudaStream_t s);
+
+// Routing and combination (moe.cu).
+struct RouteArgs {
+    const void* logits;
+    int64_t ld;
+    int bf16;
+    int T, E, k, renormalize;
+    float* weights;
+    int32_t *experts, *offsets, *rows, *slots;
+    int32_t* hist;            // workspace: [chunks][E] counts, then their exclusive prefix
+    int chunk;                // tokens per CTA
+    int chunks;
+};
+int route_chunk(int64_t T);
+cudaError_t launch_route(const RouteArgs& args, cudaStream_t s);
+cudaError_t launch_combine(const uint16_t* y, int64_t rows, int64_t ldy, const int32_t* slots, const float* weights,
+                           int64_t T, int k, int64_t N, uint16_t* out, int64_t ldo, cudaStream_t s);
+
+}  // namespace mxfp4

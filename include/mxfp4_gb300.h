@@ -66,7 +66,8 @@ int mxfp4_last_cuda_error(void);
  * 2.02: token-block entry points (mxfp4_quantize_tokens, mxfp4_gemm_tokens). 2.03: prepared
  * calls (mxfp4_call_create, mxfp4_call_create_host, mxfp4_call_run, mxfp4_call_destroy), the
  * scale_stores field of mxfp4_plan_info, mxfp4_gemm_unpacked. 2.04: mxfp4_gemm_options.flags
- * (MXFP4_GEMM_A_READY) and mxfp4_plan_info.a_early. */
+ * (MXFP4_GEMM_A_READY) and mxfp4_plan_info.a_early. 2.05: mxfp4_gemv, mxfp4_grouped_gemm,
+ * mxfp4_moe_route, mxfp4_moe_combine. */
 int mxfp4_version(void);
 
 /*
@@ -439,6 +440,104 @@ int mxfp4_selftest_timeout(int limit_us, void *stream);
 int mxfp4_gemm_noalloc(const void *a, int64_t M, int64_t K, int64_t lda,
                        const void *packed_b, int64_t N,
                        void *c, int64_t ldc, void *stream);
+
+/*
+ * mxfp4_gemv -- the weight-only product Y = X . W^T for a few tokens: W in MXFP4, X kept in bf16.
+ * Reads the packed weights of mxfp4_gemm, so a model keeps one copy of them for its prompts
+ * (mxfp4_gemm) and for single tokens. Unlike mxfp4_gemm, X is not quantized to 4 bits: every 1x32
+ * block of X is expanded into eight e2m1 terms with a scale each, which hold it to within 2^-22
+ * of the block's largest magnitude, the terms are extra token rows of the block-scaled MMA, and
+ * each token's terms are added in fp32. So y is the fp32 product of the bf16 x and the values
+ * the weights stand for, rounded once to bf16.
+ *   x        : bf16 [M, K], row stride ldx elements (ldx >= K, ldx % 8 == 0), 16-byte aligned.
+ *   packed_b : buffer written by mxfp4_prepack_b for the same N and K, 1024-byte aligned.
+ *   y        : out, bf16 [M, N], row stride ldy elements (ldy >= N), 2-byte aligned.
+ *   workspace: ws_bytes >= mxfp4_gemv_workspace_size(M, N, K), 256-byte aligned; its previous
+ *              contents do not matter. Calls sharing a workspace must be ordered.
+ *   M        : any with M * ceil(K / 256) <= 2^25; meant for up to 16 (past that every 16 tokens
+ *              read the weights again, and mxfp4_gemm is the faster product).  K: positive
+ *              multiple of 8.
+ * M == 0 or N == 0 is a no-op. A token whose x holds an infinity or NaN gets NaN outputs; other
+ * tokens are not affected. Values of x below 2^-127 may count as zero. Ordering as mxfp4_gemm: x
+ * is read and y written after the work before the call on `stream`, packed_b is requested before.
+ * Runs on the same inputs give the same bits. mxfp4_gemv_workspace_size returns 0 for invalid
+ * sizes or without a usable device.
+ */
+size_t mxfp4_gemv_workspace_size(int64_t M, int64_t N, int64_t K);
+int mxfp4_gemv(const void *x, int64_t M, int64_t K, int64_t ldx, const void *packed_b, int64_t N,
+               void *y, int64_t ldy, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * mxfp4_grouped_gemm -- matrix products grouped by expert, of ragged sizes that only the device
+ * knows: the R rows of C are sorted by group, group g has rows offsets[g] .. offsets[g+1], and
+ *   C[r, :] = MXFP4(A[rows[r], :]) . MXFP4(B_g)^T
+ * with the quantization, products and rounding of mxfp4_gemm (A quantized inside the call).
+ *   a        : bf16 [tokens, K], row stride lda (lda >= K, lda % 8 == 0), 16-byte aligned.
+ *   rows     : device int32 [R], the row of A that each row of C reads (mxfp4_moe_route's); an
+ *              index outside [0, tokens) stands for a row of zeros. NULL: row r of A, tokens == R.
+ *   offsets  : device int32 [groups + 1], not decreasing, within [0, R]. Rows of C before
+ *              offsets[0] and from offsets[groups] on are not written. Offsets that break this
+ *              rule leave C unwritten as a whole (no access out of bounds).
+ *   packed_b : the groups' packed weights one after the other, each written by mxfp4_prepack_b for
+ *              N and K (mxfp4_prepack_b_size(N, K) bytes each), 1024-byte aligned.
+ *   c        : out, bf16 [R, N], row stride ldc (ldc >= N), 2-byte aligned.
+ *   flags    : 0, or MXFP4_GROUPED_GATED: a row of A is [g, u], K elements each (lda >= 2K), and
+ *              silu(g) * u, computed in fp32 and not rounded before, is what is quantized: the
+ *              input of an expert's second projection from the output of its first.
+ *   workspace: ws_bytes >= mxfp4_grouped_gemm_workspace_size(R, groups, N, K), 256-byte aligned;
+ *              its previous contents do not matter. Calls sharing a workspace must be ordered.
+ * Limits: groups <= 1024, R <= 2^30, sizes otherwise as mxfp4_gemm (MXFP4_ERR_SHAPE beyond).
+ * R == 0, N == 0 or groups == 0 is a no-op. Ordering: a, rows and offsets are read after the work
+ * before the call on `stream`; packed_b must not be written by work still running then that lets
+ * dependent launches start early. Runs on the same inputs give the same bits.
+ */
+#define MXFP4_GROUPED_GATED 1u
+size_t mxfp4_grouped_gemm_workspace_size(int64_t R, int64_t groups, int64_t N, int64_t K);
+int mxfp4_grouped_gemm(const void *a, int64_t tokens, int64_t K, int64_t lda, const int32_t *rows,
+                       const int32_t *offsets, int64_t groups, const void *packed_b, int64_t N,
+                       void *c, int64_t R, int64_t ldc, unsigned flags, void *workspace, size_t ws_bytes,
+                       void *stream);
+
+/*
+ * mxfp4_moe_route -- the k experts with the largest logits of every token, their softmax weights,
+ * and the token-expert pairs grouped by expert for mxfp4_grouped_gemm and mxfp4_moe_combine.
+ *   logits  : [T, E], row stride ld (ld >= E), fp32 (dtype MXFP4_F32) or bf16 (MXFP4_BF16),
+ *             aligned to its type. Equal logits: the lower index first. An expert whose logit is
+ *             -inf or NaN is never chosen (a mask); a token with fewer than k others gets fewer.
+ *   k       : 1 .. min(E, MXFP4_ROUTE_MAX_K).  E <= 1024, T * k <= 2^30.
+ *   flags   : 0: the weights are the softmax over the chosen experts; MXFP4_ROUTE_ALL_EXPERTS:
+ *             over all experts of the token (then they add up to less than one).
+ *   weights : out, fp32 [T, k], largest first; 0 where nothing was chosen.
+ *   experts : out, int32 [T, k]; -1 where nothing was chosen.
+ *   offsets : out, int32 [E + 1]: expert e has the sorted rows offsets[e] .. offsets[e+1].
+ *   rows    : out, int32 [T * k]: the token of every sorted row, tokens ascending within an
+ *             expert; -1 from offsets[E] on.
+ *   slots   : out, int32 [T, k]: the sorted row of each pair; -1 where nothing was chosen.
+ *   workspace: ws_bytes >= mxfp4_moe_route_workspace_size(T, E), 4-byte aligned.
+ * All outputs are dense. T == 0 writes offsets (zeros) only.
+ */
+#define MXFP4_F32 0
+#define MXFP4_BF16 1
+#define MXFP4_ROUTE_MAX_K 32
+#define MXFP4_ROUTE_ALL_EXPERTS 1u
+size_t mxfp4_moe_route_workspace_size(int64_t T, int64_t E);
+int mxfp4_moe_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t ld, int k, unsigned flags,
+                    float *weights, int32_t *experts, int32_t *offsets, int32_t *rows, int32_t *slots,
+                    void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * mxfp4_moe_combine -- out[t, :] = sum over j of weights[t, j] * y[slots[t, j], :], added in fp32 in
+ * the order of j and rounded once to bf16: the experts' outputs back in token order.
+ *   y       : bf16 [R, N], row stride ldy (ldy >= N), 2-byte aligned.
+ *   slots   : device int32 [T, k] (mxfp4_moe_route's); one outside [0, R) adds nothing, and its
+ *             weight is not used. A token without any gets zeros.
+ *   weights : device fp32 [T, k].
+ *   out     : bf16 [T, N], row stride ldo (ldo >= N), 2-byte aligned.
+ * Rows of 16-byte aligned, 8-element multiples move in 16-byte pieces, others by elements.
+ * T == 0 or N == 0 is a no-op.
+ */
+int mxfp4_moe_combine(const void *y, int64_t R, int64_t N, int64_t ldy, const int32_t *slots, const float *weights,
+                      int64_t T, int k, void *out, int64_t ldo, void *stream);
 
 #ifdef __cplusplus
 }
