@@ -150,8 +150,14 @@ def _check(status: int, where: str) -> None:
         raise Mxfp4Error(status, where)
 
 
+# the current stream's handle without building a Stream object for it (2.9 us a call less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
