@@ -251,6 +251,24 @@ __device__ __forceinline__ void tc_copy_sf_if(uint32_t issue, uint32_t taddr, ui
         ::"r"(taddr), "l"(src_desc), "r"(issue)
         : "memory");
 }
+__device__ __forceinline__ void bulk_load_if(uint32_t issue, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                             uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1], %2, [%3], %4;\n\t}"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_expect_if(uint32_t issue, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %2, 0;\n\t"
+        "@e mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}"
+        ::"r"(bar), "r"(bytes), "r"(issue)
+        : "memory");
+}
 __device__ __forceinline__ void tc_commit_if(uint32_t issue, uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .pred e;\n\t"
@@ -433,64 +451,68 @@ mxfp4_stream_kernel(const StreamArgs p) {
 
     if (warp == 0) {
         // ---------------------------------------------------------------------- copies
-        if (lane == 0) {
-            const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
-            // the weights of the first stages go out before the wait on the token-block writer
-            int early = 0;
-            {
-                Schedule d = plan;
-                Share f;
-                while (early < p.stages && next_share(d, f)) {
-                    const Unit u = locate(p, prefix, f.unit);
-                    const uint8_t* w = p.wblk + static_cast<size_t>(u.group) * p.group_bytes +
-                                       (static_cast<size_t>(u.nt) * p.k_atoms + f.k0) * kWBlock;
-                    const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15);
-                    const uint32_t tok = n16 * 128u + (n16 > 128u ? 4u : 2u) * kSfChunk;
-                    for (int j = 0; j < f.nk && early < p.stages; ++j, ++early) {
-                        mbar_arrive_expect_tx(&full[early], kWBlock + tok);
-                        bulk_load(sW + early * kWBlock, w + static_cast<size_t>(j) * kWBlock, kWBlock, &full[early], pol_w);
-                    }
-                }
-            }
-            pdl_wait_prior_grid();
+        const uint32_t issue = elect_lane();
+        const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
+        const uint32_t sw0 = smem_addr(sW), st0 = smem_addr(sT), full0 = smem_addr(full);
+        const uint32_t sf_off = static_cast<uint32_t>(p.m_tile) * 128u;
+        // the weights of the first stages go out before the wait on the token-block writer
+        int early = 0;
+        {
             Schedule d = plan;
             Share f;
-            int s = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            while (ok && next_share(d, f)) {
+            while (early < p.stages && next_share(d, f)) {
                 const Unit u = locate(p, prefix, f.unit);
                 const uint8_t* w = p.wblk + static_cast<size_t>(u.group) * p.group_bytes +
                                    (static_cast<size_t>(u.nt) * p.k_atoms + f.k0) * kWBlock;
-                const uint8_t* t = p.tblk + (static_cast<size_t>(u.slot) * p.k_atoms + f.k0) * p.a_block;
                 const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15);
-                const uint32_t tok_rows = n16 * 128u, tok_sf = (n16 > 128u ? 4u : 2u) * kSfChunk;
-                for (int j = 0; j < f.nk; ++j) {
-                    if (issued >= p.stages && !mbar_wait(&empty[s], phase ^ 1u, lim)) {
-                        stream_fail(p, abort_flag);
-                        ok = false;
-                        break;
-                    }
-                    if (issued >= early) {
-                        mbar_arrive_expect_tx(&full[s], kWBlock + tok_rows + tok_sf);
-                        bulk_load(sW + s * kWBlock, w + static_cast<size_t>(j) * kWBlock, kWBlock, &full[s], pol_w);
-                    }
-                    const uint8_t* tj = t + static_cast<size_t>(j) * p.a_block;
-                    uint8_t* dst = sT + static_cast<uint32_t>(s) * p.a_block;
-                    bulk_load(dst, tj, tok_rows, &full[s], pol_t);
-                    bulk_load(dst + p.m_tile * 128, tj + p.m_tile * 128, tok_sf, &full[s], pol_t);
-                    ++issued;
-                    if (++s == p.stages) {
-                        s = 0;
-                        phase ^= 1u;
-                    }
+                const uint32_t tok = n16 * 128u + (n16 > 128u ? 4u : 2u) * kSfChunk;
+                for (int j = 0; j < f.nk && early < p.stages; ++j, ++early, w += kWBlock) {
+                    const uint32_t bar = full0 + static_cast<uint32_t>(early) * 8u;
+                    mbar_expect_if(issue, bar, kWBlock + tok);
+                    bulk_load_if(issue, sw0 + static_cast<uint32_t>(early) * kWBlock, w, kWBlock, bar, pol_w);
                 }
             }
-            // no copy may be in flight when the CTA ends (after a failure the MMA warp may have
-            // stopped waiting for them): the last fill of every stage
-            for (int j = max(0, issued - p.stages); j < issued; ++j)
-                mbar_wait(&full[j % p.stages], (j / p.stages) & 1, lim);
         }
+        pdl_wait_prior_grid();
+        Schedule d = plan;
+        Share f;
+        int s = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && next_share(d, f)) {
+            const Unit u = locate(p, prefix, f.unit);
+            const uint8_t* w = p.wblk + static_cast<size_t>(u.group) * p.group_bytes +
+                               (static_cast<size_t>(u.nt) * p.k_atoms + f.k0) * kWBlock;
+            const uint8_t* t = p.tblk + (static_cast<size_t>(u.slot) * p.k_atoms + f.k0) * p.a_block;
+            const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15);
+            const uint32_t tok_rows = n16 * 128u, tok_sf = (n16 > 128u ? 4u : 2u) * kSfChunk;
+            for (int j = 0; j < f.nk; ++j) {
+                if (issued >= p.stages && !mbar_wait(&empty[s], phase ^ 1u, lim)) {
+                    stream_fail(p, abort_flag);
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
+                if (issued >= early) {
+                    mbar_expect_if(issue, bar, kWBlock + tok_rows + tok_sf);
+                    bulk_load_if(issue, sw0 + static_cast<uint32_t>(s) * kWBlock, w, kWBlock, bar, pol_w);
+                }
+                const uint32_t dst = st0 + static_cast<uint32_t>(s) * p.a_block;
+                bulk_load_if(issue, dst, t, tok_rows, bar, pol_t);
+                bulk_load_if(issue, dst + sf_off, t + sf_off, tok_sf, bar, pol_t);
+                w += kWBlock;
+                t += p.a_block;
+                ++issued;
+                if (++s == p.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // no copy may be in flight when the CTA ends (after a failure the MMA warp may have
+        // stopped waiting for them): the last fill of every stage
+        for (int j = max(0, issued - p.stages); j < issued; ++j)
+            mbar_wait(&full[j % p.stages], (j / p.stages) & 1, lim);
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------------- MMAs
