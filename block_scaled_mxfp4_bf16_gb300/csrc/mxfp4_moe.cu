@@ -13,17 +13,22 @@ constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kSub = 128;                   // tokens ranked at a time by one bit mask per expert
 constexpr int kSubWords = kSub / 32;
-constexpr int kRouteChunks = 128;           // most chunks the tokens are cut into
 
 // Order-preserving key of a logit: larger logits have larger keys; 0 for NaN and -inf, which are
-// never routed. +0 and -0 compare equal.
+// never routed. +0 and -0 get the same key.
 __device__ __forceinline__ uint32_t logit_key(float v) {
-    if (!(v > -INFINITY)) return 0u;
-    const uint32_t b = __float_as_uint(v == 0.f ? 0.f : v);
-    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+    const uint32_t b = __float_as_uint(v + 0.f);                     // -0 + 0 = +0
+    const uint32_t key = b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+    // -inf is 0x007FFFFF with the negative NaNs below, +inf 0xFF800000 with the positive ones above
+    return key - 0x00800000u <= 0xFF000000u ? key : 0u;
 }
 __device__ __forceinline__ float key_logit(uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+}
+
+// The key of a bf16 logit again from its upper 16 bits (a negative one's lower bits are ones).
+__device__ __forceinline__ uint32_t bf16_logit_key(uint32_t key) {
+    return (key & 0xFFFF0000u) | ((key & 0x80000000u) ? 0u : 0xFFFFu);
 }
 
 template <bool kBf16>
@@ -35,56 +40,124 @@ __device__ __forceinline__ float load_logit(const void* base, int64_t i) {
 // exp(v - m), 1 where both are the same infinity
 __device__ __forceinline__ float exp_below(float v, float m) { return v == m ? 1.f : expf(v - m); }
 
-// One warp, one token: lane l holds experts l, l + 32, ... as keys. k rounds of a warp-wide
-// maximum (redux on the keys, then on the indexes that reach it: ties go to the lowest index);
-// lane j keeps the j-th winner. Returns its key (0: none) and expert.
+// Compare-exchange network for kPer = 2^m keys, largest first (Batcher's odd-even merge sort).
+template <int kPer>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[kPer]) {
+#pragma unroll
+    for (int p = 1; p < kPer; p <<= 1)
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j + q < kPer; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < kPer && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const uint32_t hi = max(key[i + j], key[i + j + q]), lo = min(key[i + j], key[i + j + q]);
+                        key[i + j] = hi;
+                        key[i + j + q] = lo;
+                    }
+}
+
+// One warp, one token: lane l holds experts l, l + 32, ..., as keys sorted once, largest first. k
+// rounds of a warp-wide maximum over the lanes' first keys; the lane that has it moves its list up.
+// Lane j keeps the j-th winner: its key (0: none), expert and softmax weight.
+//
+// bf16 logits: a key is the 16 ordered bits of the logit above 0xFFFF - expert, so all keys differ,
+// the largest is the one with the lowest index and the expert is read off it. fp32 logits: a key
+// has no room for the index. It is looked up at the end, in the winning lane's unsorted keys; where
+// two lanes share a winning key, the token is done again in rounds that compare the indexes too.
+// Bound by instructions: about 300 a token and warp for 256 experts and k = 8 (rounds that search
+// all of a lane's keys took 650).
 template <int kPer, bool kBf16>
 __device__ __forceinline__ void top_k(const RouteArgs& p, int t, int lane, uint32_t* key_out, int* expert_out,
                                       float* weight_out) {
-    uint32_t key[kPer];
+    uint32_t key[kPer], logit[kPer];
     const int64_t row = static_cast<int64_t>(t) * p.ld;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = lane + 32 * i;
-        key[i] = e < p.E ? logit_key(load_logit<kBf16>(p.logits, row + e)) : 0u;
+        logit[i] = e < p.E ? logit_key(load_logit<kBf16>(p.logits, row + e)) : 0u;
     }
-    float total = 0.f;
-    uint32_t mine = 0u;
-    int mine_e = -1;
-    uint32_t top = 0u;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if constexpr (kBf16)
+            key[i] = logit[i] ? (logit[i] & 0xFFFF0000u) | (0xFFFFu - static_cast<uint32_t>(lane + 32 * i)) : 0u;
+        else
+            key[i] = logit[i];
+    }
+    sort_keys<kPer>(key);
+    uint32_t mine = 0u, top = 0u, tied = 0u;
+    int from = 0, nth = 0, last_from = -1, last_nth = 0;
+    uint32_t last = 0u;
     for (int j = 0; j < p.k; ++j) {
-        uint32_t best = key[0];
-        int at = 0;
-#pragma unroll
-        for (int i = 1; i < kPer; ++i)
-            if (key[i] > best) {
-                best = key[i];
-                at = i;
-            }
-        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, key[0]);
         if (m == 0u) break;                       // fewer than k experts left
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? static_cast<uint32_t>(lane + 32 * at) : 0xffffffffu);
-        if (j == 0) {
-            top = m;
-            if (!p.renormalize) {                 // softmax over all experts: the sum before any is taken out
-                const float mv = key_logit(m);
-#pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (key[i]) total += exp_below(key_logit(key[i]), mv);
-            }
-        }
-        if ((e & 31u) == static_cast<uint32_t>(lane)) {
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (i == static_cast<int>(e >> 5)) key[i] = 0u;
+        const bool win = key[0] == m;
+        if (j == 0) top = m;
+        if constexpr (!kBf16) {
+            const uint32_t who = __ballot_sync(0xffffffffu, win);
+            tied |= who & (who - 1u);
+            const int w = __ffs(who) - 1;
+            last_nth = m == last && w == last_from ? last_nth + 1 : 0;   // an equal key of the same lane
+            last = m;
+            last_from = w;
         }
         if (lane == j) {
             mine = m;
-            mine_e = static_cast<int>(e);
+            from = last_from;
+            nth = last_nth;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) key[i] = win ? (i + 1 < kPer ? key[i + 1] : 0u) : key[i];
+    }
+    int mine_e = -1;
+    if constexpr (kBf16) {
+        if (mine) {
+            mine_e = static_cast<int>(0xFFFFu - (mine & 0xFFFFu));
+            mine = bf16_logit_key(mine);
+        }
+        top = bf16_logit_key(top);
+    } else if (tied == 0u) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const uint32_t v = __shfl_sync(0xffffffffu, logit[i], from & 31);
+            if (mine && v == mine && nth-- == 0) mine_e = from + 32 * i;
+        }
+    } else {
+        uint32_t left[kPer];
+        mine = 0u;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) left[i] = logit[i];
+        for (int j = 0; j < p.k; ++j) {
+            uint32_t best = left[0];
+            int at = 0;
+#pragma unroll
+            for (int i = 1; i < kPer; ++i)
+                if (left[i] > best) {
+                    best = left[i];
+                    at = i;
+                }
+            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+            if (m == 0u) break;
+            const uint32_t e = __reduce_min_sync(0xffffffffu, best == m ? static_cast<uint32_t>(lane + 32 * at) : 0xffffffffu);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (e == static_cast<uint32_t>(lane + 32 * i)) left[i] = 0u;
+            if (lane == j) {
+                mine = m;
+                mine_e = static_cast<int>(e);
+            }
         }
     }
-    const float w = mine ? exp_below(key_logit(mine), key_logit(top)) : 0.f;
-    if (p.renormalize) total = w;
+    float w = mine ? exp_below(key_logit(mine), key_logit(top)) : 0.f;
+    float total = w;
+    if (!p.renormalize) {                         // softmax over all of the token's experts
+        const float mv = key_logit(top);
+        total = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (logit[i]) total += exp_below(key_logit(logit[i]), mv);
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
     *key_out = mine;
@@ -127,20 +200,14 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sum, int* total) {
     return t - v + (warp ? warp_sum[warp - 1] : 0);
 }
 
-}  // namespace
-
-// Top-k of a chunk of tokens, a warp per token, and the chunk's count of every expert. The chunk
-// counts are what the scatter kernel needs to know where each chunk's rows go.
+// Top-k of a chunk of tokens, a warp per token; count[e] (shared): the chunk's tokens of expert e.
 template <bool kBf16>
-__global__ void __launch_bounds__(kRouteThreads)
-route_topk_kernel(const RouteArgs p) {
-    extern __shared__ int count[];   // [E]
-    pdl_wait_prior_grid();
+__device__ __forceinline__ void chunk_top_k(const RouteArgs& p, int chunk, int* count) {
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) count[e] = 0;
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t1 = min(p.T, (static_cast<int>(blockIdx.x) + 1) * p.chunk);
-    for (int t = static_cast<int>(blockIdx.x) * p.chunk + warp; t < t1; t += kRouteWarps) {
+    const int t1 = min(p.T, (chunk + 1) * p.chunk);
+    for (int t = chunk * p.chunk + warp; t < t1; t += kRouteWarps) {
         uint32_t key;
         int e;
         float w;
@@ -152,44 +219,31 @@ route_topk_kernel(const RouteArgs p) {
         }
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = count[e];
-    pdl_launch_dependents();
 }
 
-// Rows, slots and offsets. A chunk's first row of expert e is offsets[e] plus the counts of the
-// chunks before it; inside the chunk, kSub tokens at a time, a token's rank among those of its
-// expert is the number of set bits below its own in the expert's mask (a token has an expert once
-// at most), so the order is that of the tokens whatever order the threads run in.
-__global__ void __launch_bounds__(kRouteThreads)
-route_scatter_kernel(const RouteArgs p) {
-    extern __shared__ int base[];                                    // [E] next row of each expert
-    uint32_t* mask = reinterpret_cast<uint32_t*>(base + p.E);        // [E][kSubWords]
-    __shared__ int warp_sum[kRouteWarps];
-    pdl_wait_prior_grid();
-    const int c = static_cast<int>(blockIdx.x);
-    int all = 0, before = 0;
-    const int e0 = static_cast<int>(threadIdx.x);                    // E <= threads
-    if (e0 < p.E)
-        for (int i = 0; i < p.chunks; ++i) {
-            const int v = __ldcg(p.hist + static_cast<int64_t>(i) * p.E + e0);
-            all += v;
-            before += i < c ? v : 0;
-        }
+// Rows, slots and (chunk 0) offsets of a chunk. all, before: over all chunks and over those before
+// this one, the tokens of expert threadIdx.x. A chunk's first row of expert e is offsets[e] plus
+// `before`; inside the chunk, kSub tokens at a time, a token's rank among those of its expert is
+// the number of set bits below its own in the expert's mask (a token has an expert once at most),
+// so the order is that of the tokens whatever order the threads run in.
+__device__ __forceinline__ void chunk_scatter(const RouteArgs& p, int chunk, int all, int before, int* base,
+                                              uint32_t* mask, int* warp_sum) {
     int total;
     const int start = block_scan(all, warp_sum, &total);
+    const int e0 = static_cast<int>(threadIdx.x);                    // E <= threads
     if (e0 < p.E) {
         base[e0] = start + before;
-        if (c == 0) {
+        if (chunk == 0) {
             p.offsets[e0] = start;
             if (e0 == p.E - 1) p.offsets[p.E] = total;
         }
     }
     // rows past the last routed pair, a share per CTA
-    for (int64_t i = total + static_cast<int64_t>(c) * kRouteThreads + threadIdx.x; i < static_cast<int64_t>(p.T) * p.k;
-         i += static_cast<int64_t>(gridDim.x) * kRouteThreads)
+    for (int64_t i = total + static_cast<int64_t>(chunk) * kRouteThreads + threadIdx.x;
+         i < static_cast<int64_t>(p.T) * p.k; i += static_cast<int64_t>(gridDim.x) * kRouteThreads)
         p.rows[i] = -1;
-    const int t1 = min(p.T, (c + 1) * p.chunk);
-    for (int t0 = c * p.chunk; t0 < t1; t0 += kSub) {
+    const int t1 = min(p.T, (chunk + 1) * p.chunk);
+    for (int t0 = chunk * p.chunk; t0 < t1; t0 += kSub) {
         for (int i = threadIdx.x; i < p.E * kSubWords; i += kRouteThreads) mask[i] = 0u;
         __syncthreads();
         const int pairs = (min(t1, t0 + kSub) - t0) * p.k;
@@ -208,28 +262,107 @@ route_scatter_kernel(const RouteArgs p) {
             }
             p.slots[static_cast<int64_t>(t0) * p.k + i] = slot;
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
-            int n = 0;
-            for (int w = 0; w < kSubWords; ++w) n += __popc(mask[e * kSubWords + w]);
-            base[e] += n;
+        if (t0 + kSub < t1) {
+            __syncthreads();
+            for (int e = threadIdx.x; e < p.E; e += kRouteThreads) {
+                int n = 0;
+                for (int w = 0; w < kSubWords; ++w) n += __popc(mask[e * kSubWords + w]);
+                base[e] += n;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
-int route_chunk(int64_t T) {
-    const int64_t subs = (T + kSub - 1) / kSub;
-    return static_cast<int>((subs + kRouteChunks - 1) / kRouteChunks) * kSub;
+}  // namespace
+
+// All of a small call in one CTA.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRouteThreads)
+route_small_kernel(const RouteArgs p) {
+    extern __shared__ int count[];                                   // [E] counts, then next rows
+    uint32_t* mask = reinterpret_cast<uint32_t*>(count + p.E);       // [E][kSubWords]
+    __shared__ int warp_sum[kRouteWarps];
+    pdl_launch_dependents();
+    pdl_wait_prior_grid();
+    chunk_top_k<kBf16>(p, 0, count);
+    const int all = static_cast<int>(threadIdx.x) < p.E ? count[threadIdx.x] : 0;
+    chunk_scatter(p, 0, all, 0, count, mask, warp_sum);
+}
+
+// Top-k of every chunk, and the chunks' counts of every expert, which is what the scatter kernel
+// needs to know where each chunk's rows go.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRouteThreads)
+route_topk_kernel(const RouteArgs p) {
+    extern __shared__ int count[];   // [E]
+    pdl_launch_dependents();
+    pdl_wait_prior_grid();
+    chunk_top_k<kBf16>(p, static_cast<int>(blockIdx.x), count);
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = count[e];
+}
+
+// The counts are summed by the whole block, every thread an expert of some of the chunks, all its
+// loads in flight (one thread per expert and one load after the other took 10 us for 128 chunks).
+__global__ void __launch_bounds__(kRouteThreads)
+route_scatter_kernel(const RouteArgs p) {
+    extern __shared__ int base[];                                    // [E] next row of each expert
+    uint32_t* mask = reinterpret_cast<uint32_t*>(base + p.E);        // [E][kSubWords]
+    __shared__ int warp_sum[kRouteWarps];
+    pdl_launch_dependents();
+    pdl_wait_prior_grid();
+    const int c = static_cast<int>(blockIdx.x);
+    int* sum_all = base;
+    int* sum_before = reinterpret_cast<int*>(mask);
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) sum_all[e] = sum_before[e] = 0;
+    __syncthreads();
+    const int lanes = (p.E + 31) / 32 * 32, ways = kRouteThreads / lanes;   // E <= threads: at least one way
+    const int way = static_cast<int>(threadIdx.x) / lanes, e = static_cast<int>(threadIdx.x) - way * lanes;
+    if (way < ways && e < p.E) {
+        int all = 0, before = 0;
+        constexpr int kFlight = 16;
+        for (int i0 = way; i0 < p.chunks; i0 += kFlight * ways) {
+            int v[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                const int i = i0 + u * ways;
+                v[u] = i < p.chunks ? __ldcg(p.hist + static_cast<int64_t>(i) * p.E + e) : 0;
+            }
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                all += v[u];
+                before += i0 + u * ways < c ? v[u] : 0;
+            }
+        }
+        atomicAdd(&sum_all[e], all);
+        atomicAdd(&sum_before[e], before);
+    }
+    __syncthreads();
+    const int e0 = static_cast<int>(threadIdx.x);
+    const int all = e0 < p.E ? sum_all[e0] : 0, before = e0 < p.E ? sum_before[e0] : 0;
+    __syncthreads();                                                 // base and mask are written over from here
+    chunk_scatter(p, c, all, before, base, mask, warp_sum);
+}
+
+// Tokens per CTA: one CTA up to kSub tokens (one launch for the whole call), then as many as make a
+// CTA per SM, and no fewer than a warp's worth each.
+int route_chunk(int64_t T, int sm_count) {
+    if (T <= kSub) return kSub;
+    const int64_t per = (T + sm_count - 1) / sm_count;
+    return static_cast<int>(per < kRouteWarps ? kRouteWarps : per);
 }
 
 cudaError_t launch_route(const RouteArgs& args, cudaStream_t s) {
     const size_t count = static_cast<size_t>(args.E) * 4;
     const size_t scatter = count + static_cast<size_t>(args.E) * kSubWords * 4;
-    cudaError_t e = args.bf16 ? launch_pdl(route_topk_kernel<true>, dim3(args.chunks), dim3(kRouteThreads), count, s, args)
-                              : launch_pdl(route_topk_kernel<false>, dim3(args.chunks), dim3(kRouteThreads), count, s, args);
+    const dim3 grid(args.chunks), block(kRouteThreads);
+    if (args.chunks == 1)
+        return args.bf16 ? launch_pdl(route_small_kernel<true>, grid, block, scatter, s, args)
+                         : launch_pdl(route_small_kernel<false>, grid, block, scatter, s, args);
+    const cudaError_t e = args.bf16 ? launch_pdl(route_topk_kernel<true>, grid, block, count, s, args)
+                                    : launch_pdl(route_topk_kernel<false>, grid, block, count, s, args);
     if (e != cudaSuccess) return e;
-    return launch_pdl(route_scatter_kernel, dim3(args.chunks), dim3(kRouteThreads), scatter, s, args);
+    return launch_pdl(route_scatter_kernel, grid, block, scatter, s, args);
 }
 
 // ------------------------------------------------------------------------ combination

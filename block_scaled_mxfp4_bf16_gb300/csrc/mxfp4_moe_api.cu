@@ -48,8 +48,10 @@ int run_stream(const StreamPlan& plan, const DeviceInfo& di, uint8_t* ws, const 
     a.k_atoms = plan.k_atoms;
     a.stages = plan.stages;
     a.min_steps = plan.min_steps;
+    a.runs = plan.runs;
     a.a_block = plan.a_block;
     a.tmem_cols = plan.tmem_cols;
+    a.c_vec = aligned(c, 16) && ldc % 8 == 0 ? 1 : 0;
     a.wait_limit_ns = wait_limit_ns();
     const cudaError_t e = launch_stream(plan, a, terms, s);
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
@@ -125,14 +127,16 @@ int mxfp4_grouped_gemm(const void* a, int64_t tokens, int64_t K, int64_t lda, co
                       static_cast<int>(R), N, c, ldc, 1, s);
 }
 
-static int64_t route_chunks(int64_t T) {
-    const int64_t chunk = route_chunk(T);
+static int64_t route_chunks(int64_t T, int sm_count) {
+    const int64_t chunk = route_chunk(T, sm_count);
     return T > 0 ? (T + chunk - 1) / chunk : 1;
 }
 
 size_t mxfp4_moe_route_workspace_size(int64_t T, int64_t E) {
     if (T < 0 || E < 1 || E > kMaxGroups || T > kMaxRows) return 0;
-    return static_cast<size_t>(route_chunks(T)) * static_cast<size_t>(E) * 4;
+    DeviceInfo di;
+    if (device_info(&di) != MXFP4_OK) return 0;
+    return static_cast<size_t>(route_chunks(T, di.sm_count)) * static_cast<size_t>(E) * 4;
 }
 
 int mxfp4_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int k, unsigned flags,
@@ -146,10 +150,11 @@ int mxfp4_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t
     if (!aligned(logits, dtype == MXFP4_BF16 ? 2 : 4) || !aligned(weights, 4) || !aligned(experts, 4) ||
         !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(slots, 4) || !aligned(workspace, 4))
         return MXFP4_ERR_ALIGN;
-    if (!workspace || ws_bytes < mxfp4_moe_route_workspace_size(T, E)) return MXFP4_ERR_WORKSPACE;
     DeviceInfo di;
     const int st = device_info(&di);
     if (st != MXFP4_OK) return st;
+    const int64_t chunks = route_chunks(T, di.sm_count);
+    if (!workspace || ws_bytes < static_cast<size_t>(chunks) * static_cast<size_t>(E) * 4) return MXFP4_ERR_WORKSPACE;
     RouteArgs r = {};
     r.logits = logits;
     r.ld = ld;
@@ -164,8 +169,8 @@ int mxfp4_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t
     r.rows = rows;
     r.slots = slots;
     r.hist = static_cast<int32_t*>(workspace);
-    r.chunk = route_chunk(T);
-    r.chunks = static_cast<int>(route_chunks(T));
+    r.chunk = route_chunk(T, di.sm_count);
+    r.chunks = static_cast<int>(chunks);
     const cudaError_t e = launch_route(r, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }

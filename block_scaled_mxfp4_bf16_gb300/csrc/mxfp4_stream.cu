@@ -12,7 +12,8 @@
 // begin the next). A unit cut between CTAs is added up by whichever of them arrives last, in the
 // order of K from the fp32 sums that the others left in the workspace: no CTA waits for another,
 // and the result does not depend on the order of arrival. With few units (decoding) there is no
-// full wave and every SM streams an equal share of the weights.
+// full wave and every SM streams an equal share of the weights. (StreamArgs::runs: no waves, all
+// units cut into one run per CTA; see make_stream_plan.)
 //
 // Warps: 0 copies (weights and token blocks, one mbarrier per stage), 1 tensor memory and the
 // MMAs (two accumulators: the next unit's MMAs run while the last one is stored), 4-11 the
@@ -80,15 +81,18 @@ __device__ __forceinline__ void gate_pair(uint32_t g, uint32_t u, float* v) {
     v[1] = g1 / (1.f + expf(-g1)) * __uint_as_float(u & 0xFFFF0000u);
 }
 
-// One warp per 32 consecutive 1x32 blocks of one sorted row, a lane per block: the row's group is
-// looked up once per warp. Blocks past K become zero codes; an index outside [0, tokens) gives a
-// row of zeros. kGated: a row of a holds [g, u], K each, and silu(g) * u is quantized.
+// A warp takes `step` consecutive 1x32 blocks of one sorted row (all of them when there are rows
+// enough to fill the GPU), a lane per block, 32 at a time with the next 32 on their way: the row's
+// group and source are looked up once. Blocks past K become zero codes; an index outside
+// [0, tokens) gives a row of zeros. kGated: a row of a holds [g, u], K each, and silu(g) * u is
+// quantized. Bound by bytes when rows are many: 16384 x 7168 bf16 read (half of them from L2) and
+// 4.25 bits a value written, 45 us in all.
 template <bool kGated>
 __global__ void __launch_bounds__(256)
 quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K, int64_t lda,
                        const int32_t* index, const int32_t* offsets, int groups, int rows, int m_tile, int k_atoms,
                        uint32_t a_block, uint8_t* __restrict__ blocks, uint32_t* counters, int n_counters,
-                       int warps_per_row) {
+                       int parts, int step) {
     pdl_wait_prior_grid();   // a, index and offsets may come from the previous grid
     // dependents may start now: what they read early (the offsets) was complete before this grid
     pdl_launch_dependents();
@@ -97,10 +101,11 @@ quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K
     const int lane = threadIdx.x & 31;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int nblk = static_cast<int>((K + 31) / 32);
-    for (int64_t it = w; it < static_cast<int64_t>(rows) * warps_per_row; it += warps) {
-        const int r = static_cast<int>(it / warps_per_row);
-        const int kb = static_cast<int>(it - static_cast<int64_t>(r) * warps_per_row) * 32 + lane;
+    for (int64_t it = w; it < static_cast<int64_t>(rows) * parts; it += warps) {
+        const int r = static_cast<int>(it / parts);
+        const int kb0 = static_cast<int>(it - static_cast<int64_t>(r) * parts) * step;
+        const int kb1 = min(k_atoms * 8, kb0 + step);
+        const int64_t src = index ? static_cast<int64_t>(index[r]) : r;
         const int g = offsets ? group_of_row(offsets, groups, r, lane) : 0;
         if (g >= groups) continue;                 // past the last group
         int begin, n;
@@ -109,32 +114,45 @@ quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K
         const int per = tile_rows(n, m_tile);
         const int tile = (r - begin) / per;
         const uint32_t rr = static_cast<uint32_t>(r - begin - tile * per);
-        const int64_t src = index ? static_cast<int64_t>(index[r]) : r;
-        uint32_t v[16], out[4] = {0u, 0u, 0u, 0u}, byte = 0u;
-        if (kb < nblk && src >= 0 && src < tokens) {
-            const uint16_t* at = a + src * lda + static_cast<int64_t>(kb) * 32;
-            const int64_t left = K - static_cast<int64_t>(kb) * 32;
-            load_block32_upto(at, left, v);
-            if constexpr (kGated) {
-                uint32_t u[16];
-                float h[32];
-                load_block32_upto(at + K, left, u);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) gate_pair(v[i], u[i], &h[2 * i]);
-                byte = quantize_block32_f32(h, out);
-            } else {
-                byte = quantize_block32(v, out);
+        uint8_t* out_row = blocks + static_cast<size_t>(tile_slot(begin, g, tile, m_tile)) * k_atoms * a_block;
+        const uint16_t* row = a + src * lda;
+        const bool present = src >= 0 && src < tokens;
+        constexpr int kWords = kGated ? 32 : 16;
+        uint32_t next[kWords];
+        auto load = [&](int kb) {
+            const int64_t k = static_cast<int64_t>(kb) * 32;
+            if (present && kb < kb1 && k < K) {
+                load_block32_upto(row + k, K - k, *reinterpret_cast<uint32_t(*)[16]>(&next[0]));
+                if constexpr (kGated) load_block32_upto(row + K + k, K - k, *reinterpret_cast<uint32_t(*)[16]>(&next[16]));
             }
-        }
-        uint32_t word = byte << (8 * (lane & 3));
-        word |= __shfl_xor_sync(0xffffffffu, word, 1);
-        word |= __shfl_xor_sync(0xffffffffu, word, 2);
-        if (kb < k_atoms * 8) {
-            uint8_t* blk = blocks + (static_cast<size_t>(tile_slot(begin, g, tile, m_tile)) * k_atoms + (kb >> 3)) * a_block;
-            const uint32_t c = static_cast<uint32_t>(kb & 7);
-            *reinterpret_cast<uint4*>(blk + swz_chunk_offset(rr, c)) = make_uint4(out[0], out[1], out[2], out[3]);
-            if ((lane & 3) == 0)
-                *reinterpret_cast<uint32_t*>(blk + static_cast<uint32_t>(m_tile) * 128u + block_sf_offset(rr, c)) = word;
+        };
+        load(kb0 + lane);
+        for (int base = kb0; base < kb1; base += 32) {
+            const int kb = base + lane;
+            uint32_t v[kWords], out[4] = {0u, 0u, 0u, 0u}, byte = 0u;
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) v[i] = next[i];
+            load(kb + 32);
+            if (present && static_cast<int64_t>(kb) * 32 < K && kb < kb1) {
+                if constexpr (kGated) {
+                    float h[32];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) gate_pair(v[i], v[16 + i], &h[2 * i]);
+                    byte = quantize_block32_f32(h, out);
+                } else {
+                    byte = quantize_block32(v, out);
+                }
+            }
+            uint32_t word = byte << (8 * (lane & 3));
+            word |= __shfl_xor_sync(0xffffffffu, word, 1);
+            word |= __shfl_xor_sync(0xffffffffu, word, 2);
+            if (kb < kb1) {
+                uint8_t* blk = out_row + static_cast<size_t>(kb >> 3) * a_block;
+                const uint32_t c = static_cast<uint32_t>(kb & 7);
+                *reinterpret_cast<uint4*>(blk + swz_chunk_offset(rr, c)) = make_uint4(out[0], out[1], out[2], out[3]);
+                if ((lane & 3) == 0)
+                    *reinterpret_cast<uint32_t*>(blk + static_cast<uint32_t>(m_tile) * 128u + block_sf_offset(rr, c)) = word;
+            }
         }
     }
 }
@@ -278,79 +296,93 @@ __device__ __forceinline__ void tc_commit_if(uint32_t issue, uint64_t* bar) {
         : "memory");
 }
 
-// What every role of a CTA walks through: whole units first, then its run of the split units.
-struct Schedule {
-    int units, waves;          // all units; full waves of whole units
-    int64_t s, s1;             // this CTA's run of steps over the split units
-    int64_t share;             // steps per CTA of the split units
-    int wave;
-    int k_atoms, grid, cta;
-};
-
-struct Share {
-    int unit;                  // index over all units
+// What every role of a CTA walks through: its whole units, then its run of the split units, share
+// by share (a share is the part of one unit that is this CTA's).
+struct Walk {
+    // the share
+    int nt, slot, row0, rows;  // weight tile; token-block tile; its first sorted row and its rows
+    int k0, nk;                // 256-K steps [k0, k0 + nk) of the unit
     int split;                 // index among the split units, -1: the whole unit in one CTA
-    int k0, nk;                // 256-K steps [k0, k0 + nk)
+    // the schedule
+    int units, waves, wave;    // all units; full waves of whole units; the next wave
+    int64_t s, s1, share;      // the run over the steps of the split units; steps per CTA of them
+    // the group the unit lies in
+    int group, first, end;     // its units [first, end)
+    int tiles, per, begin, n;  // token tiles, rows per tile, sorted rows [begin, begin + n)
+    float inv_tiles;
 };
 
-__device__ __forceinline__ Schedule make_schedule(int units, int k_atoms, int min_steps) {
-    Schedule d;
-    d.units = units;
-    d.k_atoms = k_atoms;
-    d.grid = static_cast<int>(gridDim.x);
-    d.cta = static_cast<int>(blockIdx.x);
-    d.waves = units / d.grid;
-    d.wave = 0;
-    const int64_t steps = static_cast<int64_t>(units - d.waves * d.grid) * k_atoms;
-    d.share = max((steps + d.grid - 1) / d.grid, static_cast<int64_t>(min(min_steps, k_atoms)));
-    d.s = min(steps, d.share * d.cta);
-    d.s1 = min(steps, d.s + d.share);
-    return d;
-}
-
-__device__ __forceinline__ bool next_share(Schedule& d, Share& f) {
-    if (d.wave < d.waves) {
-        f.unit = d.wave * d.grid + d.cta;
-        f.split = -1;
-        f.k0 = 0;
-        f.nk = d.k_atoms;
-        ++d.wave;
-        return true;
+// Units are ordered by group, then weight tile, then token tile: the CTAs that work at the same
+// time share the group's weights as well as its tokens. `unit` never decreases along a walk, so the
+// group is found by stepping on from the last one, and its numbers are worked out once a group
+// (worked out again for every unit, with a search and four divisions, 6000 rows x 2880 x 2040
+// measured 56 us instead of 49).
+__device__ __forceinline__ void locate(const StreamArgs& p, const int* prefix, int unit, Walk& w) {
+    if (unit >= w.end) {
+        int g = w.group + 1;
+        while (prefix[g + 1] * p.n_tiles <= unit) ++g;
+        w.group = g;
+        w.first = prefix[g] * p.n_tiles;
+        w.end = prefix[g + 1] * p.n_tiles;
+        w.tiles = prefix[g + 1] - prefix[g];
+        w.inv_tiles = 1.f / static_cast<float>(w.tiles);
+        group_rows(p.offsets, p.rows, g, &w.begin, &w.n);
+        w.per = ((w.n + w.tiles - 1) / w.tiles + 15) / 16 * 16;   // tile_rows(n, m_tile)
     }
-    if (d.s >= d.s1) return false;
-    const int u = static_cast<int>(d.s / d.k_atoms);
-    f.unit = d.waves * d.grid + u;
-    f.k0 = static_cast<int>(d.s - static_cast<int64_t>(u) * d.k_atoms);
-    f.nk = static_cast<int>(min(static_cast<int64_t>(d.k_atoms - f.k0), d.s1 - d.s));
-    f.split = f.nk == d.k_atoms ? -1 : u;
-    d.s += f.nk;
-    return true;
+    const int r = unit - w.first;
+    int nt = w.tiles == 1 ? r : __float2int_rz(static_cast<float>(r) * w.inv_tiles);   // r / tiles, off by one at most
+    int i = r - nt * w.tiles;
+    if (i < 0) {
+        --nt;
+        i += w.tiles;
+    } else if (i >= w.tiles) {
+        ++nt;
+        i -= w.tiles;
+    }
+    w.nt = nt;
+    w.slot = tile_slot(w.begin, w.group, i, p.m_tile);
+    w.row0 = w.begin + i * w.per;
+    w.rows = min(w.per, w.n - i * w.per);
 }
 
-// Where a unit lies: its group, token tile and weight tile.
-struct Unit {
-    int group, nt, slot, row0, rows;   // rows: the tile's token-block rows; row0: its first sorted row
-};
-
-__device__ __forceinline__ Unit locate(const StreamArgs& p, const int* prefix, int unit) {
-    Unit u;
-    const int tile = unit / p.n_tiles;
-    u.nt = unit - tile * p.n_tiles;
-    int lo = 0, hi = p.groups;       // prefix[lo] <= tile < prefix[hi]
+__device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefix, int units) {
+    Walk w = {};
+    w.units = units;
+    w.waves = p.runs ? 0 : units / static_cast<int>(gridDim.x);
+    const int64_t steps = static_cast<int64_t>(units - w.waves * static_cast<int>(gridDim.x)) * p.k_atoms;
+    w.share = max((steps + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(min(p.min_steps, p.k_atoms)));
+    w.s = min(steps, w.share * blockIdx.x);
+    w.s1 = min(steps, w.s + w.share);
+    // the group before the first unit's, by bisection
+    const int unit = w.waves ? static_cast<int>(blockIdx.x) : static_cast<int>(w.s / p.k_atoms);
+    int lo = 0, hi = p.groups;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= tile) lo = mid;
+        if (prefix[mid] * p.n_tiles <= unit) lo = mid;
         else hi = mid;
     }
-    u.group = lo;
-    const int i = tile - prefix[lo];
-    int begin, n;
-    group_rows(p.offsets, p.rows, lo, &begin, &n);
-    const int per = tile_rows(n, p.m_tile);
-    u.slot = tile_slot(begin, lo, i, p.m_tile);
-    u.row0 = begin + i * per;
-    u.rows = min(per, n - i * per);
-    return u;
+    w.group = lo - 1;
+    w.end = 0;
+    return w;
+}
+
+__device__ __forceinline__ bool next_share(const StreamArgs& p, const int* prefix, Walk& w) {
+    if (w.wave < w.waves) {
+        locate(p, prefix, w.wave * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x), w);
+        w.split = -1;
+        w.k0 = 0;
+        w.nk = p.k_atoms;
+        ++w.wave;
+        return true;
+    }
+    if (w.s >= w.s1) return false;
+    const int u = static_cast<int>(w.s / p.k_atoms);
+    locate(p, prefix, w.waves * static_cast<int>(gridDim.x) + u, w);
+    w.k0 = static_cast<int>(w.s - static_cast<int64_t>(u) * p.k_atoms);
+    w.nk = static_cast<int>(min(static_cast<int64_t>(p.k_atoms - w.k0), w.s1 - w.s));
+    w.split = w.nk == p.k_atoms ? -1 : u;
+    w.s += w.nk;
+    return true;
 }
 
 __device__ __forceinline__ void stream_fail(const StreamArgs& p, volatile uint32_t* abort_flag) {
@@ -374,6 +406,70 @@ __device__ __forceinline__ void load_tokens(uint32_t taddr, float (&v)[16 / kTer
     }
 }
 
+// 32 columns of 16 lanes (from the lane and column of taddr) as the fragment of an m16n8 matrix
+// instruction per 8 columns: thread t holds rows t / 4 (v[4i], v[4i+1]) and t / 4 + 8 (v[4i+2],
+// v[4i+3]), columns 8i + 2 (t % 4) and the next.
+__device__ __forceinline__ void tmem_load_frag32(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Four 8x8 matrices of 16-bit values, stored transposed: lane 8m + r gives the address of row r
+// (a column of the fragments) of matrix m, eight values.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// A whole unit's accumulator (lane = weight row, column = token) -> bf16 C. A warp owns 32 weight
+// rows; per 8 tokens it packs its fragments, transposes them through 640 bytes of shared memory
+// (rows of 64 bytes, 80 apart) and stores 16 bytes a lane: one store instruction writes 64
+// contiguous bytes of each of 8 rows of C. (One column of 32 2-byte values per store measured
+// the same in waves, 3 % slower in runs.)
+__device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, int rows, int64_t row0, int n0, int half,
+                                           int lane, uint8_t* stage) {
+    const uint32_t st = smem_addr(stage);
+    const uint32_t put = st + static_cast<uint32_t>((lane & 7) * 80 + (lane >> 3) * 16);
+    const uint32_t got = st + static_cast<uint32_t>((lane >> 2) * 80 + (lane & 3) * 16);
+    const int n = n0 + (lane & 3) * 8;
+    for (int cb = half * 32; cb < rows; cb += 64) {
+        uint32_t lo[16], hi[16];
+        tmem_load_frag32(trow + static_cast<uint32_t>(cb), lo);
+        tmem_load_frag32(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
+        tmem_load_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (cb + 8 * i < rows) {
+                __syncwarp();
+                stmatrix_x4_trans(put, pack_bf16x2(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])),
+                                  pack_bf16x2(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])),
+                                  pack_bf16x2(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
+                                  pack_bf16x2(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])));
+                __syncwarp();
+                uint4 v;
+                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(got) : "memory");
+                const int m = cb + 8 * i + (lane >> 2);
+                if (m < rows && n < p.N) {
+                    uint16_t* cp = p.c + (row0 + m) * p.ldc + n;
+                    if (p.c_vec && n + 8 <= p.N) {
+                        *reinterpret_cast<uint4*>(cp) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (n + k < p.N) cp[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+                    }
+                }
+            }
+        }
+    }
+}
+
 }  // namespace
 
 template <int kTermsPer>
@@ -390,9 +486,10 @@ mxfp4_stream_kernel(const StreamArgs p) {
     uint64_t* acc_empty = acc_full + 2;                          // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    volatile uint32_t* last_flag = tmem_slot + 2;
-    int* warp_sum = reinterpret_cast<int*>(tmem_slot + 4);       // [16]
-    int* prefix = warp_sum + 16;                                 // [groups + 1] token tiles before a group
+    volatile uint32_t* last_flag = tmem_slot + 4;                // [4], each written once
+    int* warp_sum = reinterpret_cast<int*>(tmem_slot + 8);       // [16]
+    uint8_t* epi_stage = reinterpret_cast<uint8_t*>(warp_sum + 16);   // [8 warps][kEpiStage]
+    int* prefix = reinterpret_cast<int*>(epi_stage + 8 * kEpiStage);  // [groups + 1] token tiles before a group
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
@@ -446,27 +543,27 @@ mxfp4_stream_kernel(const StreamArgs p) {
     }
     if (threadIdx.x == 0) prefix[0] = 0;
     const int units = __syncthreads_or(bad ? 1 : 0) ? 0 : carry * p.n_tiles;
-    const Schedule plan = make_schedule(units, p.k_atoms, p.min_steps);
+    const Walk start = begin_walk(p, prefix, units);
     pdl_launch_dependents();
 
     if (warp == 0) {
         // ---------------------------------------------------------------------- copies
         const uint32_t issue = elect_lane();
-        const uint64_t pol_w = policy_evict_first(), pol_t = policy_evict_last();
+        // weights that another tile of the group reads too stay in L2, others pass through it
+        const uint64_t pol_t = policy_evict_last(), pol_once = policy_evict_first();
         const uint32_t sw0 = smem_addr(sW), st0 = smem_addr(sT), full0 = smem_addr(full);
         const uint32_t sf_off = static_cast<uint32_t>(p.m_tile) * 128u;
         // the weights of the first stages go out before the wait on the token-block writer
         int early = 0;
         {
-            Schedule d = plan;
-            Share f;
-            while (early < p.stages && next_share(d, f)) {
-                const Unit u = locate(p, prefix, f.unit);
+            Walk u = start;
+            while (early < p.stages && next_share(p, prefix, u)) {
+                const uint64_t pol_w = u.tiles > 1 ? pol_t : pol_once;
                 const uint8_t* w = p.wblk + static_cast<size_t>(u.group) * p.group_bytes +
-                                   (static_cast<size_t>(u.nt) * p.k_atoms + f.k0) * kWBlock;
+                                   (static_cast<size_t>(u.nt) * p.k_atoms + u.k0) * kWBlock;
                 const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15);
                 const uint32_t tok = n16 * 128u + (n16 > 128u ? 4u : 2u) * kSfChunk;
-                for (int j = 0; j < f.nk && early < p.stages; ++j, ++early, w += kWBlock) {
+                for (int j = 0; j < u.nk && early < p.stages; ++j, ++early, w += kWBlock) {
                     const uint32_t bar = full0 + static_cast<uint32_t>(early) * 8u;
                     mbar_expect_if(issue, bar, kWBlock + tok);
                     bulk_load_if(issue, sw0 + static_cast<uint32_t>(early) * kWBlock, w, kWBlock, bar, pol_w);
@@ -474,19 +571,18 @@ mxfp4_stream_kernel(const StreamArgs p) {
             }
         }
         pdl_wait_prior_grid();
-        Schedule d = plan;
-        Share f;
+        Walk u = start;
         int s = 0, issued = 0;
         uint32_t phase = 0;
         bool ok = true;
-        while (ok && next_share(d, f)) {
-            const Unit u = locate(p, prefix, f.unit);
+        while (ok && next_share(p, prefix, u)) {
+            const uint64_t pol_w = u.tiles > 1 ? pol_t : pol_once;
             const uint8_t* w = p.wblk + static_cast<size_t>(u.group) * p.group_bytes +
-                               (static_cast<size_t>(u.nt) * p.k_atoms + f.k0) * kWBlock;
-            const uint8_t* t = p.tblk + (static_cast<size_t>(u.slot) * p.k_atoms + f.k0) * p.a_block;
+                               (static_cast<size_t>(u.nt) * p.k_atoms + u.k0) * kWBlock;
+            const uint8_t* t = p.tblk + (static_cast<size_t>(u.slot) * p.k_atoms + u.k0) * p.a_block;
             const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15);
             const uint32_t tok_rows = n16 * 128u, tok_sf = (n16 > 128u ? 4u : 2u) * kSfChunk;
-            for (int j = 0; j < f.nk; ++j) {
+            for (int j = 0; j < u.nk; ++j) {
                 if (issued >= p.stages && !mbar_wait(&empty[s], phase ^ 1u, lim)) {
                     stream_fail(p, abort_flag);
                     ok = false;
@@ -534,8 +630,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
             const uint64_t sfw_desc0 = desc_sf(smem_addr(sW + kBRowsBytes));
             const uint64_t sft_desc0 = desc_sf(smem_addr(sT + p.m_tile * 128));
             const uint32_t w_step = kWBlock >> 4, t_step = p.a_block >> 4, chunk = kSfChunk >> 4;
-            Schedule d = plan;
-            Share f;
+            Walk u = start;
             int s = 0, nshare = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -553,8 +648,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
                     tc_copy_sf_if(issue, sft + 12u, std_ + 3 * chunk);
                 }
             };
-            while (ok && next_share(d, f)) {
-                const Unit u = locate(p, prefix, f.unit);
+            while (ok && next_share(p, prefix, u)) {
                 const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15);
                 const uint32_t idesc0 = idesc_mxf4(n16), idesc1 = idesc0 | (2u << 29) | (2u << 4);
                 const int b = nshare & 1;
@@ -564,7 +658,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
                     break;
                 }
                 tc_fence_after_sync();
-                for (int j = 0; j < f.nk; ++j) {
+                for (int j = 0; j < u.nk; ++j) {
                     if (!mbar_wait(&full[s], phase, lim)) {
                         stream_fail(p, abort_flag);
                         ok = false;
@@ -604,12 +698,10 @@ mxfp4_stream_kernel(const StreamArgs p) {
         const int nl = (warp & 3) * 32 + lane;       // weight row within the tile
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         constexpr int kTok = 16 / kTermsPer;         // tokens per 16 columns
-        const int tile_tokens = p.m_tile / kTermsPer;
-        Schedule d = plan;
-        Share f;
+        const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;
+        Walk u = start;
         int nshare = 0;
-        while (next_share(d, f)) {
-            const Unit u = locate(p, prefix, f.unit);
+        while (next_share(p, prefix, u)) {
             const int b = nshare & 1;
             const bool got = mbar_wait(&acc_full[b], (nshare >> 1) & 1, lim);
             if (!got) stream_fail(p, abort_flag);
@@ -619,58 +711,76 @@ mxfp4_stream_kernel(const StreamArgs p) {
             const int n = u.nt * kTileN + nl;
             const int tokens = u.rows / kTermsPer;   // exact: rows are kTermsPer per token
             const int64_t row0 = u.row0 / kTermsPer;
-            bool last = f.split < 0;
-            int64_t c_first = 0, c_last = 0;
-            if (f.split >= 0) {
-                // this CTA's sums of the unit into its slot of the workspace: slot 0 for the unit
-                // its run begins in, slot 1 for one it reaches later
-                float* mine = p.partial + (static_cast<size_t>(d.cta) * 2 + (f.k0 == 0 && d.s - f.nk != d.share * d.cta ? 1 : 0)) *
-                                              (static_cast<size_t>(tile_tokens) * kTileN);
-                for (int cb = half * 16; cb < u.rows; cb += 32) {
-                    float v[kTok];
-                    load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
-                    const int m0 = cb / kTermsPer;
-#pragma unroll
-                    for (int i = 0; i < kTok; ++i)
-                        if (m0 + i < tokens) __stcg(mine + static_cast<size_t>(m0 + i) * kTileN + nl, v[i]);
-                }
-                // contributors: the CTAs whose runs meet the unit's steps
-                const int64_t first = static_cast<int64_t>(f.split) * d.k_atoms;
-                c_first = first / d.share;
-                c_last = (first + d.k_atoms - 1) / d.share;
-                __threadfence();
-                named_barrier(2, kStreamEpiThreads);
-                if (threadIdx.x == 128)
-                    *last_flag = atomicAdd(&p.counters[f.split], 1u) == static_cast<uint32_t>(c_last - c_first) ? 1u : 0u;
-                named_barrier(2, kStreamEpiThreads);
-                last = *last_flag != 0u;
-                __threadfence();
-            }
-            if (last) {
-                for (int cb = half * 16; cb < u.rows; cb += 32) {
-                    float v[kTok];
-                    const int m0 = cb / kTermsPer;
-                    if (f.split < 0) {
-                        load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < kTok; ++i) v[i] = 0.f;
-                        for (int64_t c = c_first; c <= c_last; ++c) {
-                            // the unit is the first of c's run unless the run began before it
-                            const int slot = c * d.share < static_cast<int64_t>(f.split) * d.k_atoms ? 1 : 0;
-                            const float* src = p.partial + (static_cast<size_t>(c) * 2 + slot) *
-                                                               (static_cast<size_t>(tile_tokens) * kTileN);
+            if (kTermsPer == 1 && u.split < 0) {
+                store_tile(p, acc, u.rows, u.row0, u.nt * kTileN + (warp & 3) * 32, half, lane,
+                           epi_stage + (warp - 4) * kEpiStage);
+            } else {
+                // A unit of several CTAs: each but the last to arrive leaves its sums in its slot of
+                // the workspace (slot 0 for the unit its run begins in, slot 1 for one it reaches
+                // later); the last adds all of them in the order of K, its own from tensor memory.
+                bool last = true;
+                int64_t c_first = 0, c_last = 0;
+                const int64_t unit_step = static_cast<int64_t>(u.split) * p.k_atoms;
+                if (u.split >= 0) {
+                    c_first = unit_step / u.share;
+                    c_last = (unit_step + p.k_atoms - 1) / u.share;
+                    const uint32_t others = static_cast<uint32_t>(c_last - c_first);
+                    const int slot = u.k0 == 0 && u.s - u.nk != u.share * static_cast<int64_t>(blockIdx.x) ? 1 : 0;
+                    volatile uint32_t* flag = last_flag + 2 * slot;
+                    uint32_t* counter = p.counters + c_first;   // a split unit is named by its first CTA
+                    if (threadIdx.x == 128) flag[0] = *reinterpret_cast<volatile uint32_t*>(counter) == others ? 1u : 0u;
+                    named_barrier(2, kStreamEpiThreads);
+                    last = flag[0] != 0u;
+                    if (!last) {
+                        float* mine = p.partial + (static_cast<size_t>(blockIdx.x) * 2 + slot) * slot_floats;
+                        for (int cb = half * 16; cb < u.rows; cb += 32) {
+                            float v[kTok];
+                            load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
+                            const int m0 = cb / kTermsPer;
 #pragma unroll
                             for (int i = 0; i < kTok; ++i)
-                                if (m0 + i < tokens) v[i] += __ldcg(src + static_cast<size_t>(m0 + i) * kTileN + nl);
+                                if (m0 + i < tokens) __stcg(mine + static_cast<size_t>(m0 + i) * kTileN + nl, v[i]);
                         }
+                        __threadfence();
+                        named_barrier(2, kStreamEpiThreads);
+                        if (threadIdx.x == 128) flag[1] = atomicAdd(counter, 1u) == others ? 1u : 0u;
+                        named_barrier(2, kStreamEpiThreads);
+                        last = flag[1] != 0u;
                     }
-                    if (n < p.N) {
-                        uint16_t* cp = p.c + (row0 + m0) * p.ldc + n;
+                    __threadfence();
+                }
+                if (last) {
+                    for (int cb = half * 16; cb < u.rows; cb += 32) {
+                        float own[kTok], v[kTok];
+                        const int m0 = cb / kTermsPer;
+                        load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), own);
+                        if (u.split < 0) {
 #pragma unroll
-                        for (int i = 0; i < kTok; ++i) {
-                            if (m0 + i < tokens) *cp = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
-                            cp += p.ldc;
+                            for (int i = 0; i < kTok; ++i) v[i] = own[i];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < kTok; ++i) v[i] = 0.f;
+                            for (int64_t c = c_first; c <= c_last; ++c) {
+                                // the unit is the first of c's run unless the run began before it
+                                const float* src = p.partial + (static_cast<size_t>(c) * 2 + (c * u.share < unit_step ? 1 : 0)) *
+                                                                   slot_floats;
+                                float theirs[kTok];
+                                if (c != static_cast<int64_t>(blockIdx.x)) {   // all loads in flight before the first is added
+#pragma unroll
+                                    for (int i = 0; i < kTok; ++i)
+                                        theirs[i] = m0 + i < tokens ? __ldcg(src + static_cast<size_t>(m0 + i) * kTileN + nl) : 0.f;
+                                }
+#pragma unroll
+                                for (int i = 0; i < kTok; ++i) v[i] += c == static_cast<int64_t>(blockIdx.x) ? own[i] : theirs[i];
+                            }
+                        }
+                        if (n < p.N) {
+                            uint16_t* cp = p.c + (row0 + m0) * p.ldc + n;
+#pragma unroll
+                            for (int i = 0; i < kTok; ++i) {
+                                if (m0 + i < tokens) *cp = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+                                cp += p.ldc;
+                            }
                         }
                     }
                 }
@@ -699,12 +809,21 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
         p.m_tile = static_cast<int>(rows < 128 ? (rows + 15) / 16 * 16 : 128);
     } else {
         const int64_t mean = (rows + groups - 1) / groups;
+        
         p.m_tile = mean <= 48 ? 64 : mean <= 256 ? 128 : 192;
+        // Groups of several tiles with short K: no waves, every CTA takes the tiles of a weight tile
+        // one after the other and rereads its weights from L2, where all CTAs' fit (152 x 12 steps
+        // are 32 MB; 6000 rows in 48 groups x 2880 x 2040 53.7 -> 50.0 us, but 16384 rows in 16 groups
+        // x 4096 x 7168, 28 steps, 240 -> 428). In waves the CTAs of a group read a weight at the
+        // same time, once from memory, but then wait for the same few weights together.
+        p.runs = mean > 48 && p.k_atoms <= 12;
+
     }
     p.min_steps = 4;
     p.nmc = (p.m_tile + 127) / 128;
     p.a_block = static_cast<uint32_t>(p.m_tile) * 128u + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
-    const size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 16 + 64 + (static_cast<size_t>(groups) + 1) * 4;
+    const size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 + 8 * kEpiStage +
+                         (static_cast<size_t>(groups) + 1) * 4;
     p.stages = static_cast<int>((kSmemLimit - extra) / (kWBlock + p.a_block));
     if (p.stages > kStreamMaxStages) p.stages = kStreamMaxStages;
     p.smem_bytes = static_cast<size_t>(p.stages) * (kWBlock + p.a_block) + extra;
@@ -727,13 +846,16 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
 cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,
                                    const int32_t* offsets, int groups, int rows, bool gated, const StreamPlan& plan,
                                    uint8_t* blocks, uint32_t* counters, cudaStream_t s) {
-    const int wpr = (plan.k_atoms * 8 + 31) / 32;
-    const int64_t warps = static_cast<int64_t>(rows) * wpr;
-    int64_t grid = (warps + 7) / 8;
+    // as many parts of a row as make enough warps for every SM, whole rows beyond that
+    const int chunks = (plan.k_atoms * 8 + 31) / 32;
+    const int64_t want = (int64_t(4096) + rows - 1) / rows;
+    const int per = static_cast<int>(want >= chunks ? 1 : chunks / want);
+    const int parts = (chunks + per - 1) / per;
+    int64_t grid = (static_cast<int64_t>(rows) * parts + 7) / 8;
     if (grid > 65535) grid = 65535;
-    return launch_pdl(gated ? quantize_groups_kernel<true> : quantize_groups_kernel<false>, dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, tokens, K, lda, index,
-                      offsets, groups, rows, plan.m_tile, plan.k_atoms, plan.a_block, blocks, counters, plan.ctas + 1,
-                      wpr);
+    return launch_pdl(gated ? quantize_groups_kernel<true> : quantize_groups_kernel<false>,
+                      dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, tokens, K, lda, index, offsets, groups, rows,
+                      plan.m_tile, plan.k_atoms, plan.a_block, blocks, counters, plan.ctas + 1, parts, per * 32);
 }
 
 cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx, const StreamPlan& plan,

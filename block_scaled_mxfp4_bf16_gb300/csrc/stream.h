@@ -9,6 +9,7 @@ constexpr int kMaxGroups = 1024;          // groups (experts) one launch can add
 constexpr int kStreamThreads = 384;       // warps 0-3: copies, MMAs, two spare; warps 4-11: epilogue
 constexpr int kStreamEpiThreads = 256;
 constexpr int kStreamMaxStages = 10;
+constexpr int kEpiStage = 640;            // bytes of shared memory an epilogue warp transposes through
 constexpr int kTerms = 8;                 // e2m1 terms an activation is expanded into (weight-only)
 
 // A group of n rows is cut into tiles_of(n) token tiles of tile_rows(n) rows (a multiple of 16,
@@ -39,14 +40,16 @@ struct StreamArgs {
     uint32_t* status;
     int groups, rows, N;      // rows: token-block rows (grouped) or tokens * terms (weight-only)
     int m_tile, nmc, n_tiles, k_atoms, stages;
+    int runs;                 // no waves of whole units (make_stream_plan)
     int min_steps;            // fewest 256-K steps a split unit's share has
     uint32_t a_block;
     uint32_t tmem_cols;
+    int c_vec;                // C's rows are 16-byte aligned
     uint64_t wait_limit_ns;
 };
 
 struct StreamPlan {
-    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, min_steps;
+    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, min_steps, runs;
     uint32_t a_block, tmem_cols;
     size_t smem_bytes;
     size_t off_counters, off_partial, ws_total;   // workspace: token blocks at 0
@@ -76,7 +79,7 @@ struct RouteArgs {
     int chunk;                // tokens per CTA
     int chunks;
 };
-int route_chunk(int64_t T);
+int route_chunk(int64_t T, int sm_count);
 cudaError_t launch_route(const RouteArgs& args, cudaStream_t s);
 cudaError_t launch_combine(const uint16_t* y, int64_t rows, int64_t ldy, const int32_t* slots, const float* weights,
                            int64_t T, int k, int64_t N, uint16_t* out, int64_t ldo, cudaStream_t s);

@@ -36,8 +36,18 @@ def _scratch(workspace, need: int, device: torch.device, stream, st: int) -> tup
     return workspace.data_ptr(), workspace.nbytes
 
 
+def _dense_rows(t: torch.Tensor) -> bool:
+    """Whether the columns lie next to each other (strides of 0 or 1 element say nothing)."""
+    return t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1 or t.shape[0] == 0)
+
+
+def _ld(t: torch.Tensor) -> int:
+    """Row stride of a 2-D tensor; a single row has none that matters."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
 def _bf16_rows(t: torch.Tensor, name: str) -> None:
-    if t.dtype != torch.bfloat16 or t.dim() != 2 or t.stride(1) != 1:
+    if t.dtype != torch.bfloat16 or not _dense_rows(t):
         raise ValueError(f"{name} must be a 2-D bf16 tensor with unit column stride")
 
 
@@ -55,7 +65,7 @@ def _out(t: torch.Tensor | None, shape: tuple, device: torch.device, name: str, 
     if t is None:
         return _empty(shape, torch.bfloat16, device, stream)
     _on(t, device, name)
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or t.stride(1) != 1:
+    if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not _dense_rows(t):
         raise ValueError(f"{name} must be a bf16 {list(shape)} tensor with unit column stride")
     return t
 
@@ -80,7 +90,7 @@ def mxfp4_gemv(x: torch.Tensor, packed_b: torch.Tensor, N: int, y: torch.Tensor 
     st = _stream(stream)
     need = _need("mxfp4_gemv_workspace_size", device, M, N, K) if M and N else 0
     ws, ws_bytes = _scratch(workspace, need, device, stream, st)
-    _check(L.mxfp4_gemv(x.data_ptr(), M, K, x.stride(0), packed_b.data_ptr(), N, y.data_ptr(), y.stride(0), ws, ws_bytes,
+    _check(L.mxfp4_gemv(x.data_ptr(), M, K, _ld(x), packed_b.data_ptr(), N, y.data_ptr(), _ld(y), ws, ws_bytes,
                         st), "mxfp4_gemv")
     return y
 
@@ -139,8 +149,8 @@ def mxfp4_grouped_gemm(a: torch.Tensor, packed_b: torch.Tensor, offsets: torch.T
     st = _stream(stream)
     need = _need("mxfp4_grouped_gemm_workspace_size", device, R, E, N, K) if R and E and N else 0
     ws, ws_bytes = _scratch(workspace, need, device, stream, st)
-    _check(L.mxfp4_grouped_gemm(a.data_ptr(), tokens, K, a.stride(0), rows_ptr, offsets.data_ptr(), E,
-                                packed_b.data_ptr(), N, c.data_ptr(), R, c.stride(0), 1 if gated else 0, ws, ws_bytes, st),
+    _check(L.mxfp4_grouped_gemm(a.data_ptr(), tokens, K, _ld(a), rows_ptr, offsets.data_ptr(), E,
+                                packed_b.data_ptr(), N, c.data_ptr(), R, _ld(c), 1 if gated else 0, ws, ws_bytes, st),
            "mxfp4_grouped_gemm")
     return c
 
@@ -167,7 +177,7 @@ def mxfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, work
     L = load_library()
     _dev(logits, "logits")
     dtype = _LOGIT_TYPES.get(logits.dtype)
-    if dtype is None or logits.dim() != 2 or logits.stride(1) != 1:
+    if dtype is None or not _dense_rows(logits):
         raise ValueError("logits must be a 2-D fp32 or bf16 tensor with unit column stride")
     T, E = logits.shape
     if not 1 <= k <= min(E, 32):
@@ -180,7 +190,7 @@ def mxfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, work
     slots = _empty((T, k), torch.int32, device, stream)
     st = _stream(stream)
     ws, ws_bytes = _scratch(workspace, _need("mxfp4_moe_route_workspace_size", device, T, E), device, stream, st)
-    _check(L.mxfp4_moe_route(logits.data_ptr(), dtype, T, E, logits.stride(0), k, 0 if renormalize else 1,
+    _check(L.mxfp4_moe_route(logits.data_ptr(), dtype, T, E, _ld(logits), k, 0 if renormalize else 1,
                              weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
                              slots.data_ptr(), ws, ws_bytes, st), "mxfp4_moe_route")
     return MoeRouting(weights, experts, offsets, rows, slots)
@@ -200,6 +210,6 @@ def mxfp4_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
     _index(slots, (T, k), y.device, "slots")
     _index(weights, (T, k), y.device, "weights", torch.float32)
     out = _out(out, (T, N), y.device, "out", stream)
-    _check(L.mxfp4_moe_combine(y.data_ptr(), R, N, y.stride(0), slots.data_ptr(), weights.data_ptr(), T, k,
-                               out.data_ptr(), out.stride(0), _stream(stream)), "mxfp4_moe_combine")
+    _check(L.mxfp4_moe_combine(y.data_ptr(), R, N, _ld(y), slots.data_ptr(), weights.data_ptr(), T, k,
+                               out.data_ptr(), _ld(out), _stream(stream)), "mxfp4_moe_combine")
     return out
