@@ -1,97 +1,123 @@
 """The mixture-of-experts and weight-only operators of the binding: mxfp4_gemv, mxfp4_grouped_gemm,
 mxfp4_moe_route and mxfp4_moe_combine. As in the rest of the binding, the functions only check and
-marshal arguments; every step runs in the library's CUDA kernels."""
+marshal arguments; every step runs in the library's CUDA kernels.
+
+These calls sit between short kernels in a decoding loop, where the host's time is the loop's time,
+so each reads a tensor property once and leaves the reports of what is wrong to slower helpers."""
 from __future__ import annotations
 
 from typing import NamedTuple
 
 import torch
 
-from . import (Mxfp4Error, _check, _check_packed, _dev, _on, _stream, _workspace, load_library, mxfp4_prepack_b,
-               mxfp4_prepack_b_size)
+from . import (_WS, Mxfp4Error, _check, _check_packed, _dev, _on, _raw_stream, _stream, _workspace, load_library,
+               mxfp4_prepack_b, mxfp4_prepack_b_size)
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _NEED: dict = {}
 
 
-def _need(query: str, device: torch.device, *sizes: int) -> int:
-    """A workspace query, remembered per (device, sizes): it depends only on those."""
-    key = (query, device.index, *sizes)
+def _need(query: str, *sizes: int) -> int:
+    """A size query of the library, remembered per argument list and current device: it depends only on those."""
+    key = (query, *sizes, torch.cuda.current_device())
     need = _NEED.get(key)
     if need is None:
         need = getattr(load_library(), query)(*sizes)
-        _NEED[key] = need
+        if need:
+            _NEED[key] = need
     return need
 
 
-def _scratch(workspace, need: int, device: torch.device, stream, st: int) -> tuple:
+def _begin(t: torch.Tensor, name: str, stream) -> int:
+    """The stream of a call whose first operand is `t`, which must live on the current CUDA device."""
+    d = t.get_device()
+    if d < 0 or d != torch.cuda.current_device():
+        _dev(t, name)
+    return _raw_stream(d) if stream is None and _raw_stream is not None else _stream(stream)
+
+
+def _scratch(workspace, need: int, t: torch.Tensor, stream, st: int) -> tuple:
     """(pointer, bytes) of the caller's workspace, or of the binding's own for this stream."""
-    if workspace is None:
-        workspace = _workspace(device, need, stream, st)
-        if workspace is None:
-            return None, 0
-    else:
-        _on(workspace, device, "workspace")
+    if workspace is not None:
+        _on(workspace, t.device, "workspace")
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
+    elif need == 0:
+        return None, 0
+    else:
+        workspace = _WS.get((t.get_device(), st))
+        if workspace is None or workspace.nbytes < need:
+            workspace = _workspace(t.device, need, stream, st)
     return workspace.data_ptr(), workspace.nbytes
 
 
-def _dense_rows(t: torch.Tensor) -> bool:
-    """Whether the columns lie next to each other (strides of 0 or 1 element say nothing)."""
-    return t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1 or t.shape[0] == 0)
+def _rows_of(t: torch.Tensor, name: str) -> int:
+    """The row stride of a 2-D tensor whose columns lie next to each other (a single row has none
+    that matters)."""
+    if t.dim() == 2:
+        rows, cols = t.shape
+        ld, step = t.stride()
+        if step == 1 or cols <= 1 or rows == 0:
+            return ld if rows > 1 else cols
+    raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
 
 
-def _ld(t: torch.Tensor) -> int:
-    """Row stride of a 2-D tensor; a single row has none that matters."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _bf16_rows(t: torch.Tensor, name: str) -> int:
+    if t.dtype != _BF16:
+        raise ValueError(f"{name} must be a bf16 tensor")
+    return _rows_of(t, name)
 
 
-def _bf16_rows(t: torch.Tensor, name: str) -> None:
-    if t.dtype != torch.bfloat16 or not _dense_rows(t):
-        raise ValueError(f"{name} must be a 2-D bf16 tensor with unit column stride")
+# the allocation that compiled graphs use: 0.6 us a tensor less than torch.empty
+_empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
-def _empty(shape: tuple, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
-    """An output of the call: its memory belongs to the stream that writes it."""
+def _empty(shape: tuple, dtype: torch.dtype, t: torch.Tensor, stream) -> torch.Tensor:
+    """An output of a call, on t's (the current) device: its memory belongs to the stream that writes it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        if _empty_strided is not None and t.get_device() >= 0:
+            return _empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
+        return torch.empty(shape, dtype=dtype, device=t.device)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=t.device)
 
 
-def _out(t: torch.Tensor | None, shape: tuple, device: torch.device, name: str, stream) -> torch.Tensor:
-    if t is None:
-        return _empty(shape, torch.bfloat16, device, stream)
-    _on(t, device, name)
-    if t.dtype != torch.bfloat16 or tuple(t.shape) != shape or not _dense_rows(t):
-        raise ValueError(f"{name} must be a bf16 {list(shape)} tensor with unit column stride")
-    return t
+def _out(out: torch.Tensor | None, shape: tuple, t: torch.Tensor, name: str, stream) -> tuple:
+    """(output, its row stride): the caller's, checked, or a new one."""
+    if out is None:
+        return _empty(shape, _BF16, t, stream), shape[1]
+    _on(out, t.device, name)
+    if tuple(out.shape) != shape:
+        raise ValueError(f"{name} must be a {list(shape)} tensor")
+    return out, _bf16_rows(out, name)
 
 
-def _index(t: torch.Tensor, shape: tuple, device: torch.device, name: str, dtype=torch.int32) -> None:
-    if t.device != device or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {device}")
+def _index(t: torch.Tensor, shape: tuple, like: torch.Tensor, name: str, dtype=_I32) -> int:
+    """Pointer of a dense index (or weight) tensor on the operands' device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {like.device}")
+    return t.data_ptr()
 
 
 def mxfp4_gemv(x: torch.Tensor, packed_b: torch.Tensor, N: int, y: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [M, N] bf16 = x . W^T for a few tokens, x [M, K] kept in bf16 (not quantized), W the MXFP4
     weights of `packed_b` (mxfp4_prepack_b): the weight-only product, on the weights mxfp4_gemm uses."""
-    L = load_library()
-    _dev(x, "x")
-    _bf16_rows(x, "x")
+    st = _begin(x, "x", stream)
+    ldx = _bf16_rows(x, "x")
     M, K = x.shape
-    device = x.device
+    need = 0
     if M and N:
-        _check_packed(packed_b, N, K, device)
-    y = _out(y, (M, N), device, "y", stream)
-    st = _stream(stream)
-    need = _need("mxfp4_gemv_workspace_size", device, M, N, K) if M and N else 0
-    ws, ws_bytes = _scratch(workspace, need, device, stream, st)
-    _check(L.mxfp4_gemv(x.data_ptr(), M, K, _ld(x), packed_b.data_ptr(), N, y.data_ptr(), _ld(y), ws, ws_bytes,
-                        st), "mxfp4_gemv")
+        _check_packed(packed_b, N, K, x.device)
+        need = _need("mxfp4_gemv_workspace_size", M, N, K)
+    y, ldy = _out(y, (M, N), x, "y", stream)
+    ws, ws_bytes = _scratch(workspace, need, x, stream, st)
+    status = load_library().mxfp4_gemv(x.data_ptr(), M, K, ldx, packed_b.data_ptr(), N, y.data_ptr(), ldy, ws, ws_bytes,
+                                       st)
+    if status:
+        _check(status, "mxfp4_gemv")
     return y
 
 
@@ -122,36 +148,34 @@ def mxfp4_grouped_gemm(a: torch.Tensor, packed_b: torch.Tensor, offsets: torch.T
     [E+1] and `rows` [R]: int32 on the device, as mxfp4_moe_route returns them (rows None: row r of
     `a`). gated: a's rows are [g, u] and silu(g) * u is the product's input, K = a.shape[1] / 2.
     Rows of C that belong to no expert are not written."""
-    L = load_library()
-    _dev(a, "a")
-    _bf16_rows(a, "a")
+    st = _begin(a, "a", stream)
+    lda = _bf16_rows(a, "a")
     tokens, K = a.shape
     if gated:
         if K % 2:
             raise ValueError("a gated product's a must have an even number of columns")
         K //= 2
-    device = a.device
     if packed_b.dim() != 2 or not packed_b.is_contiguous():
         raise ValueError("packed_b must be a contiguous [E, bytes] buffer (mxfp4_prepack_experts)")
     E = packed_b.shape[0]
     if E and N:
-        _check_packed(packed_b[0] if E > 1 else packed_b, N, K, device)
-        if packed_b.shape[1] * packed_b.element_size() != mxfp4_prepack_b_size(N, K):
+        _check_packed(packed_b, N, K, a.device)
+        if packed_b.nbytes != E * _need("mxfp4_prepack_b_size", N, K):
             raise ValueError(f"packed_b's rows must have mxfp4_prepack_b_size({N}, {K}) bytes")
-    _index(offsets, (E + 1,), device, "offsets")
+    offsets_ptr = _index(offsets, (E + 1,), a, "offsets")
     if rows is None:
         R, rows_ptr = tokens, None
     else:
         R = rows.shape[0] if rows.dim() == 1 else -1
-        _index(rows, (R,), device, "rows")
-        rows_ptr = rows.data_ptr()
-    c = _out(c, (R, N), device, "c", stream)
-    st = _stream(stream)
-    need = _need("mxfp4_grouped_gemm_workspace_size", device, R, E, N, K) if R and E and N else 0
-    ws, ws_bytes = _scratch(workspace, need, device, stream, st)
-    _check(L.mxfp4_grouped_gemm(a.data_ptr(), tokens, K, _ld(a), rows_ptr, offsets.data_ptr(), E,
-                                packed_b.data_ptr(), N, c.data_ptr(), R, _ld(c), 1 if gated else 0, ws, ws_bytes, st),
-           "mxfp4_grouped_gemm")
+        rows_ptr = _index(rows, (R,), a, "rows")
+    c, ldc = _out(c, (R, N), a, "c", stream)
+    need = _need("mxfp4_grouped_gemm_workspace_size", R, E, N, K) if R and E and N else 0
+    ws, ws_bytes = _scratch(workspace, need, a, stream, st)
+    status = load_library().mxfp4_grouped_gemm(a.data_ptr(), tokens, K, lda, rows_ptr, offsets_ptr, E,
+                                               packed_b.data_ptr(), N, c.data_ptr(), R, ldc, 1 if gated else 0, ws,
+                                               ws_bytes, st)
+    if status:
+        _check(status, "mxfp4_grouped_gemm")
     return c
 
 
@@ -174,25 +198,25 @@ def mxfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, work
     """Top-k routing of logits [T, E] (fp32 or bf16): the k largest per token (ties to the lower index;
     -inf and NaN are masks), their softmax weights (over the k, or with renormalize=False over all
     experts), and the token-expert pairs grouped by expert."""
-    L = load_library()
-    _dev(logits, "logits")
+    st = _begin(logits, "logits", stream)
     dtype = _LOGIT_TYPES.get(logits.dtype)
-    if dtype is None or not _dense_rows(logits):
-        raise ValueError("logits must be a 2-D fp32 or bf16 tensor with unit column stride")
+    if dtype is None:
+        raise ValueError("logits must be an fp32 or bf16 tensor")
+    ld = _rows_of(logits, "logits")
     T, E = logits.shape
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must lie in 1 .. min(E, 32) = {min(E, 32)}")
-    device = logits.device
-    weights = _empty((T, k), torch.float32, device, stream)
-    experts = _empty((T, k), torch.int32, device, stream)
-    offsets = _empty((E + 1,), torch.int32, device, stream)
-    rows = _empty((T * k,), torch.int32, device, stream)
-    slots = _empty((T, k), torch.int32, device, stream)
-    st = _stream(stream)
-    ws, ws_bytes = _scratch(workspace, _need("mxfp4_moe_route_workspace_size", device, T, E), device, stream, st)
-    _check(L.mxfp4_moe_route(logits.data_ptr(), dtype, T, E, _ld(logits), k, 0 if renormalize else 1,
-                             weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(), rows.data_ptr(),
-                             slots.data_ptr(), ws, ws_bytes, st), "mxfp4_moe_route")
+    weights = _empty((T, k), _F32, logits, stream)
+    experts = _empty((T, k), _I32, logits, stream)
+    offsets = _empty((E + 1,), _I32, logits, stream)
+    rows = _empty((T * k,), _I32, logits, stream)
+    slots = _empty((T, k), _I32, logits, stream)
+    ws, ws_bytes = _scratch(workspace, _need("mxfp4_moe_route_workspace_size", T, E), logits, stream, st)
+    status = load_library().mxfp4_moe_route(logits.data_ptr(), dtype, T, E, ld, k, 0 if renormalize else 1,
+                                            weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(),
+                                            rows.data_ptr(), slots.data_ptr(), ws, ws_bytes, st)
+    if status:
+        _check(status, "mxfp4_moe_route")
     return MoeRouting(weights, experts, offsets, rows, slots)
 
 
@@ -200,16 +224,17 @@ def mxfp4_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
                       stream=None) -> torch.Tensor:
     """out [T, N] bf16 = sum over j of weights[t, j] * y[slots[t, j]] (fp32 sums), y [R, N] bf16 in the
     grouped order; a slot outside [0, R) adds nothing."""
-    L = load_library()
-    _dev(y, "y")
-    _bf16_rows(y, "y")
+    st = _begin(y, "y", stream)
+    ldy = _bf16_rows(y, "y")
     R, N = y.shape
     if slots.dim() != 2:
         raise ValueError("slots must be [T, k]")
     T, k = slots.shape
-    _index(slots, (T, k), y.device, "slots")
-    _index(weights, (T, k), y.device, "weights", torch.float32)
-    out = _out(out, (T, N), y.device, "out", stream)
-    _check(L.mxfp4_moe_combine(y.data_ptr(), R, N, _ld(y), slots.data_ptr(), weights.data_ptr(), T, k,
-                               out.data_ptr(), _ld(out), _stream(stream)), "mxfp4_moe_combine")
+    slots_ptr = _index(slots, (T, k), y, "slots")
+    weights_ptr = _index(weights, (T, k), y, "weights", _F32)
+    out, ldo = _out(out, (T, N), y, "out", stream)
+    status = load_library().mxfp4_moe_combine(y.data_ptr(), R, N, ldy, slots_ptr, weights_ptr, T, k, out.data_ptr(), ldo,
+                                              st)
+    if status:
+        _check(status, "mxfp4_moe_combine")
     return out
