@@ -27,21 +27,24 @@ int stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, D
     return make_stream_plan(rows, groups, N, K, terms, di->sm_count, plan) == 0 ? MXFP4_OK : MXFP4_ERR_SHAPE;
 }
 
-int run_stream(const StreamPlan& plan, const DeviceInfo& di, uint8_t* ws, const void* packed_b, size_t group_bytes,
-               const int32_t* offsets, int groups, int rows, int64_t N, void* c, int64_t ldc, int terms, cudaStream_t s) {
+// The operands of a stream product, and the launch.
+StreamArgs stream_args(const void* packed_b, int64_t N, int64_t K, void* c, int64_t ldc) {
     StreamArgs a = {};
-    a.tblk = ws;
     a.wblk = static_cast<const uint8_t*>(packed_b);
-    a.group_bytes = group_bytes;
-    a.offsets = offsets;
     a.c = static_cast<uint16_t*>(c);
     a.ldc = ldc;
-    a.partial = reinterpret_cast<float*>(ws + plan.off_partial);
-    a.counters = reinterpret_cast<uint32_t*>(ws + plan.off_counters);
-    a.status = di.status;
-    a.groups = groups;
-    a.rows = rows;
     a.N = static_cast<int>(N);
+    a.K = K;
+    a.c_vec = aligned(c, 16) && ldc % 8 == 0 ? 1 : 0;
+    return a;
+}
+
+int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8_t* ws, int terms, cudaStream_t s) {
+    a.tblk = ws;
+    a.partial = reinterpret_cast<float*>(ws + plan.off_partial);
+    a.counters = reinterpret_cast<unsigned long long*>(ws + plan.off_counters);
+    a.tag = next_call_tag();
+    a.status = di.status;
     a.m_tile = plan.m_tile;
     a.nmc = plan.nmc;
     a.n_tiles = plan.n_tiles;
@@ -51,7 +54,6 @@ int run_stream(const StreamPlan& plan, const DeviceInfo& di, uint8_t* ws, const 
     a.runs = plan.runs;
     a.a_block = plan.a_block;
     a.tmem_cols = plan.tmem_cols;
-    a.c_vec = aligned(c, 16) && ldc % 8 == 0 ? 1 : 0;
     a.wait_limit_ns = wait_limit_ns();
     const cudaError_t e = launch_stream(plan, a, terms, s);
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
@@ -84,10 +86,17 @@ int mxfp4_gemv(const void* x, int64_t M, int64_t K, int64_t ldx, const void* pac
     if (!aligned(workspace, 256)) return MXFP4_ERR_ALIGN;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_expand_terms(static_cast<const uint16_t*>(x), static_cast<int>(M), K, ldx, plan, ws,
-                                              reinterpret_cast<uint32_t*>(ws + plan.off_counters), s);
-    if (e != cudaSuccess) return cuda_fail(e);
-    return run_stream(plan, di, ws, packed_b, 0, nullptr, 1, static_cast<int>(M) * kTerms, N, y, ldy, kTerms, s);
+    StreamArgs a = stream_args(packed_b, N, K, y, ldy);
+    a.groups = 1;
+    a.rows = static_cast<int>(M) * kTerms;
+    a.a = static_cast<const uint16_t*>(x);
+    a.lda = ldx;
+    a.tokens = M;
+    if (!plan.fused) {
+        const cudaError_t e = launch_expand_terms(a.a, static_cast<int>(M), K, ldx, plan, ws, s);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return run_stream(plan, di, a, ws, kTerms, s);
 }
 
 size_t mxfp4_grouped_gemm_workspace_size(int64_t R, int64_t groups, int64_t N, int64_t K) {
@@ -119,12 +128,21 @@ int mxfp4_grouped_gemm(const void* a, int64_t tokens, int64_t K, int64_t lda, co
     if (!aligned(workspace, 256)) return MXFP4_ERR_ALIGN;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_quantize_groups(static_cast<const uint16_t*>(a), tokens, K, lda, rows, offsets,
-                                                 static_cast<int>(groups), static_cast<int>(R), gated, plan, ws,
-                                                 reinterpret_cast<uint32_t*>(ws + plan.off_counters), s);
-    if (e != cudaSuccess) return cuda_fail(e);
-    return run_stream(plan, di, ws, packed_b, packed_b_bytes(N, K), offsets, static_cast<int>(groups),
-                      static_cast<int>(R), N, c, ldc, 1, s);
+    StreamArgs g = stream_args(packed_b, N, K, c, ldc);
+    g.group_bytes = packed_b_bytes(N, K);
+    g.offsets = offsets;
+    g.groups = static_cast<int>(groups);
+    g.rows = static_cast<int>(R);
+    g.a = static_cast<const uint16_t*>(a);
+    g.lda = lda;
+    g.tokens = tokens;
+    g.index = rows;
+    g.gated = gated ? 1 : 0;
+    if (!plan.fused) {
+        const cudaError_t e = launch_quantize_groups(g.a, tokens, K, lda, rows, offsets, g.groups, g.rows, gated, plan, ws, s);
+        if (e != cudaSuccess) return cuda_fail(e);
+    }
+    return run_stream(plan, di, g, ws, 1, s);
 }
 
 static int64_t route_chunks(int64_t T, int sm_count) {

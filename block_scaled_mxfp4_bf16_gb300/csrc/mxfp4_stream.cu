@@ -21,12 +21,22 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <chrono>
 #include <mutex>
 
 #include "mma_desc.cuh"
 #include "quant_device.cuh"
 #include "stream.h"
 
+#ifndef SPLITCOST
+#define SPLITCOST 8
+#endif
+#ifndef FUSE_M
+#define FUSE_M 4
+#endif
+#ifndef FUSE_MEAN
+#define FUSE_MEAN 8
+#endif
 namespace mxfp4 {
 namespace {
 
@@ -38,7 +48,7 @@ __device__ __forceinline__ void group_rows(const int32_t* offsets, int rows, int
         *n = rows;
         return;
     }
-    const int b = min(max(offsets[g], 0), rows), e = min(max(offsets[g + 1], 0), rows);
+    const int b = min(max(__ldcg(offsets + g), 0), rows), e = min(max(__ldcg(offsets + g + 1), 0), rows);
     *begin = b;
     *n = max(0, e - b);
 }
@@ -47,7 +57,7 @@ __device__ __forceinline__ void group_rows(const int32_t* offsets, int rows, int
 // whole warp with independent loads.
 __device__ __forceinline__ int group_of_row(const int32_t* offsets, int groups, int r, int lane) {
     int below = 0;
-    for (int g = lane; g < groups; g += 32) below += offsets[g + 1] <= r ? 1 : 0;
+    for (int g = lane; g < groups; g += 32) below += __ldcg(offsets + g + 1) <= r ? 1 : 0;
     return __reduce_add_sync(0xffffffffu, below);
 }
 
@@ -73,12 +83,33 @@ __device__ __forceinline__ uint32_t quantize_block32_f32(const float (&v)[32], u
     return static_cast<uint32_t>(s + 127);
 }
 
+// load_block32_upto through L2 (the block may have been written by the previous grid).
+__device__ __forceinline__ void load_block_cg(const uint16_t* src, int64_t avail, uint32_t (&w)[16]) {
+    const uint4* p = reinterpret_cast<const uint4*>(src);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 v = 8 * i < avail ? __ldcg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * i + 0] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+    }
+}
+
 // silu(g) * u of a pair of bf16 words' low and high halves, in fp32 (not rounded to bf16 before it
-// is quantized).
+// is quantized). The exponential and the reciprocal are the hardware's approximations, under 2^-20
+// of the value together where it matters (|g| < 16): what is quantized to four bits next moves by
+// far less than a quantization step, and the exact functions cost five times the instructions.
+// exp(-g) overflows to infinity for g < -88, whose reciprocal is 0.
+__device__ __forceinline__ float silu(float g) {
+    float e, r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return g * r;
+}
 __device__ __forceinline__ void gate_pair(uint32_t g, uint32_t u, float* v) {
-    const float g0 = __uint_as_float(g << 16), g1 = __uint_as_float(g & 0xFFFF0000u);
-    v[0] = g0 / (1.f + expf(-g0)) * __uint_as_float(u << 16);
-    v[1] = g1 / (1.f + expf(-g1)) * __uint_as_float(u & 0xFFFF0000u);
+    v[0] = silu(__uint_as_float(g << 16)) * __uint_as_float(u << 16);
+    v[1] = silu(__uint_as_float(g & 0xFFFF0000u)) * __uint_as_float(u & 0xFFFF0000u);
 }
 
 // A warp takes `step` consecutive 1x32 blocks of one sorted row (all of them when there are rows
@@ -91,13 +122,10 @@ template <bool kGated>
 __global__ void __launch_bounds__(256)
 quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K, int64_t lda,
                        const int32_t* index, const int32_t* offsets, int groups, int rows, int m_tile, int k_atoms,
-                       uint32_t a_block, uint8_t* __restrict__ blocks, uint32_t* counters, int n_counters,
-                       int parts, int step) {
+                       uint32_t a_block, uint8_t* __restrict__ blocks, int parts, int step) {
     pdl_wait_prior_grid();   // a, index and offsets may come from the previous grid
     // dependents may start now: what they read early (the offsets) was complete before this grid
     pdl_launch_dependents();
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0u;
     const int lane = threadIdx.x & 31;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
@@ -174,25 +202,12 @@ __device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
 // it reaches 4 at most: half of the spacing there, 1, leaves 2^(s-3). So every further term adds
 // three bits, and after eight the rest is at most 2^(s0-21), under 2^-22 of the block's largest
 // value: what an fp32 sum keeps of it. Every step is exact in fp32 (a residual is a multiple of
-// the element's last bit, and smaller). Four lanes share a block, eight elements each.
-// A block that holds an infinity or NaN gets the e8m0 NaN as its scales: the token's outputs
-// become NaN. Scales stop at 2^-127; what lies below is dropped.
-__global__ void __launch_bounds__(128)
-expand_terms_kernel(const uint16_t* __restrict__ x, int M, int64_t K, int64_t ldx, int m_tile, int per_tile,
-                    int k_atoms, uint32_t a_block, uint8_t* __restrict__ blocks, uint32_t* counters, int n_counters, FastDiv fd_row) {
-    pdl_launch_dependents();
-    const uint32_t row_items = static_cast<uint32_t>(k_atoms) * 8u;
-    const int lane = threadIdx.x & 31, part = lane & 3;
-    const uint32_t it = (blockIdx.x * blockDim.x + threadIdx.x) >> 2;
-    const uint32_t m = fast_div(it, fd_row);
-    const uint32_t kb = it - m * row_items;
-    const bool live = m < static_cast<uint32_t>(M);
-    const int64_t k = static_cast<int64_t>(kb) * 32 + part * 8;
-    pdl_wait_prior_grid();
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < n_counters; i += blockDim.x) counters[i] = 0u;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (live && k < K) w = *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * ldx + k);
+// the element's last bit, and smaller). Four neighbouring lanes share a block, eight elements w
+// each; emit(t, codes, scale byte) gets each term's four code bytes of the lane. All lanes of the
+// warp call. A block that holds an infinity or NaN gets the e8m0 NaN as its scales: the token's
+// outputs become NaN. Scales stop at 2^-127; what lies below is dropped.
+template <typename Emit>
+__device__ __forceinline__ void expand_quarter(const uint4& w, Emit emit) {
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};
     float v[8];
     uint32_t amax = 0u;
@@ -204,17 +219,13 @@ expand_terms_kernel(const uint16_t* __restrict__ x, int M, int64_t K, int64_t ld
     }
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    if (!live) return;
     const bool finite = amax < 0x7F800000u;
     // exponent of the largest value, one more when its mantissa exceeds 1.5, less 2 (6 = 1.5 * 4)
     int s = max(static_cast<int>((amax + 0x3FFFFFu) >> 23) - 127 - 2, -127);
-    const uint32_t tile = m / static_cast<uint32_t>(per_tile);   // per_tile: tokens per tile
-    const uint32_t r0 = (m - tile * per_tile) * kTerms;
-    uint8_t* blk = blocks + (static_cast<size_t>(tile) * k_atoms + (kb >> 3)) * a_block;
-    const uint32_t c = kb & 7u;
 #pragma unroll
     for (int t = 0; t < kTerms; ++t) {
-        const float up = inv_scale(s), down = s == -127 ? __uint_as_float(0x00400000u) : __uint_as_float(static_cast<uint32_t>(s + 127) << 23);
+        const float up = inv_scale(s);
+        const float down = __uint_as_float(s == -127 ? 0x00400000u : static_cast<uint32_t>(s + 127) << 23);
         uint32_t codes = 0u;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -224,13 +235,35 @@ expand_terms_kernel(const uint16_t* __restrict__ x, int M, int64_t K, int64_t ld
             v[2 * i] = __fmaf_rn(-q.x, down, v[2 * i]);
             v[2 * i + 1] = __fmaf_rn(-q.y, down, v[2 * i + 1]);
         }
-        const uint32_t r = r0 + static_cast<uint32_t>(t);
-        *reinterpret_cast<uint32_t*>(blk + swz_chunk_offset(r, c) + part * 4) = finite ? codes : 0x22222222u;
-        if (part == 0)
-            blk[static_cast<uint32_t>(m_tile) * 128u + block_sf_offset(r, c)] =
-                static_cast<uint8_t>(finite ? s + 127 : 255);
+        emit(t, finite ? codes : 0x22222222u, finite ? static_cast<uint32_t>(s + 127) : 255u);
         s = max(s - (t == 0 ? 2 : 3), -127);
     }
+}
+
+__global__ void __launch_bounds__(128)
+expand_terms_kernel(const uint16_t* __restrict__ x, int M, int64_t K, int64_t ldx, int m_tile, int per_tile,
+                    int k_atoms, uint32_t a_block, uint8_t* __restrict__ blocks, FastDiv fd_row) {
+    pdl_launch_dependents();
+    const uint32_t row_items = static_cast<uint32_t>(k_atoms) * 8u;
+    const uint32_t it = (blockIdx.x * blockDim.x + threadIdx.x) >> 2, part = threadIdx.x & 3;
+    const uint32_t m = fast_div(it, fd_row);
+    const uint32_t kb = it - m * row_items;
+    const bool live = m < static_cast<uint32_t>(M);
+    const int64_t k = static_cast<int64_t>(kb) * 32 + part * 8;
+    pdl_wait_prior_grid();
+    uint4 w = make_uint4(0u, 0u, 0u, 0u);
+    if (live && k < K) w = *reinterpret_cast<const uint4*>(x + static_cast<int64_t>(m) * ldx + k);
+    const uint32_t tile = m / static_cast<uint32_t>(per_tile);   // per_tile: tokens per tile
+    const uint32_t r0 = (m - tile * per_tile) * kTerms, c = kb & 7u;
+    uint8_t* blk = blocks + (static_cast<size_t>(tile) * k_atoms + (kb >> 3)) * a_block;
+    expand_quarter(w, [&](int t, uint32_t codes, uint32_t scale) {
+        const uint32_t r = r0 + static_cast<uint32_t>(t);
+        if (live) {
+            *reinterpret_cast<uint32_t*>(blk + swz_chunk_offset(r, c) + part * 4) = codes;
+            if (part == 0)
+                blk[static_cast<uint32_t>(m_tile) * 128u + block_sf_offset(r, c)] = static_cast<uint8_t>(scale);
+        }
+    });
 }
 
 // ------------------------------------------------------------------------ the product
@@ -326,7 +359,8 @@ __device__ __forceinline__ void locate(const StreamArgs& p, const int* prefix, i
         w.end = prefix[g + 1] * p.n_tiles;
         w.tiles = prefix[g + 1] - prefix[g];
         w.inv_tiles = 1.f / static_cast<float>(w.tiles);
-        group_rows(p.offsets, p.rows, g, &w.begin, &w.n);
+        w.begin = prefix[p.groups + 1 + g];        // the groups' first rows follow the prefix
+        w.n = prefix[p.groups + 2 + g] - w.begin;
         w.per = ((w.n + w.tiles - 1) / w.tiles + 15) / 16 * 16;   // tile_rows(n, m_tile)
     }
     const int r = unit - w.first;
@@ -350,7 +384,8 @@ __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefi
     w.units = units;
     w.waves = p.runs ? 0 : units / static_cast<int>(gridDim.x);
     const int64_t steps = static_cast<int64_t>(units - w.waves * static_cast<int>(gridDim.x)) * p.k_atoms;
-    w.share = max((steps + gridDim.x - 1) / gridDim.x, static_cast<int64_t>(min(p.min_steps, p.k_atoms)));
+    w.share = (steps + gridDim.x - 1) / gridDim.x;
+    if (!p.runs && w.share + SPLITCOST > p.k_atoms) w.share = p.k_atoms;
     w.s = min(steps, w.share * blockIdx.x);
     w.s1 = min(steps, w.s + w.share);
     // the group before the first unit's, by bisection
@@ -470,11 +505,78 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
     }
 }
 
+// One 256-K step (step k of K) of a tile's tokens into a stage, by one warp.
+// Grouped: a lane per 1x32 block, eight to a row; src: in lane r, the row of A that row r reads (-1:
+// zeros). Weight-only: a token at a time, four lanes per block.
+template <int kTermsPer>
+__device__ __forceinline__ void write_step(const StreamArgs& p, const Walk& u, int k, int64_t src, uint8_t* blk, int lane) {
+    const int64_t k0 = static_cast<int64_t>(k) * kAtomK;
+    uint8_t* sf = blk + p.m_tile * 128;
+    if constexpr (kTermsPer == 1) {
+        for (int r0 = 0; r0 < u.rows; r0 += 4) {
+            const int r = r0 + (lane >> 3);
+            const uint32_t c = static_cast<uint32_t>(lane & 7);
+            const int64_t row = __shfl_sync(0xffffffffu, src, r & 31);
+            const int64_t left = p.K - (k0 + c * 32);
+            const bool present = r < u.rows && row >= 0 && left > 0;
+            uint32_t v[16], out[4] = {0u, 0u, 0u, 0u}, byte = 0u;
+            const uint16_t* at = p.a + row * p.lda + k0 + c * 32;
+            if (present) load_block_cg(at, left, v);
+            if (p.gated) {
+                uint32_t g[16];
+                if (present) {
+                    load_block_cg(at + p.K, left, g);
+                    float h[32];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) gate_pair(v[i], g[i], &h[2 * i]);
+                    byte = quantize_block32_f32(h, out);
+                }
+            } else if (present) {
+                byte = quantize_block32(v, out);
+            }
+            if (r < u.rows) {
+                *reinterpret_cast<uint4*>(blk + swz_chunk_offset(static_cast<uint32_t>(r), c)) =
+                    make_uint4(out[0], out[1], out[2], out[3]);
+                sf[block_sf_offset(static_cast<uint32_t>(r), c)] = static_cast<uint8_t>(byte);
+            }
+        }
+    } else {
+        const int64_t at = k0 + lane * 8;
+        const uint32_t c = static_cast<uint32_t>(lane >> 2), part = static_cast<uint32_t>(lane & 3);
+        const int m0 = u.row0 / kTermsPer, tokens = u.rows / kTermsPer;
+        for (int m = 0; m < tokens; ++m) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (at < p.K) w = __ldcg(reinterpret_cast<const uint4*>(p.a + (m0 + m) * p.lda + at));
+            expand_quarter(w, [&](int t, uint32_t codes, uint32_t scale) {
+                const uint32_t r = static_cast<uint32_t>(m * kTerms + t);
+                *reinterpret_cast<uint32_t*>(blk + swz_chunk_offset(r, c) + part * 4) = codes;
+                if (part == 0) sf[block_sf_offset(r, c)] = static_cast<uint8_t>(scale);
+            });
+        }
+    }
+}
+
+// One more arrival at a split unit's counter: how many came before. A word belongs to this call if
+// its upper bits are the call's tag, which no other call has; anything else, left there by other
+// uses of the workspace, counts as none. So the counters need no launch that clears them.
+// `seen`: the word as read a moment ago.
+__device__ __forceinline__ uint32_t arrive(unsigned long long* counter, unsigned long long seen, uint64_t tag) {
+    while (true) {
+        const unsigned long long mine = (seen >> 8) == tag ? seen : static_cast<unsigned long long>(tag << 8);
+        const unsigned long long was = atomicCAS(counter, seen, mine + 1);
+        if (was == seen) return static_cast<uint32_t>(mine & 0xFFu);
+        seen = was;
+    }
+}
+
 }  // namespace
 
-template <int kTermsPer>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+// kFused: tiles of few rows, whose tokens six warps (2, 3, 12-15) quantize or expand straight into
+// the stages, a step each in turn: no token blocks in memory and no launch before this one.
+template <int kTermsPer, bool kFused>
+__global__ void __launch_bounds__(kFused ? kFusedThreads : kStreamThreads, 1)
 mxfp4_stream_kernel(const StreamArgs p) {
+    constexpr int kThreads = kFused ? kFusedThreads : kStreamThreads;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t stage_bytes = kWBlock + p.a_block;
@@ -490,6 +592,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
     int* warp_sum = reinterpret_cast<int*>(tmem_slot + 8);       // [16]
     uint8_t* epi_stage = reinterpret_cast<uint8_t*>(warp_sum + 16);   // [8 warps][kEpiStage]
     int* prefix = reinterpret_cast<int*>(epi_stage + 8 * kEpiStage);  // [groups + 1] token tiles before a group
+    int* begins = prefix + p.groups + 1;                              // [groups + 1] first rows of the groups
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
@@ -497,7 +600,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], kFused ? 2 : 1);   // the copies' bytes, and in fused tiles a token warp
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -509,19 +612,23 @@ mxfp4_stream_kernel(const StreamArgs p) {
     }
     // Token tiles before each group: an inclusive scan over the groups, a chunk of the block's
     // threads at a time. The offsets were complete before the token-block writer started its
-    // dependents, so they are read (and the first weights requested) while it still runs.
+    // dependents, so they are read (and the first weights requested) while it still runs; without
+    // a writer, after the wait for the work before.
     // Offsets that decrease or leave [0, rows] would break the tiling: then no unit is computed.
     int carry = 0;
     bool bad = false;
-    for (int g0 = 0; g0 < p.groups; g0 += kStreamThreads) {
+    if (kFused && p.offsets) pdl_wait_prior_grid();
+    for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
         const int g = g0 + static_cast<int>(threadIdx.x);
         int t = 0;
         if (g < p.groups) {
             int begin, n;
             group_rows(p.offsets, p.rows, g, &begin, &n);
             t = tiles_of(n, p.m_tile);
+            begins[g] = begin;
+            if (g == p.groups - 1) begins[p.groups] = begin + n;
             if (p.offsets) {
-                const int b = p.offsets[g], e = p.offsets[g + 1];
+                const int b = __ldcg(p.offsets + g), e = __ldcg(p.offsets + g + 1);
                 bad = bad || b < 0 || e < b || e > p.rows;
             }
         }
@@ -534,7 +641,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
         if (lane == 31) warp_sum[warp] = t;
         __syncthreads();
         int before = carry;
-        for (int i = 0; i < kStreamThreads / 32; ++i) {
+        for (int i = 0; i < kThreads / 32; ++i) {
             const int v = warp_sum[i];
             if (i < warp) before += v;
             carry += v;
@@ -562,7 +669,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
                 const uint8_t* w = p.wblk + static_cast<size_t>(u.group) * p.group_bytes +
                                    (static_cast<size_t>(u.nt) * p.k_atoms + u.k0) * kWBlock;
                 const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15);
-                const uint32_t tok = n16 * 128u + (n16 > 128u ? 4u : 2u) * kSfChunk;
+                const uint32_t tok = kFused ? 0u : n16 * 128u + (n16 > 128u ? 4u : 2u) * kSfChunk;
                 for (int j = 0; j < u.nk && early < p.stages; ++j, ++early, w += kWBlock) {
                     const uint32_t bar = full0 + static_cast<uint32_t>(early) * 8u;
                     mbar_expect_if(issue, bar, kWBlock + tok);
@@ -590,12 +697,14 @@ mxfp4_stream_kernel(const StreamArgs p) {
                 }
                 const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
                 if (issued >= early) {
-                    mbar_expect_if(issue, bar, kWBlock + tok_rows + tok_sf);
+                    mbar_expect_if(issue, bar, kWBlock + (kFused ? 0u : tok_rows + tok_sf));
                     bulk_load_if(issue, sw0 + static_cast<uint32_t>(s) * kWBlock, w, kWBlock, bar, pol_w);
                 }
-                const uint32_t dst = st0 + static_cast<uint32_t>(s) * p.a_block;
-                bulk_load_if(issue, dst, t, tok_rows, bar, pol_t);
-                bulk_load_if(issue, dst + sf_off, t + sf_off, tok_sf, bar, pol_t);
+                if (!kFused) {
+                    const uint32_t dst = st0 + static_cast<uint32_t>(s) * p.a_block;
+                    bulk_load_if(issue, dst, t, tok_rows, bar, pol_t);
+                    bulk_load_if(issue, dst + sf_off, t + sf_off, tok_sf, bar, pol_t);
+                }
                 w += kWBlock;
                 t += p.a_block;
                 ++issued;
@@ -688,6 +797,34 @@ mxfp4_stream_kernel(const StreamArgs p) {
             }
         }
         __syncwarp();
+    } else if (kFused && (warp < 4 || warp >= 12)) {
+        // ---------------------------------------------------------------------- tokens
+        const int tw = warp < 4 ? warp - 2 : warp - 10;
+        pdl_wait_prior_grid();
+        Walk u = start;
+        int step = 0, mine = tw;    // steps before the share; the next step that is this warp's
+        bool ok = true;
+        while (ok && next_share(p, prefix, u)) {
+            int64_t src = -1;       // grouped: lane r's row of A
+            if (kTermsPer == 1 && mine < step + u.nk && lane < u.rows) {
+                src = p.index ? static_cast<int64_t>(__ldcg(p.index + u.row0 + lane)) : u.row0 + lane;
+                if (src >= p.tokens) src = -1;
+            }
+            for (; mine < step + u.nk; mine += kTokenWarps) {
+                const int s = mine % p.stages;
+                if (mine >= p.stages && !mbar_wait(&empty[s], (mine / p.stages - 1) & 1, lim)) {
+                    stream_fail(p, abort_flag);
+                    ok = false;
+                    break;
+                }
+                write_step<kTermsPer>(p, u, u.k0 + (mine - step), src, sT + static_cast<uint32_t>(s) * p.a_block, lane);
+                fence_proxy_async_smem();   // the MMAs read the stage through the async proxy
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+            }
+            step += u.nk;
+        }
+        __syncwarp();
     } else if (warp >= 4) {
         // ---------------------------------------------------------------------- epilogue
         pdl_wait_prior_grid();   // C and the workspace may still be read by earlier work
@@ -727,8 +864,9 @@ mxfp4_stream_kernel(const StreamArgs p) {
                     const uint32_t others = static_cast<uint32_t>(c_last - c_first);
                     const int slot = u.k0 == 0 && u.s - u.nk != u.share * static_cast<int64_t>(blockIdx.x) ? 1 : 0;
                     volatile uint32_t* flag = last_flag + 2 * slot;
-                    uint32_t* counter = p.counters + c_first;   // a split unit is named by its first CTA
-                    if (threadIdx.x == 128) flag[0] = *reinterpret_cast<volatile uint32_t*>(counter) == others ? 1u : 0u;
+                    unsigned long long* counter = p.counters + c_first;   // a split unit is named by its first CTA
+                    if (threadIdx.x == 128)
+                        flag[0] = *reinterpret_cast<volatile unsigned long long*>(counter) == (p.tag << 8 | others) ? 1u : 0u;
                     named_barrier(2, kStreamEpiThreads);
                     last = flag[0] != 0u;
                     if (!last) {
@@ -741,13 +879,16 @@ mxfp4_stream_kernel(const StreamArgs p) {
                             for (int i = 0; i < kTok; ++i)
                                 if (m0 + i < tokens) __stcg(mine + static_cast<size_t>(m0 + i) * kTileN + nl, v[i]);
                         }
+                        unsigned long long seen = 0ull;
+                        if (threadIdx.x == 128) seen = *reinterpret_cast<volatile unsigned long long*>(counter);
                         __threadfence();
                         named_barrier(2, kStreamEpiThreads);
-                        if (threadIdx.x == 128) flag[1] = atomicAdd(counter, 1u) == others ? 1u : 0u;
+                        if (threadIdx.x == 128) flag[1] = arrive(counter, seen, p.tag) == others ? 1u : 0u;
                         named_barrier(2, kStreamEpiThreads);
                         last = flag[1] != 0u;
                     }
                     __threadfence();
+                    if (last && threadIdx.x == 128) *counter = 0ull;   // as found by a replay of this launch
                 }
                 if (last) {
                     for (int cb = half * 16; cb < u.rows; cb += 32) {
@@ -807,23 +948,23 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     p.n_tiles = static_cast<int>((N + kTileN - 1) / kTileN);
     if (terms > 1) {
         p.m_tile = static_cast<int>(rows < 128 ? (rows + 15) / 16 * 16 : 128);
+        p.fused = rows <= FUSE_M * kTerms;
     } else {
         const int64_t mean = (rows + groups - 1) / groups;
-        
-        p.m_tile = mean <= 48 ? 64 : mean <= 256 ? 128 : 192;
+        p.fused = mean <= FUSE_MEAN;
+        p.m_tile = p.fused ? 32 : mean <= 48 ? 64 : mean <= 256 ? 128 : 192;
         // Groups of several tiles with short K: no waves, every CTA takes the tiles of a weight tile
         // one after the other and rereads its weights from L2, where all CTAs' fit (152 x 12 steps
         // are 32 MB; 6000 rows in 48 groups x 2880 x 2040 53.7 -> 50.0 us, but 16384 rows in 16 groups
         // x 4096 x 7168, 28 steps, 240 -> 428). In waves the CTAs of a group read a weight at the
         // same time, once from memory, but then wait for the same few weights together.
         p.runs = mean > 48 && p.k_atoms <= 12;
-
     }
     p.min_steps = 4;
     p.nmc = (p.m_tile + 127) / 128;
     p.a_block = static_cast<uint32_t>(p.m_tile) * 128u + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
     const size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 + 8 * kEpiStage +
-                         (static_cast<size_t>(groups) + 1) * 4;
+                         2 * (static_cast<size_t>(groups) + 1) * 4;
     p.stages = static_cast<int>((kSmemLimit - extra) / (kWBlock + p.a_block));
     if (p.stages > kStreamMaxStages) p.stages = kStreamMaxStages;
     p.smem_bytes = static_cast<size_t>(p.stages) * (kWBlock + p.a_block) + extra;
@@ -835,17 +976,32 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     if (tiles * p.n_tiles > (int64_t(1) << 31) - 1) return -1;
     const int64_t steps = tiles * p.n_tiles * static_cast<int64_t>(p.k_atoms);
     p.ctas = static_cast<int>(steps < sm_count ? steps : sm_count);
-    const size_t blocks = static_cast<size_t>(tiles) * p.k_atoms * p.a_block;
+    const size_t blocks = p.fused ? 0 : static_cast<size_t>(tiles) * p.k_atoms * p.a_block;
     p.off_counters = (blocks + 1023) / 1024 * 1024;
-    p.off_partial = p.off_counters + (static_cast<size_t>(p.ctas + 1) * 4 + 1023) / 1024 * 1024;
+    p.off_partial = p.off_counters + (static_cast<size_t>(p.ctas) * 8 + 1023) / 1024 * 1024;
     p.ws_total = p.off_partial + static_cast<size_t>(p.ctas) * 2 * (p.m_tile / terms) * kTileN * sizeof(float);
     *out = p;
     return 0;
 }
 
+// A number of this process's own for every call, 56 bits and never 0 (the splitmix64 finaliser of a
+// counter that starts at the clock and the process's address layout).
+uint64_t next_call_tag() {
+    static std::atomic<uint64_t> counter{
+        static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count()) ^
+        (reinterpret_cast<uintptr_t>(&make_stream_plan) << 20)};
+    while (true) {
+        uint64_t z = counter.fetch_add(1, std::memory_order_relaxed) * 0x9E3779B97F4A7C15ull;
+        z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+        z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+        z = (z ^ (z >> 31)) >> 8;
+        if (z != 0) return z;
+    }
+}
+
 cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,
                                    const int32_t* offsets, int groups, int rows, bool gated, const StreamPlan& plan,
-                                   uint8_t* blocks, uint32_t* counters, cudaStream_t s) {
+                                   uint8_t* blocks, cudaStream_t s) {
     // as many parts of a row as make enough warps for every SM, whole rows beyond that
     const int chunks = (plan.k_atoms * 8 + 31) / 32;
     const int64_t want = (int64_t(4096) + rows - 1) / rows;
@@ -855,40 +1011,39 @@ cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K,
     if (grid > 65535) grid = 65535;
     return launch_pdl(gated ? quantize_groups_kernel<true> : quantize_groups_kernel<false>,
                       dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, tokens, K, lda, index, offsets, groups, rows,
-                      plan.m_tile, plan.k_atoms, plan.a_block, blocks, counters, plan.ctas + 1, parts, per * 32);
+                      plan.m_tile, plan.k_atoms, plan.a_block, blocks, parts, per * 32);
 }
 
 cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx, const StreamPlan& plan,
-                                uint8_t* blocks, uint32_t* counters, cudaStream_t s) {
+                                uint8_t* blocks, cudaStream_t s) {
     const int64_t lanes = static_cast<int64_t>(M) * plan.k_atoms * 8 * 4;
     return launch_pdl(expand_terms_kernel, dim3(static_cast<unsigned>((lanes + 127) / 128)), dim3(128), 0, s, x, M, K, ldx,
                       plan.m_tile, tile_rows(M * kTerms, plan.m_tile) / kTerms, plan.k_atoms, plan.a_block, blocks,
-                      counters, plan.ctas + 1, make_fastdiv(static_cast<uint32_t>(plan.k_atoms) * 8u));
+                      make_fastdiv(static_cast<uint32_t>(plan.k_atoms) * 8u));
 }
 
-template <int kTermsPer>
-static cudaError_t set_stream_attributes() {
+template <int kTermsPer, bool kFused>
+static cudaError_t launch_stream_as(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {
     static std::mutex mu;
     static std::atomic<bool> done[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(mxfp4_stream_kernel<kTermsPer>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kSmemLimit));
-    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
-    return e;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        std::lock_guard<std::mutex> lock(mu);
+        e = cudaFuncSetAttribute(mxfp4_stream_kernel<kTermsPer, kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kSmemLimit));
+        if (e != cudaSuccess) return e;
+        done[dev].store(true, std::memory_order_release);
+    }
+    return launch_pdl(mxfp4_stream_kernel<kTermsPer, kFused>, dim3(plan.ctas), dim3(kFused ? kFusedThreads : kStreamThreads),
+                      plan.smem_bytes, s, args);
 }
 
 cudaError_t launch_stream(const StreamPlan& plan, const StreamArgs& args, int terms, cudaStream_t s) {
-    cudaError_t e = terms == 1 ? set_stream_attributes<1>() : set_stream_attributes<kTerms>();
-    if (e != cudaSuccess) return e;
-    return terms == 1 ? launch_pdl(mxfp4_stream_kernel<1>, dim3(plan.ctas), dim3(kStreamThreads), plan.smem_bytes, s, args)
-                      : launch_pdl(mxfp4_stream_kernel<kTerms>, dim3(plan.ctas), dim3(kStreamThreads), plan.smem_bytes, s,
-                                   args);
+    if (terms == 1) return plan.fused ? launch_stream_as<1, true>(plan, args, s) : launch_stream_as<1, false>(plan, args, s);
+    return plan.fused ? launch_stream_as<kTerms, true>(plan, args, s) : launch_stream_as<kTerms, false>(plan, args, s);
 }
 
 }  // namespace mxfp4

@@ -8,6 +8,8 @@ namespace mxfp4 {
 constexpr int kMaxGroups = 1024;          // groups (experts) one launch can address
 constexpr int kStreamThreads = 384;       // warps 0-3: copies, MMAs, two spare; warps 4-11: epilogue
 constexpr int kStreamEpiThreads = 256;
+constexpr int kFusedThreads = 512;        // warps 2, 3 and 12-15 write the tokens' stages
+constexpr int kTokenWarps = 6;
 constexpr int kStreamMaxStages = 10;
 constexpr int kEpiStage = 640;            // bytes of shared memory an epilogue warp transposes through
 constexpr int kTerms = 8;                 // e2m1 terms an activation is expanded into (weight-only)
@@ -36,7 +38,13 @@ struct StreamArgs {
     uint16_t* c;
     int64_t ldc;
     float* partial;           // [2 * CTAs][128 * tokens per tile] fp32 partial sums of split units
-    uint32_t* counters;       // [CTAs + 1] arrivals per split unit, zero at the start
+    unsigned long long* counters;   // [CTAs] arrivals per split unit under the call's tag
+    uint64_t tag;
+    // fused: the activations themselves instead of token blocks
+    const uint16_t* a;
+    int64_t lda, tokens, K;
+    const int32_t* index;     // grouped: row of a for each sorted row, or null
+    int gated;
     uint32_t* status;
     int groups, rows, N;      // rows: token-block rows (grouped) or tokens * terms (weight-only)
     int m_tile, nmc, n_tiles, k_atoms, stages;
@@ -50,6 +58,7 @@ struct StreamArgs {
 
 struct StreamPlan {
     int m_tile, nmc, stages, ctas, k_atoms, n_tiles, min_steps, runs;
+    int fused;                // tokens written by the product's own warps, no launch before it
     uint32_t a_block, tmem_cols;
     size_t smem_bytes;
     size_t off_counters, off_partial, ws_total;   // workspace: token blocks at 0
@@ -61,10 +70,11 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
 // a [tokens, K] rows -> token blocks of the sorted rows: row r of the blocks is a[index ? index[r] : r].
 cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,
                                    const int32_t* offsets, int groups, int rows, bool gated, const StreamPlan& plan,
-                                   uint8_t* blocks, uint32_t* counters, cudaStream_t s);
+                                   uint8_t* blocks, cudaStream_t s);
 // x [M, K] rows -> kTerms token-block rows per token.
 cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx, const StreamPlan& plan,
-                                uint8_t* blocks, uint32_t* counters, cudaStream_t s);
+                                uint8_t* blocks, cudaStream_t s);
+uint64_t next_call_tag();
 cudaError_t launch_stream(const StreamPlan& plan, const StreamArgs& args, int terms, cudaStream_t s);
 
 // Routing and combination (moe.cu).
