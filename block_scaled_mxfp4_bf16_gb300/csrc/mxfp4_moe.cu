@@ -368,34 +368,55 @@ cudaError_t launch_route(const RouteArgs& args, cudaStream_t s) {
 // ------------------------------------------------------------------------ combination
 
 // out[t, n..n+kVec) = sum over j of weights[t, j] * y[slots[t, j], n..n+kVec) in fp32, in the order
-// of j; a slot outside [0, rows) adds nothing.
+// of j; a slot outside [0, rows) adds nothing. Bound by the bytes of y: the slots of eight j are
+// read together, then all their rows' pieces are in flight before the first is added.
 template <int kVec>
 __global__ void __launch_bounds__(256)
 combine_kernel(const uint16_t* __restrict__ y, int64_t rows, int64_t ldy, const int32_t* __restrict__ slots,
-               const float* __restrict__ weights, int64_t items, int k, int64_t vecs, int64_t N,
-               uint16_t* __restrict__ out, int64_t ldo) {
+               const float* __restrict__ weights, int64_t T, int k, int vecs, uint16_t* __restrict__ out, int64_t ldo) {
     pdl_launch_dependents();
     pdl_wait_prior_grid();
+    const int64_t items = T * vecs;
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; it < items;
          it += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-        const int64_t t = it / vecs, n = (it - t * vecs) * kVec;
+        const int64_t t = items <= 0xFFFFFFFFll ? static_cast<int64_t>(static_cast<uint32_t>(it) / static_cast<uint32_t>(vecs))
+                                                : it / vecs;
+        const int64_t n = (it - t * vecs) * kVec;
         float acc[kVec] = {};
-        for (int j = 0; j < k; ++j) {
-            const int64_t slot = slots[t * k + j];
-            if (slot < 0 || slot >= rows) continue;
-            const float w = weights[t * k + j];
-            const uint16_t* src = y + slot * ldy + n;
+        constexpr int kFlight = 8;
+        for (int j0 = 0; j0 < k; j0 += kFlight) {
+            int32_t slot[kFlight];
+            float w[kFlight];
+#pragma unroll
+            for (int u = 0; u < kFlight; ++u) {
+                slot[u] = j0 + u < k ? slots[t * k + j0 + u] : -1;
+                w[u] = j0 + u < k ? weights[t * k + j0 + u] : 0.f;
+            }
             if constexpr (kVec == 8) {
-                const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src));
-                const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+                uint4 v[kFlight];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[2 * i] = fmaf(w, __uint_as_float(words[i] << 16), acc[2 * i]);
-                    acc[2 * i + 1] = fmaf(w, __uint_as_float(words[i] & 0xFFFF0000u), acc[2 * i + 1]);
-                }
+                for (int u = 0; u < kFlight; ++u)
+                    if (slot[u] >= 0 && slot[u] < rows)
+                        v[u] = __ldcs(reinterpret_cast<const uint4*>(y + slot[u] * ldy + n));
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u)
+                    if (slot[u] >= 0 && slot[u] < rows) {
+                        const uint32_t words[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            acc[2 * i] = fmaf(w[u], __uint_as_float(words[i] << 16), acc[2 * i]);
+                            acc[2 * i + 1] = fmaf(w[u], __uint_as_float(words[i] & 0xFFFF0000u), acc[2 * i + 1]);
+                        }
+                    }
             } else {
+                uint16_t v[kFlight];
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) acc[i] = fmaf(w, __uint_as_float(static_cast<uint32_t>(src[i]) << 16), acc[i]);
+                for (int u = 0; u < kFlight; ++u)
+                    if (slot[u] >= 0 && slot[u] < rows) v[u] = y[slot[u] * ldy + n];
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u)
+                    if (slot[u] >= 0 && slot[u] < rows)
+                        acc[0] = fmaf(w[u], __uint_as_float(static_cast<uint32_t>(v[u]) << 16), acc[0]);
             }
         }
         uint16_t* dst = out + t * ldo + n;
@@ -406,10 +427,9 @@ combine_kernel(const uint16_t* __restrict__ y, int64_t rows, int64_t ldy, const 
                 const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
                 words[i] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            *reinterpret_cast<uint4*>(dst) = make_uint4(words[0], words[1], words[2], words[3]);
+            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(words[0], words[1], words[2], words[3]));
         } else {
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) dst[i] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i]));
+            dst[0] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
         }
     }
 }
@@ -418,11 +438,11 @@ cudaError_t launch_combine(const uint16_t* y, int64_t rows, int64_t ldy, const i
                            int64_t T, int k, int64_t N, uint16_t* out, int64_t ldo, cudaStream_t s) {
     const bool vec = N % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0 &&
                      reinterpret_cast<uintptr_t>(out) % 16 == 0;
-    const int64_t vecs = vec ? N / 8 : N, items = T * vecs;
-    const int64_t blocks = (items + 255) / 256;
+    const int vecs = static_cast<int>(vec ? N / 8 : N);
+    const int64_t blocks = (T * vecs + 255) / 256;
     const dim3 grid(static_cast<unsigned>(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF));
-    return vec ? launch_pdl(combine_kernel<8>, grid, dim3(256), 0, s, y, rows, ldy, slots, weights, items, k, vecs, N, out, ldo)
-               : launch_pdl(combine_kernel<1>, grid, dim3(256), 0, s, y, rows, ldy, slots, weights, items, k, vecs, N, out, ldo);
+    return launch_pdl(vec ? combine_kernel<8> : combine_kernel<1>, grid, dim3(256), 0, s, y, rows, ldy, slots, weights, T, k,
+                      vecs, out, ldo);
 }
 
 }  // namespace mxfp4

@@ -24,7 +24,7 @@ bool gemv_sizes_ok(int64_t M, int64_t N, int64_t K) {
 int stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, DeviceInfo* di, StreamPlan* plan) {
     const int st = device_info(di);
     if (st != MXFP4_OK) return st;
-    return make_stream_plan(rows, groups, N, K, terms, di->sm_count, plan) == 0 ? MXFP4_OK : MXFP4_ERR_SHAPE;
+    return make_stream_plan(rows, groups, N, K, terms, di->sm_count, stream_clusters, plan) == 0 ? MXFP4_OK : MXFP4_ERR_SHAPE;
 }
 
 // The operands of a stream product, and the launch.
@@ -50,7 +50,7 @@ int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8
     a.n_tiles = plan.n_tiles;
     a.k_atoms = plan.k_atoms;
     a.stages = plan.stages;
-    a.min_steps = plan.min_steps;
+    a.cluster = plan.cluster;
     a.runs = plan.runs;
     a.a_block = plan.a_block;
     a.tmem_cols = plan.tmem_cols;

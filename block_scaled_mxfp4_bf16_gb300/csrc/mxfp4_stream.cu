@@ -28,15 +28,6 @@
 #include "quant_device.cuh"
 #include "stream.h"
 
-#ifndef SPLITCOST
-#define SPLITCOST 8
-#endif
-#ifndef FUSE_M
-#define FUSE_M 4
-#endif
-#ifndef FUSE_MEAN
-#define FUSE_MEAN 8
-#endif
 namespace mxfp4 {
 namespace {
 
@@ -385,9 +376,17 @@ __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefi
     w.waves = p.runs ? 0 : units / static_cast<int>(gridDim.x);
     const int64_t steps = static_cast<int64_t>(units - w.waves * static_cast<int>(gridDim.x)) * p.k_atoms;
     w.share = (steps + gridDim.x - 1) / gridDim.x;
-    if (!p.runs && w.share + SPLITCOST > p.k_atoms) w.share = p.k_atoms;
+    // a split unit costs what eight steps do (4 us: sums out, arrival, sums in): not for less
+    if (!p.runs && w.share + kSplitSteps > p.k_atoms) w.share = p.k_atoms;
     w.s = min(steps, w.share * blockIdx.x);
     w.s1 = min(steps, w.s + w.share);
+    if (p.cluster > 1) {   // the CTAs of a cluster share one unit
+        const int rank = static_cast<int>(blockIdx.x) % p.cluster;
+        const int base = p.k_atoms / p.cluster, rem = p.k_atoms % p.cluster;
+        w.waves = 0;
+        w.s = static_cast<int64_t>(blockIdx.x / p.cluster) * p.k_atoms + rank * base + min(rank, rem);
+        w.s1 = min(static_cast<int64_t>(units) * p.k_atoms, w.s + base + (rank < rem ? 1 : 0));
+    }
     // the group before the first unit's, by bisection
     const int unit = w.waves ? static_cast<int>(blockIdx.x) : static_cast<int>(w.s / p.k_atoms);
     int lo = 0, hi = p.groups;
@@ -571,12 +570,13 @@ __device__ __forceinline__ uint32_t arrive(unsigned long long* counter, unsigned
 
 }  // namespace
 
-// kFused: tiles of few rows, whose tokens six warps (2, 3, 12-15) quantize or expand straight into
-// the stages, a step each in turn: no token blocks in memory and no launch before this one.
+// kFused: tiles of few rows, whose tokens warps of their own (2, 3 and from 12 on) quantize or expand
+// straight into the stages, a step each in turn: no token blocks in memory and no launch before this one.
 template <int kTermsPer, bool kFused>
-__global__ void __launch_bounds__(kFused ? kFusedThreads : kStreamThreads, 1)
+__global__ void __launch_bounds__(stream_threads(kTermsPer, kFused), 1)
 mxfp4_stream_kernel(const StreamArgs p) {
-    constexpr int kThreads = kFused ? kFusedThreads : kStreamThreads;
+    constexpr int kThreads = stream_threads(kTermsPer, kFused);
+    constexpr int kTokenWarps = token_warps(kTermsPer);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t stage_bytes = kWBlock + p.a_block;
@@ -593,22 +593,28 @@ mxfp4_stream_kernel(const StreamArgs p) {
     uint8_t* epi_stage = reinterpret_cast<uint8_t*>(warp_sum + 16);   // [8 warps][kEpiStage]
     int* prefix = reinterpret_cast<int*>(epi_stage + 8 * kEpiStage);  // [groups + 1] token tiles before a group
     int* begins = prefix + p.groups + 1;                              // [groups + 1] first rows of the groups
+    float* recv = reinterpret_cast<float*>(begins + p.groups + 1);    // [cluster - 1][tokens][128], first CTA of a cluster
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const uint64_t lim = p.wait_limit_ns;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < p.stages; ++s) {
-            mbar_init(&full[s], kFused ? 2 : 1);   // the copies' bytes, and in fused tiles a token warp
-            mbar_init(&empty[s], 1);
-        }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], kStreamEpiThreads / 32);
-        }
-        *abort_flag = 0u;
+    if (threadIdx.x < p.stages) {
+        mbar_init(&full[threadIdx.x], kFused ? 2 : 1);   // the copies' bytes, and in fused tiles a token warp
+        mbar_init(&empty[threadIdx.x], 1);
         fence_mbar_init();
+    } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
+        mbar_init(&acc_full[threadIdx.x - 32], 1);
+        mbar_init(&acc_empty[threadIdx.x - 32], kStreamEpiThreads / 32);
+        fence_mbar_init();
+    } else if (threadIdx.x == 64) {
+        *abort_flag = 0u;
+        prefix[0] = 0;
+        if (!p.offsets) {   // one group
+            prefix[1] = tiles_of(p.rows, p.m_tile);
+            begins[0] = 0;
+            begins[1] = p.rows;
+        }
     }
     // Token tiles before each group: an inclusive scan over the groups, a chunk of the block's
     // threads at a time. The offsets were complete before the token-block writer started its
@@ -618,7 +624,8 @@ mxfp4_stream_kernel(const StreamArgs p) {
     int carry = 0;
     bool bad = false;
     if (kFused && p.offsets) pdl_wait_prior_grid();
-    for (int g0 = 0; g0 < p.groups; g0 += kThreads) {
+    if (!p.offsets) carry = tiles_of(p.rows, p.m_tile);
+    for (int g0 = 0; p.offsets && g0 < p.groups; g0 += kThreads) {
         const int g = g0 + static_cast<int>(threadIdx.x);
         int t = 0;
         if (g < p.groups) {
@@ -627,10 +634,8 @@ mxfp4_stream_kernel(const StreamArgs p) {
             t = tiles_of(n, p.m_tile);
             begins[g] = begin;
             if (g == p.groups - 1) begins[p.groups] = begin + n;
-            if (p.offsets) {
-                const int b = __ldcg(p.offsets + g), e = __ldcg(p.offsets + g + 1);
-                bad = bad || b < 0 || e < b || e > p.rows;
-            }
+            const int b = __ldcg(p.offsets + g), e = __ldcg(p.offsets + g + 1);
+            bad = bad || b < 0 || e < b || e > p.rows;
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -648,9 +653,10 @@ mxfp4_stream_kernel(const StreamArgs p) {
         }
         if (g < p.groups) prefix[g + 1] = before + t;
     }
-    if (threadIdx.x == 0) prefix[0] = 0;
     const int units = __syncthreads_or(bad ? 1 : 0) ? 0 : carry * p.n_tiles;
     const Walk start = begin_walk(p, prefix, units);
+    const bool clustered = kTermsPer > 1 && p.cluster > 1;
+    if (clustered) cluster_arrive_relaxed();   // this CTA's shared memory may be written by its peers
     pdl_launch_dependents();
 
     if (warp == 0) {
@@ -838,6 +844,8 @@ mxfp4_stream_kernel(const StreamArgs p) {
         const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;
         Walk u = start;
         int nshare = 0;
+        int unit_n = 0, unit_tokens = 0;
+        int64_t unit_row0 = 0;
         while (next_share(p, prefix, u)) {
             const int b = nshare & 1;
             const bool got = mbar_wait(&acc_full[b], (nshare >> 1) & 1, lim);
@@ -848,7 +856,28 @@ mxfp4_stream_kernel(const StreamArgs p) {
             const int n = u.nt * kTileN + nl;
             const int tokens = u.rows / kTermsPer;   // exact: rows are kTermsPer per token
             const int64_t row0 = u.row0 / kTermsPer;
-            if (kTermsPer == 1 && u.split < 0) {
+            if (clustered) {
+                // this CTA's part of the cluster's unit: into the first CTA's shared memory, which
+                // adds the parts below, once every CTA has passed the cluster's barrier
+                unit_n = n;
+                unit_tokens = tokens;
+                unit_row0 = row0;
+                const uint32_t rank = blockIdx.x % p.cluster;
+                __syncwarp();
+                cluster_wait();    // the first CTA runs
+                if (rank != 0u) {
+                    const uint32_t to = map_to_rank(smem_addr(recv), 0u) +
+                                        (rank - 1u) * static_cast<uint32_t>(slot_floats) * 4u + static_cast<uint32_t>(nl) * 4u;
+                    for (int cb = half * 16; cb < u.rows; cb += 32) {
+                        float v[kTok];
+                        load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
+                        const int m0 = cb / kTermsPer;
+#pragma unroll
+                        for (int i = 0; i < kTok; ++i)
+                            if (m0 + i < tokens) st_cluster_f32(to + static_cast<uint32_t>(m0 + i) * (kTileN * 4u), v[i]);
+                    }
+                }
+            } else if (kTermsPer == 1 && u.split < 0) {
                 store_tile(p, acc, u.rows, u.row0, u.nt * kTileN + (warp & 3) * 32, half, lane,
                            epi_stage + (warp - 4) * kEpiStage);
             } else {
@@ -931,6 +960,33 @@ mxfp4_stream_kernel(const StreamArgs p) {
             if (lane == 0) mbar_arrive(&acc_empty[b]);
             ++nshare;
         }
+        if (clustered) {
+            if (nshare == 0) cluster_wait();   // failed, or no share: the handshake all the same
+            __syncwarp();
+            cluster_sync();
+            if (blockIdx.x % p.cluster == 0u && nshare != 0 && *abort_flag == 0u && unit_n < p.N) {
+                for (int cb = half * 16; cb < unit_tokens * kTermsPer; cb += 32) {
+                    float v[kTok];
+                    const int m0 = cb / kTermsPer;
+                    load_tokens<kTermsPer>(trow + static_cast<uint32_t>(cb), v);   // its only share: accumulator 0
+                    for (int r = 1; r < p.cluster; ++r) {
+                        const float* part = recv + static_cast<size_t>(r - 1) * slot_floats + nl;
+#pragma unroll
+                        for (int i = 0; i < kTok; ++i)
+                            if (m0 + i < unit_tokens) v[i] += part[(m0 + i) * kTileN];
+                    }
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i)
+                        if (m0 + i < unit_tokens)
+                            p.c[(unit_row0 + m0 + i) * p.ldc + unit_n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+                }
+            }
+        }
+    }
+    if (clustered && (warp < 4 || warp >= 12)) {
+        __syncwarp();
+        cluster_wait();
+        cluster_sync();
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -942,16 +998,24 @@ mxfp4_stream_kernel(const StreamArgs p) {
 
 // ------------------------------------------------------------------------ plan and launches
 
-int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count, StreamPlan* out) {
+int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count,
+                     int (*clusters_of)(int), StreamPlan* out) {
     StreamPlan p = {};
     p.k_atoms = static_cast<int>((K + kAtomK - 1) / kAtomK);
     p.n_tiles = static_cast<int>((N + kTileN - 1) / kTileN);
     if (terms > 1) {
         p.m_tile = static_cast<int>(rows < 128 ? (rows + 15) / 16 * 16 : 128);
-        p.fused = rows <= FUSE_M * kTerms;
+        // Fused, every CTA expands the tokens of each of its steps itself: no launch before, and none of
+        // the host's 4 us for it, but 0.8 us a token and step of latency on eight warps. Two tokens:
+        // 2880 x 2040 5.9 against 5.5 us unfused on the device, 7168 x 7168 9.2 against 8.4; with the
+        // host's time 10 against 13.
+        p.fused = rows <= 2 * kTerms;
     } else {
         const int64_t mean = (rows + groups - 1) / groups;
-        p.fused = mean <= FUSE_MEAN;
+        // Fused: the tokens of a tile are quantized again for each of its weight tiles. 1 token, 8 of 64
+        // experts x 4096 x 2048: 12.0 us against 12.2 unfused and 4 us less of the host's time; 4 rows
+        // an expert cost 43.1 against 41.6 (gated 51.8 against 42.6).
+        p.fused = mean <= 2;
         p.m_tile = p.fused ? 32 : mean <= 48 ? 64 : mean <= 256 ? 128 : 192;
         // Groups of several tiles with short K: no waves, every CTA takes the tiles of a weight tile
         // one after the other and rereads its weights from L2, where all CTAs' fit (152 x 12 steps
@@ -960,22 +1024,41 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
         // same time, once from memory, but then wait for the same few weights together.
         p.runs = mean > 48 && p.k_atoms <= 12;
     }
-    p.min_steps = 4;
+    p.cluster = 1;
     p.nmc = (p.m_tile + 127) / 128;
     p.a_block = static_cast<uint32_t>(p.m_tile) * 128u + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
-    const size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 + 8 * kEpiStage +
+    size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 + 8 * kEpiStage +
                          2 * (static_cast<size_t>(groups) + 1) * 4;
-    p.stages = static_cast<int>((kSmemLimit - extra) / (kWBlock + p.a_block));
-    if (p.stages > kStreamMaxStages) p.stages = kStreamMaxStages;
-    p.smem_bytes = static_cast<size_t>(p.stages) * (kWBlock + p.a_block) + extra;
-    const uint32_t cols = 2u * p.m_tile + static_cast<uint32_t>(p.stages) * 8u * (1u + p.nmc);
-    if (p.stages < 2 || cols > 512u) return -1;
-    p.tmem_cols = 32;
-    while (p.tmem_cols < cols) p.tmem_cols <<= 1;
     const int64_t tiles = stream_tile_bound(rows, groups, p.m_tile);
     if (tiles * p.n_tiles > (int64_t(1) << 31) - 1) return -1;
-    const int64_t steps = tiles * p.n_tiles * static_cast<int64_t>(p.k_atoms);
-    p.ctas = static_cast<int>(steps < sm_count ? steps : sm_count);
+    // Weight-only, and units for less than half of the SMs: the CTAs of a cluster share a unit, as
+    // many as there are SMs for, each with two steps at least, and add their parts through the first
+    // one's shared memory. (Through the workspace, the same sums take 4 us more at the end.)
+    const int64_t all_units = terms > 1 ? static_cast<int64_t>(tiles_of(static_cast<int>(rows), p.m_tile)) * p.n_tiles : 0;
+    if (terms > 1) {
+        for (int s = kMaxStreamCluster; s > 1; --s)
+            if (2 * s <= p.k_atoms && all_units <= clusters_of(s)) {
+                p.cluster = s;
+                break;
+            }
+    }
+    const size_t recv = static_cast<size_t>(p.cluster - 1) * (p.m_tile / terms) * kTileN * sizeof(float);
+    extra += recv;
+    p.stages = static_cast<int>((kSmemLimit - extra) / (kWBlock + p.a_block));
+    if (p.stages > kStreamMaxStages) p.stages = kStreamMaxStages;
+    // no more stages than a CTA has steps: the next call's CTAs then fit beside this one's and ask for
+    // their weights while it ends
+    if (terms > 1 && (p.cluster > 1 || all_units <= sm_count)) {
+        const int per_cta = (p.k_atoms + p.cluster - 1) / p.cluster;
+        if (p.stages > per_cta) p.stages = per_cta;
+    }
+    p.smem_bytes = static_cast<size_t>(p.stages) * (kWBlock + p.a_block) + extra;
+    const uint32_t cols = 2u * p.m_tile + static_cast<uint32_t>(p.stages) * 8u * (1u + p.nmc);
+    if (p.stages < 1 || cols > 512u) return -1;
+    p.tmem_cols = 32;
+    while (p.tmem_cols < cols) p.tmem_cols <<= 1;
+    const int64_t steps = (terms > 1 ? all_units : tiles * p.n_tiles) * static_cast<int64_t>(p.k_atoms);
+    p.ctas = p.cluster > 1 ? static_cast<int>(all_units) * p.cluster : static_cast<int>(steps < sm_count ? steps : sm_count);
     const size_t blocks = p.fused ? 0 : static_cast<size_t>(tiles) * p.k_atoms * p.a_block;
     p.off_counters = (blocks + 1023) / 1024 * 1024;
     p.off_partial = p.off_counters + (static_cast<size_t>(p.ctas) * 8 + 1023) / 1024 * 1024;
@@ -1023,22 +1106,69 @@ cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx
 }
 
 template <int kTermsPer, bool kFused>
-static cudaError_t launch_stream_as(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {
+static cudaError_t allow_shared_memory() {
     static std::mutex mu;
     static std::atomic<bool> done[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!done[dev].load(std::memory_order_acquire)) {
-        std::lock_guard<std::mutex> lock(mu);
-        e = cudaFuncSetAttribute(mxfp4_stream_kernel<kTermsPer, kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(kSmemLimit));
-        if (e != cudaSuccess) return e;
-        done[dev].store(true, std::memory_order_release);
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    std::lock_guard<std::mutex> lock(mu);
+    e = cudaFuncSetAttribute(mxfp4_stream_kernel<kTermsPer, kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(kSmemLimit));
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+static cudaLaunchConfig_t stream_config(dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
+                                        cudaLaunchAttribute (&attr)[2]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cfg;
+}
+
+int stream_clusters(int size) {
+    static std::mutex mu;
+    static int known[64][kMaxStreamCluster + 1];   // clusters + 1, 0: not asked yet
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64 || size < 1 || size > kMaxStreamCluster) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    if (known[dev][size] == 0) {
+        int n = 0;
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = stream_config(dim3(size), dim3(kStreamThreads), kSmemLimit, nullptr, size, attr);
+        cfg.attrs = attr + 1;
+        cfg.numAttrs = 1;
+        if (allow_shared_memory<kTerms, false>() != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, mxfp4_stream_kernel<kTerms, false>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        known[dev][size] = n + 1;
     }
-    return launch_pdl(mxfp4_stream_kernel<kTermsPer, kFused>, dim3(plan.ctas), dim3(kFused ? kFusedThreads : kStreamThreads),
-                      plan.smem_bytes, s, args);
+    return known[dev][size] - 1;
+}
+
+template <int kTermsPer, bool kFused>
+static cudaError_t launch_stream_as(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {
+    const cudaError_t e = allow_shared_memory<kTermsPer, kFused>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = stream_config(dim3(plan.ctas), dim3(stream_threads(kTermsPer, kFused)),
+                                                 plan.smem_bytes, s, plan.cluster, attr);
+    return cudaLaunchKernelEx(&cfg, mxfp4_stream_kernel<kTermsPer, kFused>, args);
 }
 
 cudaError_t launch_stream(const StreamPlan& plan, const StreamArgs& args, int terms, cudaStream_t s) {

@@ -8,8 +8,11 @@ namespace mxfp4 {
 constexpr int kMaxGroups = 1024;          // groups (experts) one launch can address
 constexpr int kStreamThreads = 384;       // warps 0-3: copies, MMAs, two spare; warps 4-11: epilogue
 constexpr int kStreamEpiThreads = 256;
-constexpr int kFusedThreads = 512;        // warps 2, 3 and 12-15 write the tokens' stages
-constexpr int kTokenWarps = 6;
+// warps that write the tokens' stages in the fused kernels (2, 3 and from 12 on); expanding takes
+// three times as long as quantizing
+constexpr int token_warps(int terms) { return terms > 1 ? 8 : 6; }
+constexpr int stream_threads(int terms, bool fused) { return kStreamThreads + (fused ? 32 * (token_warps(terms) - 2) : 0); }
+constexpr int kSplitSteps = 8;            // 256-K steps that splitting a unit between CTAs has to save
 constexpr int kStreamMaxStages = 10;
 constexpr int kEpiStage = 640;            // bytes of shared memory an epilogue warp transposes through
 constexpr int kTerms = 8;                 // e2m1 terms an activation is expanded into (weight-only)
@@ -49,7 +52,7 @@ struct StreamArgs {
     int groups, rows, N;      // rows: token-block rows (grouped) or tokens * terms (weight-only)
     int m_tile, nmc, n_tiles, k_atoms, stages;
     int runs;                 // no waves of whole units (make_stream_plan)
-    int min_steps;            // fewest 256-K steps a split unit's share has
+    int cluster;              // CTAs that share a unit through their cluster (weight-only), or 1
     uint32_t a_block;
     uint32_t tmem_cols;
     int c_vec;                // C's rows are 16-byte aligned
@@ -57,15 +60,21 @@ struct StreamArgs {
 };
 
 struct StreamPlan {
-    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, min_steps, runs;
+    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, runs, cluster;
     int fused;                // tokens written by the product's own warps, no launch before it
     uint32_t a_block, tmem_cols;
     size_t smem_bytes;
     size_t off_counters, off_partial, ws_total;   // workspace: token blocks at 0
 };
 
-// Plan for `rows` token-block rows in `groups` groups; terms: 1 (grouped) or kTerms.
-int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count, StreamPlan* plan);
+constexpr int kMaxStreamCluster = 8;
+// Clusters of `size` stream CTAs that can be resident on the current device at once (0: unknown).
+int stream_clusters(int size);
+
+// Plan for `rows` token-block rows in `groups` groups; terms: 1 (grouped) or kTerms; clusters_of:
+// stream_clusters, or a model of it.
+int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count,
+                     int (*clusters_of)(int), StreamPlan* plan);
 
 // a [tokens, K] rows -> token blocks of the sorted rows: row r of the blocks is a[index ? index[r] : r].
 cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,
