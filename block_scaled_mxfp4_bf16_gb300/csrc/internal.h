@@ -174,8 +174,6 @@ struct DeviceInfo {
 };
 
 int device_info(DeviceInfo* out);   // MXFP4_OK or an error status
-int cuda_fail(cudaError_t e);        // records e for mxfp4_last_cuda_error, returns MXFP4_ERR_CUDA
-uint64_t wait_limit_ns();            // limit of every bounded wait
 // cluster_caps: if not null, cluster_caps[s] (s = 1..kMaxSplits) is how many clusters of s CTAs
 // can be resident at once, used instead of asking the current device (no CUDA call is made).
 // a_ready: the caller declared A ready (MXFP4_GEMM_A_READY), which can change the weight-resident

@@ -5,6 +5,10 @@
 
 namespace mxfp4 {
 
+// The C ABI's shared state (mxfp4_api.cu).
+int cuda_fail(cudaError_t e);             // records e for mxfp4_last_cuda_error, returns MXFP4_ERR_CUDA
+uint64_t wait_limit_ns();                 // limit of every bounded wait
+
 constexpr int kMaxGroups = 1024;          // groups (experts) one launch can address
 constexpr int kStreamThreads = 384;       // warps 0-3: copies, MMAs, two spare; warps 4-11: epilogue
 constexpr int kStreamEpiThreads = 256;
