@@ -51,6 +51,7 @@ int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8
     a.k_atoms = plan.k_atoms;
     a.stages = plan.stages;
     a.cluster = plan.cluster;
+    a.accs = plan.accs;
     a.runs = plan.runs;
     a.a_block = plan.a_block;
     a.tmem_cols = plan.tmem_cols;

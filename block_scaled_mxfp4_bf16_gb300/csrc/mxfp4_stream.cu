@@ -593,7 +593,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
     uint8_t* epi_stage = reinterpret_cast<uint8_t*>(warp_sum + 16);   // [8 warps][kEpiStage]
     int* prefix = reinterpret_cast<int*>(epi_stage + 8 * kEpiStage);  // [groups + 1] token tiles before a group
     int* begins = prefix + p.groups + 1;                              // [groups + 1] first rows of the groups
-    float* recv = reinterpret_cast<float*>(begins + p.groups + 1);    // [cluster - 1][tokens][128], first CTA of a cluster
+    float* recv = reinterpret_cast<float*>(begins + p.groups + 1);    // [cluster][tokens][128], first CTA of a cluster
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
@@ -656,6 +656,8 @@ mxfp4_stream_kernel(const StreamArgs p) {
     const int units = __syncthreads_or(bad ? 1 : 0) ? 0 : carry * p.n_tiles;
     const Walk start = begin_walk(p, prefix, units);
     const bool clustered = kTermsPer > 1 && p.cluster > 1;
+    int unit_n = 0, unit_tokens = 0;    // clustered: the unit's weight row of this lane, tokens and first one
+    int64_t unit_row0 = 0;
     if (clustered) cluster_arrive_relaxed();   // this CTA's shared memory may be written by its peers
     pdl_launch_dependents();
 
@@ -737,8 +739,8 @@ mxfp4_stream_kernel(const StreamArgs p) {
         {
             const uint32_t issue = elect_lane();
             const uint32_t mc = static_cast<uint32_t>(p.nmc);
-            // columns: two accumulators, weight scales (8 per stage), token scales (8 nmc per stage)
-            const uint32_t t_sfw0 = tmem + 2u * static_cast<uint32_t>(p.m_tile);
+            // columns: the accumulators, weight scales (8 per stage), token scales (8 nmc per stage)
+            const uint32_t t_sfw0 = tmem + static_cast<uint32_t>(p.accs * p.m_tile);
             const uint32_t t_sft0 = t_sfw0 + 8u * static_cast<uint32_t>(p.stages);
             const uint64_t w_desc0 = desc_sw128(smem_addr(sW));
             const uint64_t t_desc0 = desc_sw128(smem_addr(sT));
@@ -844,8 +846,6 @@ mxfp4_stream_kernel(const StreamArgs p) {
         const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;
         Walk u = start;
         int nshare = 0;
-        int unit_n = 0, unit_tokens = 0;
-        int64_t unit_row0 = 0;
         while (next_share(p, prefix, u)) {
             const int b = nshare & 1;
             const bool got = mbar_wait(&acc_full[b], (nshare >> 1) & 1, lim);
@@ -865,17 +865,15 @@ mxfp4_stream_kernel(const StreamArgs p) {
                 const uint32_t rank = blockIdx.x % p.cluster;
                 __syncwarp();
                 cluster_wait();    // the first CTA runs
-                if (rank != 0u) {
-                    const uint32_t to = map_to_rank(smem_addr(recv), 0u) +
-                                        (rank - 1u) * static_cast<uint32_t>(slot_floats) * 4u + static_cast<uint32_t>(nl) * 4u;
-                    for (int cb = half * 16; cb < u.rows; cb += 32) {
-                        float v[kTok];
-                        load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
-                        const int m0 = cb / kTermsPer;
+                const uint32_t to = map_to_rank(smem_addr(recv), 0u) + rank * static_cast<uint32_t>(slot_floats) * 4u +
+                                    static_cast<uint32_t>(nl) * 4u;
+                for (int cb = half * 16; cb < u.rows; cb += 32) {
+                    float v[kTok];
+                    load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
+                    const int m0 = cb / kTermsPer;
 #pragma unroll
-                        for (int i = 0; i < kTok; ++i)
-                            if (m0 + i < tokens) st_cluster_f32(to + static_cast<uint32_t>(m0 + i) * (kTileN * 4u), v[i]);
-                    }
+                    for (int i = 0; i < kTok; ++i)
+                        if (m0 + i < tokens) st_cluster_f32(to + static_cast<uint32_t>(m0 + i) * (kTileN * 4u), v[i]);
                 }
             } else if (kTermsPer == 1 && u.split < 0) {
                 store_tile(p, acc, u.rows, u.row0, u.nt * kTileN + (warp & 3) * 32, half, lane,
@@ -960,39 +958,31 @@ mxfp4_stream_kernel(const StreamArgs p) {
             if (lane == 0) mbar_arrive(&acc_empty[b]);
             ++nshare;
         }
-        if (clustered) {
-            if (nshare == 0) cluster_wait();   // failed, or no share: the handshake all the same
-            __syncwarp();
-            cluster_sync();
-            if (blockIdx.x % p.cluster == 0u && nshare != 0 && *abort_flag == 0u && unit_n < p.N) {
-                for (int cb = half * 16; cb < unit_tokens * kTermsPer; cb += 32) {
-                    float v[kTok];
-                    const int m0 = cb / kTermsPer;
-                    load_tokens<kTermsPer>(trow + static_cast<uint32_t>(cb), v);   // its only share: accumulator 0
-                    for (int r = 1; r < p.cluster; ++r) {
-                        const float* part = recv + static_cast<size_t>(r - 1) * slot_floats + nl;
-#pragma unroll
-                        for (int i = 0; i < kTok; ++i)
-                            if (m0 + i < unit_tokens) v[i] += part[(m0 + i) * kTileN];
-                    }
-#pragma unroll
-                    for (int i = 0; i < kTok; ++i)
-                        if (m0 + i < unit_tokens)
-                            p.c[(unit_row0 + m0 + i) * p.ldc + unit_n] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
-                }
-            }
-        }
+        if (clustered && nshare == 0) cluster_wait();   // failed: the handshake all the same
     }
     if (clustered && (warp < 4 || warp >= 12)) {
         __syncwarp();
         cluster_wait();
-        cluster_sync();
     }
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(*tmem_slot, p.tmem_cols);
+    }
+    if (clustered) {
+        // No CTA holds tensor memory while it waits for the others, which may still wait for theirs.
+        __syncwarp();
+        cluster_sync();
+        if (blockIdx.x % p.cluster == 0u && warp >= 4 && warp < 12 && unit_n < p.N && *abort_flag == 0u) {
+            const int first = (warp - 4) >> 2, nl = (warp & 3) * 32 + lane;
+            const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;
+            for (int m = first; m < unit_tokens; m += 2) {   // the parts in the order of K
+                float v = 0.f;
+                for (int r = 0; r < p.cluster; ++r) v += recv[r * slot_floats + static_cast<size_t>(m) * kTileN + nl];
+                p.c[(unit_row0 + m) * p.ldc + unit_n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+            }
+        }
     }
 }
 
@@ -1042,23 +1032,29 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
                 break;
             }
     }
-    const size_t recv = static_cast<size_t>(p.cluster - 1) * (p.m_tile / terms) * kTileN * sizeof(float);
+    const size_t recv = static_cast<size_t>(p.cluster > 1 ? p.cluster : 0) * (p.m_tile / terms) * kTileN * sizeof(float);
     extra += recv;
     p.stages = static_cast<int>((kSmemLimit - extra) / (kWBlock + p.a_block));
     if (p.stages > kStreamMaxStages) p.stages = kStreamMaxStages;
-    // no more stages than a CTA has steps: the next call's CTAs then fit beside this one's and ask for
-    // their weights while it ends
-    if (terms > 1 && (p.cluster > 1 || all_units <= sm_count)) {
-        const int per_cta = (p.k_atoms + p.cluster - 1) / p.cluster;
-        if (p.stages > per_cta) p.stages = per_cta;
-    }
+    // One share per CTA: one accumulator, and no more stages than it has steps, so that the next call's
+    // CTAs fit beside this one's and ask for their weights while it ends.
+    const int64_t steps = (terms > 1 ? all_units : tiles * p.n_tiles) * static_cast<int64_t>(p.k_atoms);
+    p.ctas = p.cluster > 1 ? static_cast<int>(all_units) * p.cluster : static_cast<int>(steps < sm_count ? steps : sm_count);
+    const bool whole = all_units <= p.ctas && (steps + p.ctas - 1) / p.ctas + kSplitSteps > p.k_atoms;   // as begin_walk
+    const bool one_share = terms > 1 && (p.cluster > 1 || whole);
+    p.accs = one_share ? 1 : 2;
+    const int per_cta = (p.k_atoms + p.cluster - 1) / p.cluster;
+    if (one_share && p.stages > per_cta) p.stages = per_cta;
     p.smem_bytes = static_cast<size_t>(p.stages) * (kWBlock + p.a_block) + extra;
-    const uint32_t cols = 2u * p.m_tile + static_cast<uint32_t>(p.stages) * 8u * (1u + p.nmc);
+    const uint32_t cols = static_cast<uint32_t>(p.accs * p.m_tile) + static_cast<uint32_t>(p.stages) * 8u * (1u + p.nmc);
     if (p.stages < 1 || cols > 512u) return -1;
     p.tmem_cols = 32;
     while (p.tmem_cols < cols) p.tmem_cols <<= 1;
-    const int64_t steps = (terms > 1 ? all_units : tiles * p.n_tiles) * static_cast<int64_t>(p.k_atoms);
-    p.ctas = p.cluster > 1 ? static_cast<int>(all_units) * p.cluster : static_cast<int>(steps < sm_count ? steps : sm_count);
+    // A CTA takes at least as large a part of the SM's shared memory as of its tensor memory: CTAs that
+    // are resident together then always have their columns, and none waits for another's end.
+    const size_t sm_smem = 233472, part = sm_smem * p.tmem_cols / 512 - 1024;   // 1 KB is the system's, per CTA
+    if (p.smem_bytes < part) p.smem_bytes = part;
+    if (p.smem_bytes > kSmemLimit) return -1;
     const size_t blocks = p.fused ? 0 : static_cast<size_t>(tiles) * p.k_atoms * p.a_block;
     p.off_counters = (blocks + 1023) / 1024 * 1024;
     p.off_partial = p.off_counters + (static_cast<size_t>(p.ctas) * 8 + 1023) / 1024 * 1024;

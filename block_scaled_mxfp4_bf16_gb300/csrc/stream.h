@@ -56,6 +56,7 @@ struct StreamArgs {
     int groups, rows, N;      // rows: token-block rows (grouped) or tokens * terms (weight-only)
     int m_tile, nmc, n_tiles, k_atoms, stages;
     int runs;                 // no waves of whole units (make_stream_plan)
+    int accs;                 // accumulators in tensor memory: 2, or 1 for CTAs with one share
     int cluster;              // CTAs that share a unit through their cluster (weight-only), or 1
     uint32_t a_block;
     uint32_t tmem_cols;
@@ -64,7 +65,7 @@ struct StreamArgs {
 };
 
 struct StreamPlan {
-    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, runs, cluster;
+    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, runs, cluster, accs;
     int fused;                // tokens written by the product's own warps, no launch before it
     uint32_t a_block, tmem_cols;
     size_t smem_bytes;
