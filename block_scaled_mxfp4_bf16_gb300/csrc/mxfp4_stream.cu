@@ -1050,9 +1050,12 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     if (p.stages < 1 || cols > 512u) return -1;
     p.tmem_cols = 32;
     while (p.tmem_cols < cols) p.tmem_cols <<= 1;
-    // A CTA takes at least as large a part of the SM's shared memory as of its tensor memory: CTAs that
-    // are resident together then always have their columns, and none waits for another's end.
-    const size_t sm_smem = 233472, part = sm_smem * p.tmem_cols / 512 - 1024;   // 1 KB is the system's, per CTA
+    // A CTA takes at least as large a part of the SM's shared memory as of its tensor memory, less 2 KB:
+    // CTAs that are resident together then always have their columns, and none waits for another's end
+    // (five such CTAs fill the SM's threads, and 5 x 2 KB are worth less than the smallest 32 columns).
+    // The 2 KB let the next call's token writer start beside a CTA that has it all otherwise
+    // (16x20000x2048 13.8 us without, 9.1 with).
+    const size_t sm_smem = 233472, part = sm_smem * p.tmem_cols / 512 - 1024 - 2048;   // 1 KB is the system's, per CTA
     if (p.smem_bytes < part) p.smem_bytes = part;
     if (p.smem_bytes > kSmemLimit) return -1;
     const size_t blocks = p.fused ? 0 : static_cast<size_t>(tiles) * p.k_atoms * p.a_block;
