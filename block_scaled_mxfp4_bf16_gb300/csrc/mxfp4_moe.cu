@@ -371,6 +371,19 @@ cudaError_t launch_route(const RouteArgs& args, cudaStream_t s) {
 // of j; a slot outside [0, rows) adds nothing. Bound by the bytes of y: the slots of eight j are
 // read together, then all their rows' pieces are in flight before the first is added.
 template <int kVec>
+struct PieceOf;
+template <>
+struct PieceOf<8> { using type = uint4; };
+template <>
+struct PieceOf<4> { using type = uint2; };
+template <>
+struct PieceOf<2> { using type = unsigned int; };
+template <>
+struct PieceOf<1> { using type = unsigned short; };
+template <int kVec>
+using Piece = typename PieceOf<kVec>::type;   // kVec bf16 values
+
+template <int kVec>
 __global__ void __launch_bounds__(256)
 combine_kernel(const uint16_t* __restrict__ y, int64_t rows, int64_t ldy, const int32_t* __restrict__ slots,
                const float* __restrict__ weights, int64_t T, int k, int vecs, uint16_t* __restrict__ out, int64_t ldo) {
@@ -392,57 +405,38 @@ combine_kernel(const uint16_t* __restrict__ y, int64_t rows, int64_t ldy, const 
                 slot[u] = j0 + u < k ? slots[t * k + j0 + u] : -1;
                 w[u] = j0 + u < k ? weights[t * k + j0 + u] : 0.f;
             }
-            if constexpr (kVec == 8) {
-                uint4 v[kFlight];
+            Piece<kVec> v[kFlight];
 #pragma unroll
-                for (int u = 0; u < kFlight; ++u)
-                    if (slot[u] >= 0 && slot[u] < rows)
-                        v[u] = __ldcs(reinterpret_cast<const uint4*>(y + slot[u] * ldy + n));
+            for (int u = 0; u < kFlight; ++u)
+                if (slot[u] >= 0 && slot[u] < rows) v[u] = __ldcs(reinterpret_cast<const Piece<kVec>*>(y + slot[u] * ldy + n));
 #pragma unroll
-                for (int u = 0; u < kFlight; ++u)
-                    if (slot[u] >= 0 && slot[u] < rows) {
-                        const uint32_t words[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            for (int u = 0; u < kFlight; ++u)
+                if (slot[u] >= 0 && slot[u] < rows) {
+                    const uint16_t* e = reinterpret_cast<const uint16_t*>(&v[u]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            acc[2 * i] = fmaf(w[u], __uint_as_float(words[i] << 16), acc[2 * i]);
-                            acc[2 * i + 1] = fmaf(w[u], __uint_as_float(words[i] & 0xFFFF0000u), acc[2 * i + 1]);
-                        }
-                    }
-            } else {
-                uint16_t v[kFlight];
-#pragma unroll
-                for (int u = 0; u < kFlight; ++u)
-                    if (slot[u] >= 0 && slot[u] < rows) v[u] = y[slot[u] * ldy + n];
-#pragma unroll
-                for (int u = 0; u < kFlight; ++u)
-                    if (slot[u] >= 0 && slot[u] < rows)
-                        acc[0] = fmaf(w[u], __uint_as_float(static_cast<uint32_t>(v[u]) << 16), acc[0]);
-            }
+                    for (int i = 0; i < kVec; ++i)
+                        acc[i] = fmaf(w[u], __uint_as_float(static_cast<uint32_t>(e[i]) << 16), acc[i]);
+                }
         }
-        uint16_t* dst = out + t * ldo + n;
-        if constexpr (kVec == 8) {
-            uint32_t words[4];
+        Piece<kVec> o;
+        uint16_t* e = reinterpret_cast<uint16_t*>(&o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
-                words[i] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            __stcs(reinterpret_cast<uint4*>(dst), make_uint4(words[0], words[1], words[2], words[3]));
-        } else {
-            dst[0] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[0]));
-        }
+        for (int i = 0; i < kVec; ++i) e[i] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i]));
+        __stcs(reinterpret_cast<Piece<kVec>*>(out + t * ldo + n), o);
     }
 }
 
 cudaError_t launch_combine(const uint16_t* y, int64_t rows, int64_t ldy, const int32_t* slots, const float* weights,
                            int64_t T, int k, int64_t N, uint16_t* out, int64_t ldo, cudaStream_t s) {
-    const bool vec = N % 8 == 0 && ldy % 8 == 0 && ldo % 8 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(out) % 16 == 0;
-    const int vecs = static_cast<int>(vec ? N / 8 : N);
+    // the widest pieces that both matrices' rows are aligned to
+    const uintptr_t at = reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out);
+    const int64_t step = N | ldy | ldo;
+    const int vec = at % 16 == 0 && step % 8 == 0 ? 8 : at % 8 == 0 && step % 4 == 0 ? 4 : at % 4 == 0 && step % 2 == 0 ? 2 : 1;
+    const int vecs = static_cast<int>(N / vec);
     const int64_t blocks = (T * vecs + 255) / 256;
     const dim3 grid(static_cast<unsigned>(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF));
-    return launch_pdl(vec ? combine_kernel<8> : combine_kernel<1>, grid, dim3(256), 0, s, y, rows, ldy, slots, weights, T, k,
-                      vecs, out, ldo);
+    auto* kernel = vec == 8 ? combine_kernel<8> : vec == 4 ? combine_kernel<4> : vec == 2 ? combine_kernel<2> : combine_kernel<1>;
+    return launch_pdl(kernel, grid, dim3(256), 0, s, y, rows, ldy, slots, weights, T, k, vecs, out, ldo);
 }
 
 }  // namespace mxfp4

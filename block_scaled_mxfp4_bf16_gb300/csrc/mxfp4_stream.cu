@@ -373,11 +373,16 @@ __device__ __forceinline__ void locate(const StreamArgs& p, const int* prefix, i
 __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefix, int units) {
     Walk w = {};
     w.units = units;
-    w.waves = p.runs ? 0 : units / static_cast<int>(gridDim.x);
+    const bool runs = p.runs && units >= 4 * static_cast<int>(gridDim.x);
+    w.waves = runs ? 0 : units / static_cast<int>(gridDim.x);
     const int64_t steps = static_cast<int64_t>(units - w.waves * static_cast<int>(gridDim.x)) * p.k_atoms;
     w.share = (steps + gridDim.x - 1) / gridDim.x;
-    // a split unit costs what eight steps do (4 us: sums out, arrival, sums in): not for less
-    if (!p.runs && w.share + kSplitSteps > p.k_atoms) w.share = p.k_atoms;
+    // a split unit costs what eight steps do (4 us: sums out, arrival, sums in): not for less, and
+    // not among more than six CTAs
+    if (!runs) {
+        w.share = max(w.share, static_cast<int64_t>((p.k_atoms + 5) / 6));
+        if (w.share + kSplitSteps > p.k_atoms) w.share = p.k_atoms;
+    }
     w.s = min(steps, w.share * blockIdx.x);
     w.s1 = min(steps, w.s + w.share);
     if (p.cluster > 1) {   // the CTAs of a cluster share one unit
@@ -462,15 +467,19 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 
 // A whole unit's accumulator (lane = weight row, column = token) -> bf16 C. A warp owns 32 weight
 // rows; per 8 tokens it packs its fragments, transposes them through 640 bytes of shared memory
-// (rows of 64 bytes, 80 apart) and stores 16 bytes a lane: one store instruction writes 64
-// contiguous bytes of each of 8 rows of C. (One column of 32 2-byte values per store measured
-// the same in waves, 3 % slower in runs.)
+// (rows of 64 bytes, 80 apart) and stores kVec elements a lane, the widest that C's rows are aligned
+// to: one instruction writes 64 contiguous bytes of each of kVec rows of C. (16-byte stores and one
+// column of 2-byte stores per token measured the same in waves; for rows that are not aligned,
+// 2-byte stores of 16-byte pieces took four times as long as whole rows of 64 bytes.)
+template <int kVec>
 __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, int rows, int64_t row0, int n0, int half,
                                            int lane, uint8_t* stage) {
+    constexpr int kLanes = 32 / kVec;              // lanes per row of C
     const uint32_t st = smem_addr(stage);
     const uint32_t put = st + static_cast<uint32_t>((lane & 7) * 80 + (lane >> 3) * 16);
-    const uint32_t got = st + static_cast<uint32_t>((lane >> 2) * 80 + (lane & 3) * 16);
-    const int n = n0 + (lane & 3) * 8;
+    const int r0 = lane / kLanes, n = n0 + (lane % kLanes) * kVec;
+    const uint8_t* got = stage + r0 * 80 + (lane % kLanes) * (2 * kVec);
+    const bool whole = n + kVec <= p.N;
     for (int cb = half * 32; cb < rows; cb += 64) {
         uint32_t lo[16], hi[16];
         tmem_load_frag32(trow + static_cast<uint32_t>(cb), lo);
@@ -485,18 +494,18 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
                                   pack_bf16x2(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
                                   pack_bf16x2(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])));
                 __syncwarp();
-                uint4 v;
-                asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(got) : "memory");
-                const int m = cb + 8 * i + (lane >> 2);
-                if (m < rows && n < p.N) {
-                    uint16_t* cp = p.c + (row0 + m) * p.ldc + n;
-                    if (p.c_vec && n + 8 <= p.N) {
-                        *reinterpret_cast<uint4*>(cp) = v;
-                    } else {
-                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (n + k < p.N) cp[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+                for (int q = 0; q < 8; q += kVec) {
+                    const int m = cb + 8 * i + q + r0;
+                    uint16_t* cp = p.c + (row0 + m) * p.ldc + n;
+                    const uint8_t* from = got + q * 80;
+                    if (m < rows && whole) {
+                        if constexpr (kVec == 8) *reinterpret_cast<uint4*>(cp) = *reinterpret_cast<const uint4*>(from);
+                        else if constexpr (kVec == 4) *reinterpret_cast<uint2*>(cp) = *reinterpret_cast<const uint2*>(from);
+                        else if constexpr (kVec == 2) *reinterpret_cast<uint32_t*>(cp) = *reinterpret_cast<const uint32_t*>(from);
+                        else *cp = *reinterpret_cast<const uint16_t*>(from);
+                    } else if (kVec > 1 && m < rows) {
+                        for (int k = 0; n + k < p.N; ++k) cp[k] = reinterpret_cast<const uint16_t*>(from)[k];
                     }
                 }
             }
@@ -876,8 +885,12 @@ mxfp4_stream_kernel(const StreamArgs p) {
                         if (m0 + i < tokens) st_cluster_f32(to + static_cast<uint32_t>(m0 + i) * (kTileN * 4u), v[i]);
                 }
             } else if (kTermsPer == 1 && u.split < 0) {
-                store_tile(p, acc, u.rows, u.row0, u.nt * kTileN + (warp & 3) * 32, half, lane,
-                           epi_stage + (warp - 4) * kEpiStage);
+                const int n0 = u.nt * kTileN + (warp & 3) * 32;
+                uint8_t* stage = epi_stage + (warp - 4) * kEpiStage;
+                if (p.c_vec == 8) store_tile<8>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+                else if (p.c_vec == 4) store_tile<4>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+                else if (p.c_vec == 2) store_tile<2>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+                else store_tile<1>(p, acc, u.rows, u.row0, n0, half, lane, stage);
             } else {
                 // A unit of several CTAs: each but the last to arrive leaves its sums in its slot of
                 // the workspace (slot 0 for the unit its run begins in, slot 1 for one it reaches
@@ -928,18 +941,26 @@ mxfp4_stream_kernel(const StreamArgs p) {
                         } else {
 #pragma unroll
                             for (int i = 0; i < kTok; ++i) v[i] = 0.f;
-                            for (int64_t c = c_first; c <= c_last; ++c) {
-                                // the unit is the first of c's run unless the run began before it
-                                const float* src = p.partial + (static_cast<size_t>(c) * 2 + (c * u.share < unit_step ? 1 : 0)) *
-                                                                   slot_floats;
-                                float theirs[kTok];
-                                if (c != static_cast<int64_t>(blockIdx.x)) {   // all loads in flight before the first is added
+                            // two CTAs' sums are on their way at a time, added in the order of K
+                            for (int64_t c0 = c_first; c0 <= c_last; c0 += 2) {
+                                float theirs[2][kTok];
+#pragma unroll
+                                for (int q = 0; q < 2; ++q) {
+                                    const int64_t c = c0 + q;
+                                    if (c > c_last || c == blockIdx.x) continue;
+                                    // the unit is the first of c's run unless the run began before it
+                                    const float* src = p.partial + (static_cast<size_t>(c) * 2 + (c * u.share < unit_step ? 1 : 0)) *
+                                                                       slot_floats;
 #pragma unroll
                                     for (int i = 0; i < kTok; ++i)
-                                        theirs[i] = m0 + i < tokens ? __ldcg(src + static_cast<size_t>(m0 + i) * kTileN + nl) : 0.f;
+                                        theirs[q][i] = m0 + i < tokens ? __ldcg(src + static_cast<size_t>(m0 + i) * kTileN + nl) : 0.f;
                                 }
 #pragma unroll
-                                for (int i = 0; i < kTok; ++i) v[i] += c == static_cast<int64_t>(blockIdx.x) ? own[i] : theirs[i];
+                                for (int q = 0; q < 2; ++q) {
+                                    if (c0 + q > c_last) continue;
+#pragma unroll
+                                    for (int i = 0; i < kTok; ++i) v[i] += c0 + q == blockIdx.x ? own[i] : theirs[q][i];
+                                }
                             }
                         }
                         if (n < p.N) {
@@ -1040,7 +1061,9 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     // CTAs fit beside this one's and ask for their weights while it ends.
     const int64_t steps = (terms > 1 ? all_units : tiles * p.n_tiles) * static_cast<int64_t>(p.k_atoms);
     p.ctas = p.cluster > 1 ? static_cast<int>(all_units) * p.cluster : static_cast<int>(steps < sm_count ? steps : sm_count);
-    const bool whole = all_units <= p.ctas && (steps + p.ctas - 1) / p.ctas + kSplitSteps > p.k_atoms;   // as begin_walk
+    int64_t share = (steps + p.ctas - 1) / p.ctas;                                      // as begin_walk
+    if (share < (p.k_atoms + 5) / 6) share = (p.k_atoms + 5) / 6;
+    const bool whole = all_units <= p.ctas && share + kSplitSteps > p.k_atoms;
     const bool one_share = terms > 1 && (p.cluster > 1 || whole);
     p.accs = one_share ? 1 : 2;
     const int per_cta = (p.k_atoms + p.cluster - 1) / p.cluster;

@@ -55,12 +55,12 @@ struct StreamArgs {
     uint32_t* status;
     int groups, rows, N;      // rows: token-block rows (grouped) or tokens * terms (weight-only)
     int m_tile, nmc, n_tiles, k_atoms, stages;
-    int runs;                 // no waves of whole units (make_stream_plan)
+    int runs;                 // no waves of whole units where units are many (make_stream_plan)
     int accs;                 // accumulators in tensor memory: 2, or 1 for CTAs with one share
     int cluster;              // CTAs that share a unit through their cluster (weight-only), or 1
     uint32_t a_block;
     uint32_t tmem_cols;
-    int c_vec;                // C's rows are 16-byte aligned
+    int c_vec;                // elements of the widest stores C's rows are aligned to: 8, 4, 2 or 1
     uint64_t wait_limit_ns;
 };
 

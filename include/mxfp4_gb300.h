@@ -533,7 +533,7 @@ int mxfp4_moe_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t
  *             weight is not used. A token without any gets zeros.
  *   weights : device fp32 [T, k].
  *   out     : bf16 [T, N], row stride ldo (ldo >= N), 2-byte aligned.
- * Rows of 16-byte aligned, 8-element multiples move in 16-byte pieces, others by elements.
+ * Rows move in pieces of the widest of 16, 8, 4 and 2 bytes that N and both matrices are aligned to.
  * T == 0 or N == 0 is a no-op.
  */
 int mxfp4_moe_combine(const void *y, int64_t R, int64_t N, int64_t ldy, const int32_t *slots, const float *weights,

@@ -208,6 +208,7 @@ def test_tiles_cover_every_group_and_their_slots_are_distinct(tmp_path):
 
 
 PLAN_HARNESS = r"""
+#include <algorithm>
 #include <cstdio>
 #include <random>
 #include "stream.h"
@@ -239,7 +240,8 @@ int main() {
         else CHECK(p.ctas >= 1 && p.ctas <= 152);
         if (p.accs == 1 && p.cluster == 1) {   // every CTA really has one share: whole units, one each
             const int64_t units = (int64_t)tiles_of((int)rows, p.m_tile) * p.n_tiles, steps = units * p.k_atoms;
-            CHECK(units <= p.ctas && (units == p.ctas || (steps + p.ctas - 1) / p.ctas + kSplitSteps > p.k_atoms));
+            const int64_t share = std::max<int64_t>((steps + p.ctas - 1) / p.ctas, (p.k_atoms + 5) / 6);
+            CHECK(units <= p.ctas && (units == p.ctas || share + kSplitSteps > p.k_atoms));
         }
         // the fused kernels keep a row index per lane
         if (p.fused && terms == 1) CHECK(p.m_tile <= 32);
