@@ -11,6 +11,9 @@ namespace {
 
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWarps = kRouteThreads / 32;
+constexpr int kTopkThreads = 128;
+constexpr int kRouteSmall = kRouteWarps;    // tokens of a call in one CTA
+constexpr int kRouteRecount = 32768;        // token-expert pairs that every scatter CTA counts itself
 constexpr int kSub = 128;                   // tokens ranked at a time by one bit mask per expert
 constexpr int kSubWords = kSub / 32;
 
@@ -65,7 +68,7 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[kPer]) {
 // bf16 logits: a key is the 16 ordered bits of the logit above 0xFFFF - expert, so all keys differ,
 // the largest is the one with the lowest index and the expert is read off it. fp32 logits: a key
 // has no room for the index. It is looked up at the end, in the winning lane's unsorted keys; where
-// two lanes share a winning key, the token is done again in rounds that compare the indexes too.
+// a winning key comes twice, the token is done again in rounds that compare the indexes too.
 // Bound by instructions: about 300 a token and warp for 256 experts and k = 8 (rounds that search
 // all of a lane's keys took 650).
 template <int kPer, bool kBf16>
@@ -86,9 +89,8 @@ __device__ __forceinline__ void top_k(const RouteArgs& p, int t, int lane, uint3
             key[i] = logit[i];
     }
     sort_keys<kPer>(key);
-    uint32_t mine = 0u, top = 0u, tied = 0u;
-    int from = 0, nth = 0, last_from = -1, last_nth = 0;
-    uint32_t last = 0u;
+    uint32_t mine = 0u, top = 0u, tied = 0u, last = 0u;
+    int from = 0;
     for (int j = 0; j < p.k; ++j) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, key[0]);
         if (m == 0u) break;                       // fewer than k experts left
@@ -97,16 +99,11 @@ __device__ __forceinline__ void top_k(const RouteArgs& p, int t, int lane, uint3
         if constexpr (!kBf16) {
             const uint32_t who = __ballot_sync(0xffffffffu, win);
             tied |= who & (who - 1u);
-            const int w = __ffs(who) - 1;
-            last_nth = m == last && w == last_from ? last_nth + 1 : 0;   // an equal key of the same lane
+            if (m == last) tied = 1u;
             last = m;
-            last_from = w;
+            if (lane == j) from = __ffs(who) - 1;
         }
-        if (lane == j) {
-            mine = m;
-            from = last_from;
-            nth = last_nth;
-        }
+        if (lane == j) mine = m;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) key[i] = win ? (i + 1 < kPer ? key[i + 1] : 0u) : key[i];
     }
@@ -119,9 +116,9 @@ __device__ __forceinline__ void top_k(const RouteArgs& p, int t, int lane, uint3
         top = bf16_logit_key(top);
     } else if (tied == 0u) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const uint32_t v = __shfl_sync(0xffffffffu, logit[i], from & 31);
-            if (mine && v == mine && nth-- == 0) mine_e = from + 32 * i;
+        for (int i = kPer - 1; i >= 0; --i) {     // the lowest of the lane's that have it: found last
+            const uint32_t v = __shfl_sync(0xffffffffu, logit[i], from);
+            if (v == mine) mine_e = from + 32 * i;
         }
     } else {
         uint32_t left[kPer];
@@ -149,6 +146,7 @@ __device__ __forceinline__ void top_k(const RouteArgs& p, int t, int lane, uint3
             }
         }
     }
+    if (mine == 0u) mine_e = -1;
     float w = mine ? exp_below(key_logit(mine), key_logit(top)) : 0.f;
     float total = w;
     if (!p.renormalize) {                         // softmax over all of the token's experts
@@ -200,14 +198,11 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sum, int* total) {
     return t - v + (warp ? warp_sum[warp - 1] : 0);
 }
 
-// Top-k of a chunk of tokens, a warp per token; count[e] (shared): the chunk's tokens of expert e.
+// Top-k of tokens [t0, t1), a warp of the block each; count (if not null): += the tokens of each expert.
 template <bool kBf16>
-__device__ __forceinline__ void chunk_top_k(const RouteArgs& p, int chunk, int* count) {
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) count[e] = 0;
-    __syncthreads();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t1 = min(p.T, (chunk + 1) * p.chunk);
-    for (int t = chunk * p.chunk + warp; t < t1; t += kRouteWarps) {
+__device__ __forceinline__ void top_k_tokens(const RouteArgs& p, int t0, int t1, int* count) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = static_cast<int>(blockDim.x) >> 5;
+    for (int t = t0 + warp; t < t1; t += warps) {
         uint32_t key;
         int e;
         float w;
@@ -215,10 +210,9 @@ __device__ __forceinline__ void chunk_top_k(const RouteArgs& p, int chunk, int* 
         if (lane < p.k) {
             p.weights[static_cast<int64_t>(t) * p.k + lane] = w;
             p.experts[static_cast<int64_t>(t) * p.k + lane] = e;
-            if (e >= 0) atomicAdd(&count[e], 1);
+            if (count && e >= 0) atomicAdd(&count[e], 1);
         }
     }
-    __syncthreads();
 }
 
 // Rows, slots and (chunk 0) offsets of a chunk. all, before: over all chunks and over those before
@@ -276,7 +270,7 @@ __device__ __forceinline__ void chunk_scatter(const RouteArgs& p, int chunk, int
 
 }  // namespace
 
-// All of a small call in one CTA.
+// Few tokens (kRouteSmall): all of the call in one CTA, a token per warp.
 template <bool kBf16>
 __global__ void __launch_bounds__(kRouteThreads)
 route_small_kernel(const RouteArgs p) {
@@ -284,58 +278,102 @@ route_small_kernel(const RouteArgs p) {
     uint32_t* mask = reinterpret_cast<uint32_t*>(count + p.E);       // [E][kSubWords]
     __shared__ int warp_sum[kRouteWarps];
     pdl_launch_dependents();
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) count[e] = 0;
     pdl_wait_prior_grid();
-    chunk_top_k<kBf16>(p, 0, count);
+    __syncthreads();
+    top_k_tokens<kBf16>(p, 0, p.T, count);
+    __syncthreads();
     const int all = static_cast<int>(threadIdx.x) < p.E ? count[threadIdx.x] : 0;
     chunk_scatter(p, 0, all, 0, count, mask, warp_sum);
 }
 
-// Top-k of every chunk, and the chunks' counts of every expert, which is what the scatter kernel
-// needs to know where each chunk's rows go.
+// Top-k alone, in blocks of a few warps, so that the tokens spread over the SMs (a token is some
+// hundred instructions of one warp).
 template <bool kBf16>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kTopkThreads)
 route_topk_kernel(const RouteArgs p) {
-    extern __shared__ int count[];   // [E]
     pdl_launch_dependents();
     pdl_wait_prior_grid();
-    chunk_top_k<kBf16>(p, static_cast<int>(blockIdx.x), count);
-    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) p.hist[static_cast<int64_t>(blockIdx.x) * p.E + e] = count[e];
+    const int t0 = static_cast<int>(blockIdx.x) * (kTopkThreads / 32);
+    top_k_tokens<kBf16>(p, t0, min(p.T, t0 + kTopkThreads / 32), nullptr);
 }
 
-// The counts are summed by the whole block, every thread an expert of some of the chunks, all its
-// loads in flight (one thread per expert and one load after the other took 10 us for 128 chunks).
+// Many tokens: top-k of every chunk, and the chunks' counts of every expert, which is what the scatter
+// kernel needs to know where each chunk's rows go.
+template <bool kBf16>
+__global__ void __launch_bounds__(kRouteThreads)
+route_topk_count_kernel(const RouteArgs p) {
+    extern __shared__ int count[];   // [E]
+    pdl_launch_dependents();
+    for (int e = threadIdx.x; e < p.E; e += kRouteThreads) count[e] = 0;
+    pdl_wait_prior_grid();
+    __syncthreads();
+    const int t0 = static_cast<int>(blockIdx.x) * p.chunk;
+    top_k_tokens<kBf16>(p, t0, min(p.T, t0 + p.chunk), count);
+    __syncthreads();
+    const int pairs = (p.E + 1) / 2;
+    for (int i = threadIdx.x; i < pairs; i += kRouteThreads) {
+        const uint32_t lo = static_cast<uint32_t>(count[2 * i]), hi = 2 * i + 1 < p.E ? static_cast<uint32_t>(count[2 * i + 1]) : 0u;
+        p.hist[static_cast<int64_t>(blockIdx.x) * pairs + i] = lo | hi << 16;
+    }
+}
+
+// kCounted: the chunks' counts are read, two experts to a word, by the whole block with all loads in
+// flight (one thread per expert and one load after the other took 10 us for 128 chunks). Otherwise
+// every CTA counts all pairs itself.
+template <bool kCounted>
 __global__ void __launch_bounds__(kRouteThreads)
 route_scatter_kernel(const RouteArgs p) {
     extern __shared__ int base[];                                    // [E] next row of each expert
     uint32_t* mask = reinterpret_cast<uint32_t*>(base + p.E);        // [E][kSubWords]
     __shared__ int warp_sum[kRouteWarps];
     pdl_launch_dependents();
-    pdl_wait_prior_grid();
     const int c = static_cast<int>(blockIdx.x);
     int* sum_all = base;
     int* sum_before = reinterpret_cast<int*>(mask);
     for (int e = threadIdx.x; e < p.E; e += kRouteThreads) sum_all[e] = sum_before[e] = 0;
+    pdl_wait_prior_grid();
     __syncthreads();
-    const int lanes = (p.E + 31) / 32 * 32, ways = kRouteThreads / lanes;   // E <= threads: at least one way
-    const int way = static_cast<int>(threadIdx.x) / lanes, e = static_cast<int>(threadIdx.x) - way * lanes;
-    if (way < ways && e < p.E) {
-        int all = 0, before = 0;
-        constexpr int kFlight = 16;
-        for (int i0 = way; i0 < p.chunks; i0 += kFlight * ways) {
-            int v[kFlight];
+    if constexpr (kCounted) {
+        const int words = (p.E + 1) / 2, lanes = (words + 31) / 32 * 32, ways = kRouteThreads / lanes;
+        const int way = static_cast<int>(threadIdx.x) / lanes, i = static_cast<int>(threadIdx.x) - way * lanes;
+        if (way < ways && i < words) {
+            int all[2] = {0, 0}, before[2] = {0, 0};
+            constexpr int kFlight = 20;
+            for (int c0 = way; c0 < p.chunks; c0 += kFlight * ways) {
+                uint32_t v[kFlight];
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
-                const int i = i0 + u * ways;
-                v[u] = i < p.chunks ? __ldcg(p.hist + static_cast<int64_t>(i) * p.E + e) : 0;
+                for (int u = 0; u < kFlight; ++u) {
+                    const int r = c0 + u * ways;
+                    v[u] = r < p.chunks ? __ldcg(p.hist + static_cast<int64_t>(r) * words + i) : 0u;
+                }
+#pragma unroll
+                for (int u = 0; u < kFlight; ++u) {
+                    const int lo = static_cast<int>(v[u] & 0xFFFFu), hi = static_cast<int>(v[u] >> 16);
+                    all[0] += lo;
+                    all[1] += hi;
+                    if (c0 + u * ways < c) {
+                        before[0] += lo;
+                        before[1] += hi;
+                    }
+                }
             }
 #pragma unroll
-            for (int u = 0; u < kFlight; ++u) {
-                all += v[u];
-                before += i0 + u * ways < c ? v[u] : 0;
+            for (int h = 0; h < 2; ++h)
+                if (2 * i + h < p.E) {
+                    atomicAdd(&sum_all[2 * i + h], all[h]);
+                    atomicAdd(&sum_before[2 * i + h], before[h]);
+                }
+        }
+    } else {
+        const int pairs = p.T * p.k, mine = c * p.chunk * p.k;       // at most kRouteRecount pairs
+        for (int i = threadIdx.x; i < pairs; i += kRouteThreads) {
+            const int e = __ldcg(p.experts + i);
+            if (e >= 0) {
+                atomicAdd(&sum_all[e], 1);
+                if (i < mine) atomicAdd(&sum_before[e], 1);
             }
         }
-        atomicAdd(&sum_all[e], all);
-        atomicAdd(&sum_before[e], before);
     }
     __syncthreads();
     const int e0 = static_cast<int>(threadIdx.x);
@@ -344,25 +382,42 @@ route_scatter_kernel(const RouteArgs p) {
     chunk_scatter(p, c, all, before, base, mask, warp_sum);
 }
 
-// Tokens per CTA: one CTA up to kSub tokens (one launch for the whole call), then as many as make a
-// CTA per SM, and no fewer than a warp's worth each.
-int route_chunk(int64_t T, int sm_count) {
-    if (T <= kSub) return kSub;
-    const int64_t per = (T + sm_count - 1) / sm_count;
-    return static_cast<int>(per < kRouteWarps ? kRouteWarps : per);
+RoutePlan route_plan(int64_t T, int64_t E, int k, int sm_count) {
+    RoutePlan r = {};
+    if (T <= kRouteSmall) {
+        r.mode = 0;
+        r.chunk = kSub;
+    } else if (T * k <= kRouteRecount) {
+        r.mode = 1;
+        r.chunk = kSub;
+    } else {   // a CTA per SM; a chunk's counts fit 16 bits
+        r.mode = 2;
+        int64_t per = (T + sm_count - 1) / sm_count;
+        if (per > 32768) per = 32768;
+        r.chunk = static_cast<int>(per < kRouteWarps ? kRouteWarps : per);
+    }
+    r.chunks = static_cast<int>(T > 0 ? (T + r.chunk - 1) / r.chunk : 1);
+    r.ws_bytes = r.mode == 2 ? static_cast<size_t>(r.chunks) * static_cast<size_t>((E + 1) / 2) * 4 : 0;
+    return r;
 }
 
-cudaError_t launch_route(const RouteArgs& args, cudaStream_t s) {
+template <bool kBf16>
+static cudaError_t launch_route_as(const RouteArgs& args, int mode, cudaStream_t s) {
     const size_t count = static_cast<size_t>(args.E) * 4;
     const size_t scatter = count + static_cast<size_t>(args.E) * kSubWords * 4;
     const dim3 grid(args.chunks), block(kRouteThreads);
-    if (args.chunks == 1)
-        return args.bf16 ? launch_pdl(route_small_kernel<true>, grid, block, scatter, s, args)
-                         : launch_pdl(route_small_kernel<false>, grid, block, scatter, s, args);
-    const cudaError_t e = args.bf16 ? launch_pdl(route_topk_kernel<true>, grid, block, count, s, args)
-                                    : launch_pdl(route_topk_kernel<false>, grid, block, count, s, args);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(route_scatter_kernel, grid, block, scatter, s, args);
+    if (mode == 0) return launch_pdl(route_small_kernel<kBf16>, grid, block, scatter, s, args);
+    if (mode == 1) {
+        const dim3 blocks((args.T + kTopkThreads / 32 - 1) / (kTopkThreads / 32));
+        const cudaError_t e = launch_pdl(route_topk_kernel<kBf16>, blocks, dim3(kTopkThreads), 0, s, args);
+        return e != cudaSuccess ? e : launch_pdl(route_scatter_kernel<false>, grid, block, scatter, s, args);
+    }
+    const cudaError_t e = launch_pdl(route_topk_count_kernel<kBf16>, grid, block, count, s, args);
+    return e != cudaSuccess ? e : launch_pdl(route_scatter_kernel<true>, grid, block, scatter, s, args);
+}
+
+cudaError_t launch_route(const RouteArgs& args, int mode, cudaStream_t s) {
+    return args.bf16 ? launch_route_as<true>(args, mode, s) : launch_route_as<false>(args, mode, s);
 }
 
 // ------------------------------------------------------------------------ combination

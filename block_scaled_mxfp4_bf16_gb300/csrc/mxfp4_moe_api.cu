@@ -146,16 +146,13 @@ int mxfp4_grouped_gemm(const void* a, int64_t tokens, int64_t K, int64_t lda, co
     return run_stream(plan, di, g, ws, 1, s);
 }
 
-static int64_t route_chunks(int64_t T, int sm_count) {
-    const int64_t chunk = route_chunk(T, sm_count);
-    return T > 0 ? (T + chunk - 1) / chunk : 1;
-}
-
 size_t mxfp4_moe_route_workspace_size(int64_t T, int64_t E) {
     if (T < 0 || E < 1 || E > kMaxGroups || T > kMaxRows) return 0;
     DeviceInfo di;
     if (device_info(&di) != MXFP4_OK) return 0;
-    return static_cast<size_t>(route_chunks(T, di.sm_count)) * static_cast<size_t>(E) * 4;
+    // the most over k: 0 bytes are needed for few pairs
+    const size_t bytes = route_plan(T, E, MXFP4_ROUTE_MAX_K, di.sm_count).ws_bytes;
+    return bytes ? bytes : 4;
 }
 
 int mxfp4_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ld, int k, unsigned flags,
@@ -172,8 +169,8 @@ int mxfp4_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t
     DeviceInfo di;
     const int st = device_info(&di);
     if (st != MXFP4_OK) return st;
-    const int64_t chunks = route_chunks(T, di.sm_count);
-    if (!workspace || ws_bytes < static_cast<size_t>(chunks) * static_cast<size_t>(E) * 4) return MXFP4_ERR_WORKSPACE;
+    const RoutePlan plan = route_plan(T, E, k, di.sm_count);
+    if (plan.ws_bytes && (!workspace || ws_bytes < plan.ws_bytes)) return MXFP4_ERR_WORKSPACE;
     RouteArgs r = {};
     r.logits = logits;
     r.ld = ld;
@@ -187,10 +184,10 @@ int mxfp4_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t
     r.offsets = offsets;
     r.rows = rows;
     r.slots = slots;
-    r.hist = static_cast<int32_t*>(workspace);
-    r.chunk = route_chunk(T, di.sm_count);
-    r.chunks = static_cast<int>(chunks);
-    const cudaError_t e = launch_route(r, static_cast<cudaStream_t>(stream));
+    r.hist = static_cast<uint32_t*>(workspace);
+    r.chunk = plan.chunk;
+    r.chunks = plan.chunks;
+    const cudaError_t e = launch_route(r, plan.mode, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 

@@ -99,12 +99,17 @@ struct RouteArgs {
     int T, E, k, renormalize;
     float* weights;
     int32_t *experts, *offsets, *rows, *slots;
-    int32_t* hist;            // workspace: [chunks][E] counts, then their exclusive prefix
+    uint32_t* hist;           // workspace: [chunks][ceil(E / 2)] counts, two experts to a word
     int chunk;                // tokens per CTA
     int chunks;
 };
-int route_chunk(int64_t T, int sm_count);
-cudaError_t launch_route(const RouteArgs& args, cudaStream_t s);
+struct RoutePlan {
+    int mode;                 // 0: one CTA; 1: top-k, then a scatter that counts; 2: chunks with counts
+    int chunk, chunks;
+    size_t ws_bytes;
+};
+RoutePlan route_plan(int64_t T, int64_t E, int k, int sm_count);
+cudaError_t launch_route(const RouteArgs& args, int mode, cudaStream_t s);
 cudaError_t launch_combine(const uint16_t* y, int64_t rows, int64_t ldy, const int32_t* slots, const float* weights,
                            int64_t T, int k, int64_t N, uint16_t* out, int64_t ldo, cudaStream_t s);
 

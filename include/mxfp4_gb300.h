@@ -513,7 +513,8 @@ int mxfp4_grouped_gemm(const void *a, int64_t tokens, int64_t K, int64_t lda, co
  *   rows    : out, int32 [T * k]: the token of every sorted row, tokens ascending within an
  *             expert; -1 from offsets[E] on.
  *   slots   : out, int32 [T, k]: the sorted row of each pair; -1 where nothing was chosen.
- *   workspace: ws_bytes >= mxfp4_moe_route_workspace_size(T, E), 4-byte aligned.
+ *   workspace: ws_bytes >= mxfp4_moe_route_workspace_size(T, E), 4-byte aligned; its previous
+ *             contents do not matter.
  * All outputs are dense. T == 0 writes offsets (zeros) only.
  */
 #define MXFP4_F32 0

@@ -85,6 +85,16 @@ def test_route_special_logits():
             check_route(x.to(dtype).cuda(), k)
 
 
+@pytest.mark.parametrize("E", [2, 32, 33, 64, 200, 512, 1000])
+@pytest.mark.parametrize("k", [1, 2, 8])
+def test_route_takes_the_lowest_of_equal_logits(E, k):
+    g = torch.Generator().manual_seed(E)
+    few = torch.randint(-1, 2, (60, E), generator=g).float()
+    few[:3] = 0.25            # all the same
+    for dtype in (torch.float32, torch.bfloat16):
+        check_route(few.to(dtype).cuda(), min(k, E))
+
+
 def test_route_strided_logits_and_no_tokens():
     import block_scaled_mxfp4_bf16_gb300 as mx
     store = torch.randn(50, 100, device="cuda")
