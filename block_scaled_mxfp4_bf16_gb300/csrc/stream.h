@@ -19,6 +19,9 @@ constexpr int stream_threads(int terms, bool fused) { return kStreamThreads + (f
 constexpr int kSplitSteps = 8;            // 256-K steps that splitting a unit between CTAs has to save
 constexpr int kStreamMaxStages = 10;
 constexpr int kEpiStage = 640;            // bytes of shared memory an epilogue warp transposes through
+constexpr int kPairThreads = 640;         // the pair kernel: warps 12-19 write scale factors
+constexpr int kPairSfSlots = 5;           // steps whose scale factors are in tensor memory at once
+constexpr uint32_t kPairSfCols = 24;      // columns of one step: 8 weights, 16 tokens
 constexpr int kTerms = 8;                 // e2m1 terms an activation is expanded into (weight-only)
 
 // A group of n rows is cut into tiles_of(n) token tiles of tile_rows(n) rows (a multiple of 16,
@@ -66,6 +69,7 @@ struct StreamArgs {
 
 struct StreamPlan {
     int m_tile, nmc, stages, ctas, k_atoms, n_tiles, runs, cluster, accs;
+    int pair;                 // two CTAs to a unit of two weight tiles (mxfp4_stream_pair.cu)
     int fused;                // tokens written by the product's own warps, no launch before it
     uint32_t a_block, tmem_cols;
     size_t smem_bytes;
@@ -89,6 +93,7 @@ cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K,
 cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx, const StreamPlan& plan,
                                 uint8_t* blocks, cudaStream_t s);
 uint64_t next_call_tag();
+cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s);
 cudaError_t launch_stream(const StreamPlan& plan, const StreamArgs& args, int terms, cudaStream_t s);
 
 // Routing and combination (moe.cu).

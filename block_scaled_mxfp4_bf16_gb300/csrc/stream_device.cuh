@@ -1,0 +1,454 @@
+// Device code that the streaming products share: the groups' tiling, the walk over a CTA's (or a CTA
+// pair's) units, tcgen05 operations of one elected lane, and the epilogue's pieces.
+#pragma once
+#include "mma_desc.cuh"
+#include "quant_device.cuh"
+#include "stream.h"
+
+namespace mxfp4 {
+
+// Group g's rows [begin, begin + n), clamped so that offsets out of order or out of range can
+// reach no row outside [0, rows).
+__device__ __forceinline__ void group_rows(const int32_t* offsets, int rows, int g, int* begin, int* n) {
+    if (!offsets) {
+        *begin = 0;
+        *n = rows;
+        return;
+    }
+    const int b = min(max(__ldcg(offsets + g), 0), rows), e = min(max(__ldcg(offsets + g + 1), 0), rows);
+    *begin = b;
+    *n = max(0, e - b);
+}
+
+// Group that holds sorted row r: the number of offsets[1..groups] at or below r, counted by a
+// whole warp with independent loads.
+__device__ __forceinline__ int group_of_row(const int32_t* offsets, int groups, int r, int lane) {
+    int below = 0;
+    for (int g = lane; g < groups; g += 32) below += __ldcg(offsets + g + 1) <= r ? 1 : 0;
+    return __reduce_add_sync(0xffffffffu, below);
+}
+
+// tcgen05 operations of one elected lane of a converged warp. The whole warp runs the issue loop and
+// only these are predicated: the compiler then keeps descriptors and addresses in uniform
+// registers, which the instructions take their operands from. (Measured against one lane running
+// the loop alone: 1x131072x7168 98.2 -> 75.1 us, 16384 rows x 4096 x 7168 357 -> 268 us; copying
+// the next stage's scales ahead of this stage's MMAs gained nothing, 272 us.)
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void mma_mxf4_if(uint32_t issue, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 e, %7, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void tc_copy_sf_if(uint32_t issue, uint32_t taddr, uint64_t src_desc) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %2, 0;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}"
+        ::"r"(taddr), "l"(src_desc), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_load_if(uint32_t issue, uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                             uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1], %2, [%3], %4;\n\t}"
+        ::"r"(dst), "l"(src), "r"(bytes), "r"(bar), "l"(policy), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void mbar_expect_if(uint32_t issue, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %2, 0;\n\t"
+        "@e mbarrier.arrive.expect_tx.release.cta.shared::cta.b64 _, [%0], %1;\n\t}"
+        ::"r"(bar), "r"(bytes), "r"(issue)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_if(uint32_t issue, uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        ::"r"(smem_addr(bar)), "r"(issue)
+        : "memory");
+}
+
+// prefix[g + 1]: token tiles of groups 0 .. g; begins[g]: first sorted row of group g, begins[groups]:
+// the end of the last. An inclusive scan over the groups, a chunk of the block's threads at a time;
+// all threads call. prefix[0], and everything of a call without offsets, is set by the caller before.
+// Offsets that decrease or leave [0, rows] would break the tiling: then no tile is reported. Returns
+// the number of tiles, behind a barrier of the block.
+template <int kThreads>
+__device__ __forceinline__ int count_tiles(const StreamArgs& p, int* prefix, int* begins, int* warp_sum, int warp, int lane) {
+    int total = 0;
+    bool bad = false;
+    if (!p.offsets) total = tiles_of(p.rows, p.m_tile);
+    for (int g0 = 0; p.offsets && g0 < p.groups; g0 += kThreads) {
+        const int g = g0 + static_cast<int>(threadIdx.x);
+        int t = 0;
+        if (g < p.groups) {
+            int begin, n;
+            group_rows(p.offsets, p.rows, g, &begin, &n);
+            t = tiles_of(n, p.m_tile);
+            begins[g] = begin;
+            if (g == p.groups - 1) begins[p.groups] = begin + n;
+            const int b = __ldcg(p.offsets + g), e = __ldcg(p.offsets + g + 1);
+            bad = bad || b < 0 || e < b || e > p.rows;
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, t, d);
+            if (lane >= d) t += o;
+        }
+        __syncthreads();
+        if (lane == 31) warp_sum[warp] = t;
+        __syncthreads();
+        int before = total;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            const int v = warp_sum[i];
+            if (i < warp) before += v;
+            total += v;
+        }
+        if (g < p.groups) prefix[g + 1] = before + t;
+    }
+    return __syncthreads_or(bad ? 1 : 0) ? 0 : total;
+}
+
+// What every role of a CTA walks through: its whole units, then its run of the split units, share
+// by share (a share is the part of one unit that is this CTA's).
+struct Walk {
+    // the share
+    int nt, slot, row0, rows;  // weight tile; token-block tile; its first sorted row and its rows
+    int k0, nk;                // 256-K steps [k0, k0 + nk) of the unit
+    int split;                 // index among the split units, -1: the whole unit in one CTA
+    // the schedule
+    int units, waves, wave;    // all units; full waves of whole units; the next wave
+    int64_t s, s1, share;      // the run over the steps of the split units; steps per CTA of them
+    // the group the unit lies in
+    int group, first, end;     // its units [first, end)
+    int tiles, per, begin, n;  // token tiles, rows per tile, sorted rows [begin, begin + n)
+    float inv_tiles;
+};
+
+// Who walks: a CTA, or the two CTAs of a pair together, with two neighbouring weight tiles as one.
+template <bool kPair>
+__device__ __forceinline__ int walkers() { return static_cast<int>(kPair ? gridDim.x >> 1 : gridDim.x); }
+template <bool kPair>
+__device__ __forceinline__ int walker() { return static_cast<int>(kPair ? blockIdx.x >> 1 : blockIdx.x); }
+template <bool kPair>
+__device__ __forceinline__ int weight_tiles(const StreamArgs& p) { return kPair ? (p.n_tiles + 1) >> 1 : p.n_tiles; }
+
+// Units are ordered by group, then weight tile, then token tile: the CTAs that work at the same
+// time share the group's weights as well as its tokens. `unit` never decreases along a walk, so the
+// group is found by stepping on from the last one, and its numbers are worked out once a group
+// (worked out again for every unit, with a search and four divisions, 6000 rows x 2880 x 2040
+// measured 56 us instead of 49).
+template <bool kPair = false>
+__device__ __forceinline__ void locate(const StreamArgs& p, const int* prefix, int unit, Walk& w) {
+    const int n_tiles = weight_tiles<kPair>(p);
+    if (unit >= w.end) {
+        int g = w.group + 1;
+        while (prefix[g + 1] * n_tiles <= unit) ++g;
+        w.group = g;
+        w.first = prefix[g] * n_tiles;
+        w.end = prefix[g + 1] * n_tiles;
+        w.tiles = prefix[g + 1] - prefix[g];
+        w.inv_tiles = 1.f / static_cast<float>(w.tiles);
+        w.begin = prefix[p.groups + 1 + g];        // the groups' first rows follow the prefix
+        w.n = prefix[p.groups + 2 + g] - w.begin;
+        w.per = ((w.n + w.tiles - 1) / w.tiles + 15) / 16 * 16;   // tile_rows(n, m_tile)
+    }
+    const int r = unit - w.first;
+    int nt = w.tiles == 1 ? r : __float2int_rz(static_cast<float>(r) * w.inv_tiles);   // r / tiles, off by one at most
+    int i = r - nt * w.tiles;
+    if (i < 0) {
+        --nt;
+        i += w.tiles;
+    } else if (i >= w.tiles) {
+        ++nt;
+        i -= w.tiles;
+    }
+    w.nt = nt;
+    w.slot = tile_slot(w.begin, w.group, i, p.m_tile);
+    w.row0 = w.begin + i * w.per;
+    w.rows = min(w.per, w.n - i * w.per);
+}
+
+template <bool kPair = false>
+__device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefix, int units) {
+    const int grid = walkers<kPair>(), me = walker<kPair>();
+    Walk w = {};
+    w.units = units;
+    const bool runs = p.runs && units >= 4 * grid;
+    w.waves = runs ? 0 : units / grid;
+    const int64_t steps = static_cast<int64_t>(units - w.waves * grid) * p.k_atoms;
+    w.share = (steps + grid - 1) / grid;
+    // a split unit costs what eight steps do (4 us: sums out, arrival, sums in): not for less, and
+    // not among more than six CTAs
+    if (!runs) {
+        w.share = max(w.share, static_cast<int64_t>((p.k_atoms + 5) / 6));
+        if (w.share + kSplitSteps > p.k_atoms) w.share = p.k_atoms;
+    }
+    w.s = min(steps, w.share * me);
+    w.s1 = min(steps, w.s + w.share);
+    if (p.cluster > 1) {   // the CTAs of a cluster share one unit
+        const int rank = static_cast<int>(blockIdx.x) % p.cluster;
+        const int base = p.k_atoms / p.cluster, rem = p.k_atoms % p.cluster;
+        w.waves = 0;
+        w.s = static_cast<int64_t>(blockIdx.x / p.cluster) * p.k_atoms + rank * base + min(rank, rem);
+        w.s1 = min(static_cast<int64_t>(units) * p.k_atoms, w.s + base + (rank < rem ? 1 : 0));
+    }
+    // the group before the first unit's, by bisection
+    const int unit = w.waves ? me : static_cast<int>(w.s / p.k_atoms);
+    int lo = 0, hi = p.groups;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] * weight_tiles<kPair>(p) <= unit) lo = mid;
+        else hi = mid;
+    }
+    w.group = lo - 1;
+    w.end = 0;
+    return w;
+}
+
+template <bool kPair = false>
+__device__ __forceinline__ bool next_share(const StreamArgs& p, const int* prefix, Walk& w) {
+    const int grid = walkers<kPair>();
+    if (w.wave < w.waves) {
+        locate<kPair>(p, prefix, w.wave * grid + walker<kPair>(), w);
+        w.split = -1;
+        w.k0 = 0;
+        w.nk = p.k_atoms;
+        ++w.wave;
+        return true;
+    }
+    if (w.s >= w.s1) return false;
+    const int u = static_cast<int>(w.s / p.k_atoms);
+    locate<kPair>(p, prefix, w.waves * grid + u, w);
+    w.k0 = static_cast<int>(w.s - static_cast<int64_t>(u) * p.k_atoms);
+    w.nk = static_cast<int>(min(static_cast<int64_t>(p.k_atoms - w.k0), w.s1 - w.s));
+    w.split = w.nk == p.k_atoms ? -1 : u;
+    w.s += w.nk;
+    return true;
+}
+
+__device__ __forceinline__ void stream_fail(const StreamArgs& p, volatile uint32_t* abort_flag) {
+    atomicOr(p.status, 1u);
+    *abort_flag = 1u;
+}
+
+// 16 columns of this lane from column `col` as fp32: tokens (kTermsPer = 1), or sums over kTermsPer
+// columns each, the smallest terms first.
+template <int kTermsPer>
+__device__ __forceinline__ void load_tokens(uint32_t taddr, float (&v)[16 / kTermsPer]) {
+    uint32_t r[16];
+    tmem_load_16(taddr, r);
+    tmem_load_wait();
+#pragma unroll
+    for (int i = 0; i < 16 / kTermsPer; ++i) {
+        float s = __uint_as_float(r[i * kTermsPer + kTermsPer - 1]);
+#pragma unroll
+        for (int t = kTermsPer - 2; t >= 0; --t) s += __uint_as_float(r[i * kTermsPer + t]);
+        v[i] = s;
+    }
+}
+
+// 32 columns of 16 lanes (from the lane and column of taddr) as the fragment of an m16n8 matrix
+// instruction per 8 columns: thread t holds rows t / 4 (v[4i], v[4i+1]) and t / 4 + 8 (v[4i+2],
+// v[4i+3]), columns 8i + 2 (t % 4) and the next.
+__device__ __forceinline__ void tmem_load_frag32(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+// Four 8x8 matrices of 16-bit values, stored transposed: lane 8m + r gives the address of row r
+// (a column of the fragments) of matrix m, eight values.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                 ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// A whole unit's accumulator (lane = weight row, column = token) -> bf16 C. A warp owns 32 weight
+// rows; per 8 tokens it packs its fragments, transposes them through 640 bytes of shared memory
+// (rows of 64 bytes, 80 apart) and stores kVec elements a lane, the widest that C's rows are aligned
+// to: one instruction writes 64 contiguous bytes of each of kVec rows of C. (16-byte stores and one
+// column of 2-byte stores per token measured the same in waves; for rows that are not aligned,
+// 2-byte stores of 16-byte pieces took four times as long as whole rows of 64 bytes.)
+template <int kVec>
+__device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, int rows, int64_t row0, int n0, int half,
+                                           int lane, uint8_t* stage) {
+    constexpr int kLanes = 32 / kVec;              // lanes per row of C
+    const uint32_t st = smem_addr(stage);
+    const uint32_t put = st + static_cast<uint32_t>((lane & 7) * 80 + (lane >> 3) * 16);
+    const int r0 = lane / kLanes, n = n0 + (lane % kLanes) * kVec;
+    const uint8_t* got = stage + r0 * 80 + (lane % kLanes) * (2 * kVec);
+    const bool whole = n + kVec <= p.N;
+    for (int cb = half * 32; cb < rows; cb += 64) {
+        uint32_t lo[16], hi[16];
+        tmem_load_frag32(trow + static_cast<uint32_t>(cb), lo);
+        tmem_load_frag32(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
+        tmem_load_wait();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (cb + 8 * i < rows) {
+                __syncwarp();
+                stmatrix_x4_trans(put, pack_bf16x2(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])),
+                                  pack_bf16x2(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])),
+                                  pack_bf16x2(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
+                                  pack_bf16x2(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])));
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < 8; q += kVec) {
+                    const int m = cb + 8 * i + q + r0;
+                    uint16_t* cp = p.c + (row0 + m) * p.ldc + n;
+                    const uint8_t* from = got + q * 80;
+                    if (m < rows && whole) {
+                        if constexpr (kVec == 8) *reinterpret_cast<uint4*>(cp) = *reinterpret_cast<const uint4*>(from);
+                        else if constexpr (kVec == 4) *reinterpret_cast<uint2*>(cp) = *reinterpret_cast<const uint2*>(from);
+                        else if constexpr (kVec == 2) *reinterpret_cast<uint32_t*>(cp) = *reinterpret_cast<const uint32_t*>(from);
+                        else *cp = *reinterpret_cast<const uint16_t*>(from);
+                    } else if (kVec > 1 && m < rows) {
+                        for (int k = 0; n + k < p.N; ++k) cp[k] = reinterpret_cast<const uint16_t*>(from)[k];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// One more arrival at a split unit's counter: how many came before. A word belongs to this call if
+// its upper bits are the call's tag, which no other call has; anything else, left there by other
+// uses of the workspace, counts as none. So the counters need no launch that clears them.
+// `seen`: the word as read a moment ago.
+__device__ __forceinline__ uint32_t arrive(unsigned long long* counter, unsigned long long seen, uint64_t tag) {
+    while (true) {
+        const unsigned long long mine = (seen >> 8) == tag ? seen : static_cast<unsigned long long>(tag << 8);
+        const unsigned long long was = atomicCAS(counter, seen, mine + 1);
+        if (was == seen) return static_cast<uint32_t>(mine & 0xFFu);
+        seen = was;
+    }
+}
+
+// A CTA's share of a unit from its accumulator (at acc in this warp's quarter of the lanes) to C:
+// the eight epilogue warps (warps 4 .. 11) call. Weight tile nt, 128 rows.
+// A whole unit goes straight out. Of a unit split between CTAs (or pairs), each but the last to
+// arrive leaves its sums in its slot of the workspace (slot 0 for the unit its run begins in, slot 1
+// for one it reaches later); the last adds all of them in the order of K, its own from tensor memory.
+template <int kTermsPer, bool kPair>
+__device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, int nt, uint32_t acc, int half, int warp,
+                                           int lane, volatile uint32_t* last_flag, uint8_t* stage) {
+    constexpr int kTok = 16 / kTermsPer;         // tokens per 16 columns
+    constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
+    if (kTermsPer == 1 && u.split < 0) {
+        const int n0 = nt * kTileN + (warp & 3) * 32;
+        if (p.c_vec == 8) store_tile<8>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+        else if (p.c_vec == 4) store_tile<4>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+        else if (p.c_vec == 2) store_tile<2>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+        else store_tile<1>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+        return;
+    }
+    const int nl = (warp & 3) * 32 + lane, n = nt * kTileN + nl;
+    const int tokens = u.rows / kTermsPer;       // exact: rows are kTermsPer per token
+    const int64_t row0 = u.row0 / kTermsPer;
+    const int rank = kPair ? static_cast<int>(blockIdx.x & 1u) : 0;
+    const int64_t me = walker<kPair>();
+    const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;
+    const int64_t unit_step = static_cast<int64_t>(u.split) * p.k_atoms;
+    bool last = true;
+    int64_t c_first = 0, c_last = 0;
+    if (u.split >= 0) {
+        c_first = unit_step / u.share;
+        c_last = (unit_step + p.k_atoms - 1) / u.share;
+        const uint32_t others = static_cast<uint32_t>(c_last - c_first);
+        const int slot = u.k0 == 0 && u.s - u.nk != u.share * me ? 1 : 0;
+        volatile uint32_t* flag = last_flag + 2 * slot;
+        unsigned long long* counter = p.counters + (c_first * kRanks + rank);   // a split unit is named by its first walker
+        if (threadIdx.x == 128)
+            flag[0] = *reinterpret_cast<volatile unsigned long long*>(counter) == (p.tag << 8 | others) ? 1u : 0u;
+        named_barrier(2, kStreamEpiThreads);
+        last = flag[0] != 0u;
+        if (!last) {
+            float* mine = p.partial + (static_cast<size_t>(me * kRanks + rank) * 2 + slot) * slot_floats;
+            for (int cb = half * 16; cb < u.rows; cb += 32) {
+                float v[kTok];
+                load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
+                const int m0 = cb / kTermsPer;
+#pragma unroll
+                for (int i = 0; i < kTok; ++i)
+                    if (m0 + i < tokens) __stcg(mine + static_cast<size_t>(m0 + i) * kTileN + nl, v[i]);
+            }
+            unsigned long long seen = 0ull;
+            if (threadIdx.x == 128) seen = *reinterpret_cast<volatile unsigned long long*>(counter);
+            __threadfence();
+            named_barrier(2, kStreamEpiThreads);
+            if (threadIdx.x == 128) flag[1] = arrive(counter, seen, p.tag) == others ? 1u : 0u;
+            named_barrier(2, kStreamEpiThreads);
+            last = flag[1] != 0u;
+        }
+        __threadfence();
+        if (last && threadIdx.x == 128) *counter = 0ull;   // as found by a replay of this launch
+    }
+    if (!last) return;
+    for (int cb = half * 16; cb < u.rows; cb += 32) {
+        float own[kTok], v[kTok];
+        const int m0 = cb / kTermsPer;
+        load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), own);
+        if (u.split < 0) {
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) v[i] = own[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) v[i] = 0.f;
+            // two walkers' sums are on their way at a time, added in the order of K
+            for (int64_t c0 = c_first; c0 <= c_last; c0 += 2) {
+                float theirs[2][kTok];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int64_t c = c0 + q;
+                    if (c > c_last || c == me) continue;
+                    // the unit is the first of c's run unless the run began before it
+                    const float* src = p.partial + (static_cast<size_t>(c * kRanks + rank) * 2 +
+                                                    (c * u.share < unit_step ? 1 : 0)) * slot_floats;
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i)
+                        theirs[q][i] = m0 + i < tokens ? __ldcg(src + static_cast<size_t>(m0 + i) * kTileN + nl) : 0.f;
+                }
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (c0 + q > c_last) continue;
+#pragma unroll
+                    for (int i = 0; i < kTok; ++i) v[i] += c0 + q == me ? own[i] : theirs[q][i];
+                }
+            }
+        }
+        if (n < p.N) {
+            uint16_t* cp = p.c + (row0 + m0) * p.ldc + n;
+#pragma unroll
+            for (int i = 0; i < kTok; ++i) {
+                if (m0 + i < tokens) *cp = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+                cp += p.ldc;
+            }
+        }
+    }
+}
+
+}  // namespace mxfp4

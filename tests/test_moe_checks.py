@@ -226,12 +226,15 @@ int main() {
         CHECK(make_stream_plan(rows, groups, N, K, terms, 152, clusters, &p) == 0);
         // shared memory: everything the kernel lays out, within the limit, and (but for 2 KB) as large a
         // part of the SM's as the columns are of its tensor memory
-        const size_t laid = 1024 + (size_t)p.stages * (kWBlock + p.a_block) + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 +
+        const uint32_t t_stage = p.pair ? p.a_block - p.m_tile * 64 : p.a_block;
+        const size_t laid = 1024 + (size_t)p.stages * (kWBlock + t_stage) + (p.pair ? 64 : 0) + ((p.pair ? 3 : 2) * kStreamMaxStages + 4) * 8 + 32 + 64 +
                             8 * kEpiStage + 2 * (groups + 1) * 4 + (size_t)(p.cluster > 1 ? p.cluster : 0) * (p.m_tile / terms) * kTileN * 4;
         CHECK(p.smem_bytes >= laid && p.smem_bytes <= kSmemLimit);
         CHECK((p.smem_bytes + 1024 + 2048) * 512 >= (size_t)233472 * p.tmem_cols);
         CHECK(p.stages >= 1 && p.stages <= kStreamMaxStages);
-        CHECK(p.accs * p.m_tile + p.stages * 8 * (1 + p.nmc) <= (int)p.tmem_cols && p.tmem_cols <= 512);
+        const int sf_cols = p.pair ? kPairSfSlots * (int)kPairSfCols : p.stages * 8 * (1 + p.nmc);
+        CHECK(p.accs * p.m_tile + sf_cols <= (int)p.tmem_cols && p.tmem_cols <= 512);
+        if (p.pair) CHECK(terms == 1 && p.ctas % 2 == 0 && p.nmc == 2 && p.stages >= kPairSfSlots && p.cluster == 1 && p.accs == 2);
         CHECK(p.a_block == (uint32_t)(p.m_tile * 128 + p.nmc * 1024) && p.m_tile % 16 == 0 && p.m_tile <= 192);
         if (terms == 1) CHECK(p.cluster == 1 && p.accs == 2);
         // CTAs: one per SM at most, or whole clusters that are all resident, at least two steps each
