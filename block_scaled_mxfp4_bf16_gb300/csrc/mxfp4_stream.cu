@@ -78,37 +78,60 @@ __device__ __forceinline__ void gate_pair(uint32_t g, uint32_t u, float* v) {
 
 // A warp takes `step` consecutive 1x32 blocks of one sorted row (all of them when there are rows
 // enough to fill the GPU), a lane per block, 32 at a time with the next 32 on their way: the row's
-// group and source are looked up once. Blocks past K become zero codes; an index outside
+// group and source are looked up once. Rows of at most 16 or 8 blocks are taken two or four at a time
+// (kRows), each by its share of the lanes. Blocks past K become zero codes; an index outside
 // [0, tokens) gives a row of zeros. kGated: a row of a holds [g, u], K each, and silu(g) * u is
-// quantized. Bound by bytes when rows are many: 16384 x 7168 bf16 read (half of them from L2) and
-// 4.25 bits a value written, 45 us in all.
-template <bool kGated>
+// quantized. 16384 x 7168 bf16 (half of it from L2) take 45 us: the L1 cache's tag lookups (78 %) and
+// the integer pipe of the encoding share the blame. Each block takes the offsets to shared memory once:
+// when every warp looked its row's group up in L2, all of them in the same few sectors, 22672 rows of
+// K = 160 took 31 us, now 7.
+template <bool kGated, int kRows>
 __global__ void __launch_bounds__(256)
 quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K, int64_t lda,
                        const int32_t* index, const int32_t* offsets, int groups, int rows, int m_tile, int k_atoms,
                        uint32_t a_block, uint8_t* __restrict__ blocks, int parts, int step) {
+    extern __shared__ int s_offsets[];          // offsets, clamped to [0, rows]
     pdl_wait_prior_grid();   // a, index and offsets may come from the previous grid
     // dependents may start now: what they read early (the offsets) was complete before this grid
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
+    if (offsets) {
+        for (int i = threadIdx.x; i <= groups; i += blockDim.x) s_offsets[i] = min(max(__ldcg(offsets + i), 0), rows);
+        __syncthreads();
+    }
+    constexpr int kWidth = 32 / kRows;          // lanes per row
+    const int lane = threadIdx.x & 31, sub = lane / kWidth;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    for (int64_t it = w; it < static_cast<int64_t>(rows) * parts; it += warps) {
-        const int r = static_cast<int>(it / parts);
-        const int kb0 = static_cast<int>(it - static_cast<int64_t>(r) * parts) * step;
+    const int64_t row_sets = (static_cast<int64_t>(rows) + kRows - 1) / kRows;
+    for (int64_t it = w; it < row_sets * parts; it += warps) {
+        const int64_t set = it / parts;
+        const int r = static_cast<int>(set) * kRows + sub;
+        const int kb0 = static_cast<int>(it - set * parts) * step;
         const int kb1 = min(k_atoms * 8, kb0 + step);
-        const int64_t src = index ? static_cast<int64_t>(index[r]) : r;
-        const int g = offsets ? group_of_row(offsets, groups, r, lane) : 0;
-        if (g >= groups) continue;                 // past the last group
-        int begin, n;
-        group_rows(offsets, rows, g, &begin, &n);
-        if (r < begin || r >= begin + n) continue;
+        const int64_t src = r < rows ? (index ? static_cast<int64_t>(index[r]) : r) : -1;
+        int g = 0, begin = 0, n = offsets ? 0 : rows;
+        if (offsets) {
+            for (int left = groups; left > 0;) {     // offsets[1 .. groups] at or below r
+                const int h = left >> 1;
+                if (s_offsets[g + h + 1] <= r) {
+                    g += h + 1;
+                    left -= h + 1;
+                } else {
+                    left = h;
+                }
+            }
+            if (g < groups) {                        // else past the last group
+                begin = s_offsets[g];
+                n = max(0, s_offsets[g + 1] - begin);
+            }
+        }
+        const bool mine = r >= begin && r < begin + n;   // the row belongs to a group
         const int per = tile_rows(n, m_tile);
-        const int tile = (r - begin) / per;
+        const int tile = mine ? (r - begin) / per : 0;
         const uint32_t rr = static_cast<uint32_t>(r - begin - tile * per);
-        uint8_t* out_row = blocks + static_cast<size_t>(tile_slot(begin, g, tile, m_tile)) * k_atoms * a_block;
+        uint8_t* out_row = blocks + static_cast<size_t>(mine ? tile_slot(begin, g, tile, m_tile) : 0) * k_atoms * a_block;
         const uint16_t* row = a + src * lda;
-        const bool present = src >= 0 && src < tokens;
+        const bool present = mine && src >= 0 && src < tokens;
         constexpr int kWords = kGated ? 32 : 16;
         uint32_t next[kWords];
         auto load = [&](int kb) {
@@ -118,13 +141,13 @@ quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K
                 if constexpr (kGated) load_block32_upto(row + K + k, K - k, *reinterpret_cast<uint32_t(*)[16]>(&next[16]));
             }
         };
-        load(kb0 + lane);
-        for (int base = kb0; base < kb1; base += 32) {
-            const int kb = base + lane;
+        load(kb0 + lane % kWidth);
+        for (int base = kb0; base < kb1; base += kWidth) {
+            const int kb = base + lane % kWidth;
             uint32_t v[kWords], out[4] = {0u, 0u, 0u, 0u}, byte = 0u;
 #pragma unroll
             for (int i = 0; i < kWords; ++i) v[i] = next[i];
-            load(kb + 32);
+            load(kb + kWidth);
             if (present && static_cast<int64_t>(kb) * 32 < K && kb < kb1) {
                 if constexpr (kGated) {
                     float h[32];
@@ -138,7 +161,7 @@ quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K
             uint32_t word = byte << (8 * (lane & 3));
             word |= __shfl_xor_sync(0xffffffffu, word, 1);
             word |= __shfl_xor_sync(0xffffffffu, word, 2);
-            if (kb < kb1) {
+            if (mine && kb < kb1) {
                 uint8_t* blk = out_row + static_cast<size_t>(kb >> 3) * a_block;
                 const uint32_t c = static_cast<uint32_t>(kb & 7);
                 *reinterpret_cast<uint4*>(blk + swz_chunk_offset(rr, c)) = make_uint4(out[0], out[1], out[2], out[3]);
@@ -702,16 +725,24 @@ uint64_t next_call_tag() {
 cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,
                                    const int32_t* offsets, int groups, int rows, bool gated, const StreamPlan& plan,
                                    uint8_t* blocks, cudaStream_t s) {
-    // as many parts of a row as make enough warps for every SM, whole rows beyond that
+    // as many parts of a row as make enough warps for every SM, whole rows beyond that, short rows
+    // several to a warp
     const int chunks = (plan.k_atoms * 8 + 31) / 32;
     const int64_t want = (int64_t(4096) + rows - 1) / rows;
     const int per = static_cast<int>(want >= chunks ? 1 : chunks / want);
     const int parts = (chunks + per - 1) / per;
-    int64_t grid = (static_cast<int64_t>(rows) * parts + 7) / 8;
+    const int at_once = plan.k_atoms == 1 ? 4 : plan.k_atoms == 2 ? 2 : 1;
+    int64_t grid = ((static_cast<int64_t>(rows) + at_once - 1) / at_once * parts + 7) / 8;
     if (grid > 65535) grid = 65535;
-    return launch_pdl(gated ? quantize_groups_kernel<true> : quantize_groups_kernel<false>,
-                      dim3(static_cast<unsigned>(grid)), dim3(256), 0, s, a, tokens, K, lda, index, offsets, groups, rows,
-                      plan.m_tile, plan.k_atoms, plan.a_block, blocks, parts, per * 32);
+    auto* kernel = gated ? (at_once == 4   ? quantize_groups_kernel<true, 4>
+                            : at_once == 2 ? quantize_groups_kernel<true, 2>
+                                           : quantize_groups_kernel<true, 1>)
+                         : (at_once == 4   ? quantize_groups_kernel<false, 4>
+                            : at_once == 2 ? quantize_groups_kernel<false, 2>
+                                           : quantize_groups_kernel<false, 1>);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(256),
+                      static_cast<size_t>(groups + 1) * sizeof(int), s, a, tokens, K, lda, index, offsets, groups,
+                      rows, plan.m_tile, plan.k_atoms, plan.a_block, blocks, parts, per * 32);
 }
 
 cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx, const StreamPlan& plan,

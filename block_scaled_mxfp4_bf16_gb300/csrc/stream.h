@@ -18,7 +18,7 @@ constexpr int token_warps(int terms) { return terms > 1 ? 8 : 6; }
 constexpr int stream_threads(int terms, bool fused) { return kStreamThreads + (fused ? 32 * (token_warps(terms) - 2) : 0); }
 constexpr int kSplitSteps = 8;            // 256-K steps that splitting a unit between CTAs has to save
 constexpr int kStreamMaxStages = 10;
-constexpr int kEpiStage = 640;            // bytes of shared memory an epilogue warp transposes through
+constexpr int kEpiStage = 1024;           // bytes of shared memory an epilogue warp transposes through
 constexpr int kPairThreads = 640;         // the pair kernel: warps 12-19 write scale factors
 constexpr int kPairSfSlots = 5;           // steps whose scale factors are in tensor memory at once
 constexpr uint32_t kPairSfCols = 24;      // columns of one step: 8 weights, 16 tokens
@@ -63,7 +63,7 @@ struct StreamArgs {
     int cluster;              // CTAs that share a unit through their cluster (weight-only), or 1
     uint32_t a_block;
     uint32_t tmem_cols;
-    int c_vec;                // elements of the widest stores C's rows are aligned to: 8, 4, 2 or 1
+    int c_vec;                // elements a store: 8 where C's rows are aligned for it, else 1
     uint64_t wait_limit_ns;
 };
 

@@ -20,14 +20,6 @@ __device__ __forceinline__ void group_rows(const int32_t* offsets, int rows, int
     *n = max(0, e - b);
 }
 
-// Group that holds sorted row r: the number of offsets[1..groups] at or below r, counted by a
-// whole warp with independent loads.
-__device__ __forceinline__ int group_of_row(const int32_t* offsets, int groups, int r, int lane) {
-    int below = 0;
-    for (int g = lane; g < groups; g += 32) below += __ldcg(offsets + g + 1) <= r ? 1 : 0;
-    return __reduce_add_sync(0xffffffffu, below);
-}
-
 // tcgen05 operations of one elected lane of a converged warp. The whole warp runs the issue loop and
 // only these are predicated: the compiler then keeps descriptors and addresses in uniform
 // registers, which the instructions take their operands from. (Measured against one lane running
@@ -288,46 +280,63 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 }
 
 // A whole unit's accumulator (lane = weight row, column = token) -> bf16 C. A warp owns 32 weight
-// rows; per 8 tokens it packs its fragments, transposes them through 640 bytes of shared memory
-// (rows of 64 bytes, 80 apart) and stores kVec elements a lane, the widest that C's rows are aligned
-// to: one instruction writes 64 contiguous bytes of each of kVec rows of C. (16-byte stores and one
-// column of 2-byte stores per token measured the same in waves; for rows that are not aligned,
-// 2-byte stores of 16-byte pieces took four times as long as whole rows of 64 bytes.)
+// rows; 16 tokens at a time it packs its fragments, transposes them through 1 KB of shared memory and
+// stores kVec elements a lane: one instruction writes 64 contiguous bytes of each of kVec rows of C.
+// Where C's rows are aligned for it kVec is 8, else 1: 22672 rows of 5664 elements after K = 160 took
+// 145 us and 169. Rows of 5668 took 172 us with 8-byte stores and 170 with single elements, rows of
+// 5666 226 us with 4-byte stores and 170. The 1 KB hold 16 rows of 64 bytes, the 16-byte piece c of
+// row r at c ^ (r / 2 % 4), so that both the 8 rows a matrix is stored to and the pieces eight lanes read
+// touch all banks. (2-byte stores in the lanes of 16-byte ones took four times as long where C's rows
+// are not aligned; 8 tokens at a time, every piece waited for the one before.)
 template <int kVec>
 __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, int rows, int64_t row0, int n0, int half,
                                            int lane, uint8_t* stage) {
     constexpr int kLanes = 32 / kVec;              // lanes per row of C
-    const uint32_t st = smem_addr(stage);
-    const uint32_t put = st + static_cast<uint32_t>((lane & 7) * 80 + (lane >> 3) * 16);
-    const int r0 = lane / kLanes, n = n0 + (lane % kLanes) * kVec;
-    const uint8_t* got = stage + r0 * 80 + (lane % kLanes) * (2 * kVec);
+    const uint32_t put = smem_addr(stage) + static_cast<uint32_t>((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+    const int r0 = lane / kLanes, at = (lane % kLanes) * kVec, n = n0 + at;
     const bool whole = n + kVec <= p.N;
+    auto from = [&](int r) -> const uint8_t* {     // this lane's elements of row r of the 16
+        return stage + r * 64 + ((((at >> 3) ^ (r >> 1)) & 3) << 4) + (at & 7) * 2;
+    };
     for (int cb = half * 32; cb < rows; cb += 64) {
         uint32_t lo[16], hi[16];
         tmem_load_frag32(trow + static_cast<uint32_t>(cb), lo);
         tmem_load_frag32(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
         tmem_load_wait();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (cb + 8 * i < rows) {
-                __syncwarp();
-                stmatrix_x4_trans(put, pack_bf16x2(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])),
-                                  pack_bf16x2(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])),
-                                  pack_bf16x2(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
-                                  pack_bf16x2(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])));
+        for (int h = 0; h < 2; ++h) {
+            if (cb + 16 * h < rows) {
                 __syncwarp();
 #pragma unroll
-                for (int q = 0; q < 8; q += kVec) {
-                    const int m = cb + 8 * i + q + r0;
-                    uint16_t* cp = p.c + (row0 + m) * p.ldc + n;
-                    const uint8_t* from = got + q * 80;
-                    if (m < rows && whole) {
-                        if constexpr (kVec == 8) *reinterpret_cast<uint4*>(cp) = *reinterpret_cast<const uint4*>(from);
-                        else if constexpr (kVec == 4) *reinterpret_cast<uint2*>(cp) = *reinterpret_cast<const uint2*>(from);
-                        else if constexpr (kVec == 2) *reinterpret_cast<uint32_t*>(cp) = *reinterpret_cast<const uint32_t*>(from);
-                        else *cp = *reinterpret_cast<const uint16_t*>(from);
-                    } else if (kVec > 1 && m < rows) {
-                        for (int k = 0; n + k < p.N; ++k) cp[k] = reinterpret_cast<const uint16_t*>(from)[k];
+                for (int q = 0; q < 2; ++q) {
+                    const int i = 2 * h + q;
+                    stmatrix_x4_trans(put + static_cast<uint32_t>(q) * 512u,
+                                      pack_bf16x2(__uint_as_float(lo[4 * i]), __uint_as_float(lo[4 * i + 1])),
+                                      pack_bf16x2(__uint_as_float(lo[4 * i + 2]), __uint_as_float(lo[4 * i + 3])),
+                                      pack_bf16x2(__uint_as_float(hi[4 * i]), __uint_as_float(hi[4 * i + 1])),
+                                      pack_bf16x2(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])));
+                }
+                __syncwarp();
+                constexpr int kGo = 16 / kVec < 4 ? 16 / kVec : 4;      // pieces read before the first is stored
+#pragma unroll
+                for (int q0 = 0; q0 < 16; q0 += kGo * kVec) {
+                    uint4 v[kGo];
+#pragma unroll
+                    for (int q = 0; q < kGo; ++q) {
+                        const uint8_t* f = from(q0 + q * kVec + r0);
+                        if constexpr (kVec == 8) v[q] = *reinterpret_cast<const uint4*>(f);
+                        else v[q].x = *reinterpret_cast<const uint16_t*>(f);
+                    }
+#pragma unroll
+                    for (int q = 0; q < kGo; ++q) {
+                        const int r = q0 + q * kVec + r0, m = cb + 16 * h + r;
+                        uint16_t* cp = p.c + (row0 + m) * p.ldc + n;
+                        if (m < rows && whole) {
+                            if constexpr (kVec == 8) *reinterpret_cast<uint4*>(cp) = v[q];
+                            else *cp = static_cast<uint16_t>(v[q].x);
+                        } else if (kVec > 1 && m < rows) {
+                            for (int k = 0; n + k < p.N; ++k) cp[k] = reinterpret_cast<const uint16_t*>(from(r))[k];
+                        }
                     }
                 }
             }
@@ -361,8 +370,6 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
     if (kTermsPer == 1 && u.split < 0) {
         const int n0 = nt * kTileN + (warp & 3) * 32;
         if (p.c_vec == 8) store_tile<8>(p, acc, u.rows, u.row0, n0, half, lane, stage);
-        else if (p.c_vec == 4) store_tile<4>(p, acc, u.rows, u.row0, n0, half, lane, stage);
-        else if (p.c_vec == 2) store_tile<2>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         else store_tile<1>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         return;
     }
