@@ -46,6 +46,7 @@ int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8
     a.tag = next_call_tag();
     a.status = di.status;
     a.m_tile = plan.m_tile;
+    a.by_m_tile = make_fastdiv(static_cast<uint32_t>(plan.m_tile));
     a.nmc = plan.nmc;
     a.n_tiles = plan.n_tiles;
     a.k_atoms = plan.k_atoms;

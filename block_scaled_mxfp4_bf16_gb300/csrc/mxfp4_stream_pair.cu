@@ -61,7 +61,7 @@ __device__ __forceinline__ void commit_pair_if(uint32_t issue, uint64_t* bar) {
 }  // namespace
 
 __global__ void __launch_bounds__(kPairThreads, 1)
-mxfp4_stream_pair_kernel(const StreamArgs p) {
+mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t t_rows = static_cast<uint32_t>(p.m_tile) * 64u;             // half a tile's code rows, at most

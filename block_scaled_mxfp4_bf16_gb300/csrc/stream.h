@@ -64,6 +64,7 @@ struct StreamArgs {
     uint32_t a_block;
     uint32_t tmem_cols;
     int c_vec;                // elements a store: 8 where C's rows are aligned for it, else 1
+    FastDiv by_m_tile;
     uint64_t wait_limit_ns;
 };
 

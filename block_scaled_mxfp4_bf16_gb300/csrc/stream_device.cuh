@@ -126,13 +126,15 @@ struct Walk {
     // the share
     int nt, slot, row0, rows;  // weight tile; token-block tile; its first sorted row and its rows
     int k0, nk;                // 256-K steps [k0, k0 + nk) of the unit
-    int split;                 // index among the split units, -1: the whole unit in one CTA
     // the schedule
-    int units, waves, wave;    // all units; full waves of whole units; the next wave
-    int64_t s, s1, share;      // the run over the steps of the split units; steps per CTA of them
+    int waves, unit;           // full waves of whole units still to come; the next of those
+    int base, share;           // the first split unit; steps of them a CTA
+    int left, next, k_next;    // the run: steps still to come; the next unit, and its first step
     // the group the unit lies in
     int group, first, end;     // its units [first, end)
+    int upto;                  // token tiles up to its end
     int tiles, per, begin, n;  // token tiles, rows per tile, sorted rows [begin, begin + n)
+    int slot0;                 // the first tile's token-block tile
     float inv_tiles;
 };
 
@@ -145,24 +147,34 @@ template <bool kPair>
 __device__ __forceinline__ int weight_tiles(const StreamArgs& p) { return kPair ? (p.n_tiles + 1) >> 1 : p.n_tiles; }
 
 // Units are ordered by group, then weight tile, then token tile: the CTAs that work at the same
-// time share the group's weights as well as its tokens. `unit` never decreases along a walk, so the
-// group is found by stepping on from the last one, and its numbers are worked out once a group
-// (worked out again for every unit, with a search and four divisions, 6000 rows x 2880 x 2040
-// measured 56 us instead of 49).
+// time share the group's weights as well as its tokens. A unit never precedes the last one of the
+// walk, so the group is found by stepping on, and its numbers are worked out once a group. All
+// the warps of an SM walk, so every division counts where units are short: with a search and four
+// divisions for every unit, 6000 rows x 2880 x 2040 took 56 us instead of 49.
 template <bool kPair = false>
 __device__ __forceinline__ void locate(const StreamArgs& p, const int* prefix, int unit, Walk& w) {
     const int n_tiles = weight_tiles<kPair>(p);
     if (unit >= w.end) {
-        int g = w.group + 1;
-        while (prefix[g + 1] * n_tiles <= unit) ++g;
+        int g = w.group, before, after = w.upto;
+        do {
+            before = after;
+            after = prefix[++g + 1];
+        } while (after * n_tiles <= unit);
         w.group = g;
-        w.first = prefix[g] * n_tiles;
-        w.end = prefix[g + 1] * n_tiles;
-        w.tiles = prefix[g + 1] - prefix[g];
-        w.inv_tiles = 1.f / static_cast<float>(w.tiles);
+        w.upto = after;
+        w.first = before * n_tiles;
+        w.end = after * n_tiles;
+        w.tiles = after - before;
+        w.inv_tiles = __fdividef(1.f, static_cast<float>(w.tiles));
         w.begin = prefix[p.groups + 1 + g];        // the groups' first rows follow the prefix
         w.n = prefix[p.groups + 2 + g] - w.begin;
-        w.per = ((w.n + w.tiles - 1) / w.tiles + 15) / 16 * 16;   // tile_rows(n, m_tile)
+        // tile_rows(n, m_tile): 16 ceil(n / (16 tiles)), a small quotient, at most one off in fp32
+        const int unit16 = 16 * w.tiles;
+        int q = __float2int_rz(static_cast<float>(w.n - 1) * w.inv_tiles * 0.0625f);
+        if (q * unit16 >= w.n) --q;
+        else if ((q + 1) * unit16 < w.n) ++q;
+        w.per = 16 * (q + 1);
+        w.slot0 = static_cast<int>(fast_div(static_cast<uint32_t>(w.begin), p.by_m_tile)) + g;   // tile_slot(begin, g, 0, m_tile)
     }
     const int r = unit - w.first;
     int nt = w.tiles == 1 ? r : __float2int_rz(static_cast<float>(r) * w.inv_tiles);   // r / tiles, off by one at most
@@ -175,37 +187,45 @@ __device__ __forceinline__ void locate(const StreamArgs& p, const int* prefix, i
         i -= w.tiles;
     }
     w.nt = nt;
-    w.slot = tile_slot(w.begin, w.group, i, p.m_tile);
+    w.slot = w.slot0 + i;
     w.row0 = w.begin + i * w.per;
     w.rows = min(w.per, w.n - i * w.per);
 }
 
+// How `units` units fall to the CTAs: full waves of whole units, then the steps of the rest in
+// equal runs, `share` steps each.
 template <bool kPair = false>
 __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefix, int units) {
     const int grid = walkers<kPair>(), me = walker<kPair>();
     Walk w = {};
-    w.units = units;
     const bool runs = p.runs && units >= 4 * grid;
     w.waves = runs ? 0 : units / grid;
-    const int64_t steps = static_cast<int64_t>(units - w.waves * grid) * p.k_atoms;
-    w.share = (steps + grid - 1) / grid;
+    w.base = w.waves * grid;
+    const int64_t steps = static_cast<int64_t>(units - w.base) * p.k_atoms;
+    int64_t share = (steps + grid - 1) / grid;
     // a split unit costs what eight steps do (4 us: sums out, arrival, sums in): not for less, and
     // not among more than six CTAs
     if (!runs) {
-        w.share = max(w.share, static_cast<int64_t>((p.k_atoms + 5) / 6));
-        if (w.share + kSplitSteps > p.k_atoms) w.share = p.k_atoms;
+        share = max(share, static_cast<int64_t>((p.k_atoms + 5) / 6));
+        if (share + kSplitSteps > p.k_atoms) share = p.k_atoms;
     }
-    w.s = min(steps, w.share * me);
-    w.s1 = min(steps, w.s + w.share);
+    int64_t s = min(steps, share * me), s1 = min(steps, s + share);
     if (p.cluster > 1) {   // the CTAs of a cluster share one unit
         const int rank = static_cast<int>(blockIdx.x) % p.cluster;
         const int base = p.k_atoms / p.cluster, rem = p.k_atoms % p.cluster;
         w.waves = 0;
-        w.s = static_cast<int64_t>(blockIdx.x / p.cluster) * p.k_atoms + rank * base + min(rank, rem);
-        w.s1 = min(static_cast<int64_t>(units) * p.k_atoms, w.s + base + (rank < rem ? 1 : 0));
+        w.base = 0;
+        s = static_cast<int64_t>(blockIdx.x / p.cluster) * p.k_atoms + rank * base + min(rank, rem);
+        s1 = min(static_cast<int64_t>(units) * p.k_atoms, s + base + (rank < rem ? 1 : 0));
     }
+    w.share = static_cast<int>(share);
+    w.left = static_cast<int>(max(s1 - s, int64_t(0)));
+    const int u = static_cast<int>(s / p.k_atoms);
+    w.next = w.base + u;
+    w.k_next = static_cast<int>(s - static_cast<int64_t>(u) * p.k_atoms);
+    w.unit = me;
     // the group before the first unit's, by bisection
-    const int unit = w.waves ? me : static_cast<int>(w.s / p.k_atoms);
+    const int unit = w.waves > 0 ? w.unit : w.next;
     int lo = 0, hi = p.groups;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -213,28 +233,27 @@ __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefi
         else hi = mid;
     }
     w.group = lo - 1;
-    w.end = 0;
+    w.upto = prefix[lo];
     return w;
 }
 
 template <bool kPair = false>
 __device__ __forceinline__ bool next_share(const StreamArgs& p, const int* prefix, Walk& w) {
-    const int grid = walkers<kPair>();
-    if (w.wave < w.waves) {
-        locate<kPair>(p, prefix, w.wave * grid + walker<kPair>(), w);
-        w.split = -1;
+    if (w.waves > 0) {
+        locate<kPair>(p, prefix, w.unit, w);
         w.k0 = 0;
         w.nk = p.k_atoms;
-        ++w.wave;
+        --w.waves;
+        w.unit += walkers<kPair>();
         return true;
     }
-    if (w.s >= w.s1) return false;
-    const int u = static_cast<int>(w.s / p.k_atoms);
-    locate<kPair>(p, prefix, w.waves * grid + u, w);
-    w.k0 = static_cast<int>(w.s - static_cast<int64_t>(u) * p.k_atoms);
-    w.nk = static_cast<int>(min(static_cast<int64_t>(p.k_atoms - w.k0), w.s1 - w.s));
-    w.split = w.nk == p.k_atoms ? -1 : u;
-    w.s += w.nk;
+    if (w.left <= 0) return false;
+    locate<kPair>(p, prefix, w.next, w);
+    w.k0 = w.k_next;
+    w.nk = min(p.k_atoms - w.k0, w.left);
+    w.left -= w.nk;
+    ++w.next;
+    w.k_next = 0;             // whatever is left of the run begins in the next unit
     return true;
 }
 
@@ -282,9 +301,9 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 // A whole unit's accumulator (lane = weight row, column = token) -> bf16 C. A warp owns 32 weight
 // rows; 16 tokens at a time it packs its fragments, transposes them through 1 KB of shared memory and
 // stores kVec elements a lane: one instruction writes 64 contiguous bytes of each of kVec rows of C.
-// Where C's rows are aligned for it kVec is 8, else 1: 22672 rows of 5664 elements after K = 160 took
-// 145 us and 169. Rows of 5668 took 172 us with 8-byte stores and 170 with single elements, rows of
-// 5666 226 us with 4-byte stores and 170. The 1 KB hold 16 rows of 64 bytes, the 16-byte piece c of
+// Where C's rows are aligned for it kVec is 8, else 1: 22672 rows of 5664 elements after K = 160 take
+// 108 us and 131. Nothing between pays: rows of 5668 took 172 us with 8-byte stores and 170 with single
+// elements, rows of 5666 226 us with 4-byte stores and 170. The 1 KB hold 16 rows of 64 bytes, the 16-byte piece c of
 // row r at c ^ (r / 2 % 4), so that both the 8 rows a matrix is stored to and the pieces eight lanes read
 // touch all banks. (2-byte stores in the lanes of 16-byte ones took four times as long where C's rows
 // are not aligned; 8 tokens at a time, every piece waited for the one before.)
@@ -367,7 +386,7 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
                                            int lane, volatile uint32_t* last_flag, uint8_t* stage) {
     constexpr int kTok = 16 / kTermsPer;         // tokens per 16 columns
     constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
-    if (kTermsPer == 1 && u.split < 0) {
+    if (kTermsPer == 1 && u.nk == p.k_atoms) {
         const int n0 = nt * kTileN + (warp & 3) * 32;
         if (p.c_vec == 8) store_tile<8>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         else store_tile<1>(p, acc, u.rows, u.row0, n0, half, lane, stage);
@@ -379,14 +398,15 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
     const int rank = kPair ? static_cast<int>(blockIdx.x & 1u) : 0;
     const int64_t me = walker<kPair>();
     const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;
-    const int64_t unit_step = static_cast<int64_t>(u.split) * p.k_atoms;
+    const bool split = u.nk != p.k_atoms;
     bool last = true;
-    int64_t c_first = 0, c_last = 0;
-    if (u.split >= 0) {
+    int64_t unit_step = 0, c_first = 0, c_last = 0;   // the unit's first step, the walkers that share it
+    if (split) {
+        unit_step = static_cast<int64_t>(u.next - 1 - u.base) * p.k_atoms;   // the walk has passed the unit
         c_first = unit_step / u.share;
         c_last = (unit_step + p.k_atoms - 1) / u.share;
         const uint32_t others = static_cast<uint32_t>(c_last - c_first);
-        const int slot = u.k0 == 0 && u.s - u.nk != u.share * me ? 1 : 0;
+        const int slot = unit_step > u.share * me ? 1 : 0;
         volatile uint32_t* flag = last_flag + 2 * slot;
         unsigned long long* counter = p.counters + (c_first * kRanks + rank);   // a split unit is named by its first walker
         if (threadIdx.x == 128)
@@ -419,7 +439,7 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
         float own[kTok], v[kTok];
         const int m0 = cb / kTermsPer;
         load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), own);
-        if (u.split < 0) {
+        if (!split) {
 #pragma unroll
             for (int i = 0; i < kTok; ++i) v[i] = own[i];
         } else {
