@@ -76,17 +76,22 @@ __device__ __forceinline__ void gate_pair(uint32_t g, uint32_t u, float* v) {
     v[1] = silu(__uint_as_float(g & 0xFFFF0000u)) * __uint_as_float(u & 0xFFFF0000u);
 }
 
-// A warp takes `step` consecutive 1x32 blocks of one sorted row (all of them when there are rows
-// enough to fill the GPU), a lane per block, 32 at a time with the next 32 on their way: the row's
-// group and source are looked up once. Rows of at most 16 or 8 blocks are taken two or four at a time
-// (kRows), each by its share of the lanes. Blocks past K become zero codes; an index outside
-// [0, tokens) gives a row of zeros. kGated: a row of a holds [g, u], K each, and silu(g) * u is
-// quantized. 16384 x 7168 bf16 (half of it from L2) take 45 us: the L1 cache's tag lookups (78 %) and
-// the integer pipe of the encoding share the blame. Each block takes the offsets to shared memory once:
-// when every warp looked its row's group up in L2, all of them in the same few sectors, 22672 rows of
-// K = 160 took 31 us, now 10.
-template <bool kGated, int kRows>
-__global__ void __launch_bounds__(256)
+// A warp takes `step` consecutive 1x32 blocks of four sorted rows (all of them when there are rows
+// enough to fill the GPU), eight lanes a row, a lane per block: the rows' groups and sources are looked
+// up once, and whole 256-K steps leave no lane without a block. Blocks past K become zero codes; an index
+// outside [0, tokens) gives a row of zeros. kGated: a row of a holds [g, u], K each, and silu(g) * u is
+// quantized.
+//
+// 16384 x 7168 bf16 (half of it from L2) take 45 us: the L1 cache's tag lookups (78 %) and the integer
+// pipe of the encoding share the blame. Gated, 26204 x 1200 take 42 us, 3 TB/s: the two
+// transcendental instructions a value (a quarter of a warp a clock) are half of that. Eight lanes a row
+// against 32: 26204 x 1200 gated, product included, 89 -> 54 us. The next blocks are loaded while these
+// are encoded, but not in the gated kernel, whose registers are worth more (128 a thread, 16 warps an SM).
+// Each block takes the offsets to shared memory once: when every warp looked its row's group up in L2,
+// all of them in the same few sectors, 22672 rows of K = 160 took 31 us, now 10.
+constexpr int kQuantRows = 4, kQuantWidth = 32 / kQuantRows;   // rows a warp; lanes a row
+template <bool kGated>
+__global__ void __launch_bounds__(256, kGated ? 2 : 4)
 quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K, int64_t lda,
                        const int32_t* index, const int32_t* offsets, int groups, int rows, int m_tile, int k_atoms,
                        uint32_t a_block, uint8_t* __restrict__ blocks, int parts, int step) {
@@ -98,14 +103,13 @@ quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K
         for (int i = threadIdx.x; i <= groups; i += blockDim.x) s_offsets[i] = min(max(__ldcg(offsets + i), 0), rows);
         __syncthreads();
     }
-    constexpr int kWidth = 32 / kRows;          // lanes per row
-    const int lane = threadIdx.x & 31, sub = lane / kWidth;
+    const int lane = threadIdx.x & 31, sub = lane / kQuantWidth;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int64_t row_sets = (static_cast<int64_t>(rows) + kRows - 1) / kRows;
+    const int64_t row_sets = (static_cast<int64_t>(rows) + kQuantRows - 1) / kQuantRows;
     for (int64_t it = w; it < row_sets * parts; it += warps) {
         const int64_t set = it / parts;
-        const int r = static_cast<int>(set) * kRows + sub;
+        const int r = static_cast<int>(set) * kQuantRows + sub;
         const int kb0 = static_cast<int>(it - set * parts) * step;
         const int kb1 = min(k_atoms * 8, kb0 + step);
         const int64_t src = r < rows ? (index ? static_cast<int64_t>(index[r]) : r) : -1;
@@ -141,13 +145,14 @@ quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K
                 if constexpr (kGated) load_block32_upto(row + K + k, K - k, *reinterpret_cast<uint32_t(*)[16]>(&next[16]));
             }
         };
-        load(kb0 + lane % kWidth);
-        for (int base = kb0; base < kb1; base += kWidth) {
-            const int kb = base + lane % kWidth;
+        if (!kGated) load(kb0 + lane % kQuantWidth);
+        for (int base = kb0; base < kb1; base += kQuantWidth) {
+            const int kb = base + lane % kQuantWidth;
             uint32_t v[kWords], out[4] = {0u, 0u, 0u, 0u}, byte = 0u;
+            if (kGated) load(kb);
 #pragma unroll
             for (int i = 0; i < kWords; ++i) v[i] = next[i];
-            load(kb + kWidth);
+            if (!kGated) load(kb + kQuantWidth);
             if (present && static_cast<int64_t>(kb) * 32 < K && kb < kb1) {
                 if constexpr (kGated) {
                     float h[32];
@@ -725,24 +730,17 @@ uint64_t next_call_tag() {
 cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,
                                    const int32_t* offsets, int groups, int rows, bool gated, const StreamPlan& plan,
                                    uint8_t* blocks, cudaStream_t s) {
-    // as many parts of a row as make enough warps for every SM, whole rows beyond that, short rows
-    // several to a warp
-    const int chunks = (plan.k_atoms * 8 + 31) / 32;
-    const int64_t want = (int64_t(4096) + rows - 1) / rows;
-    const int per = static_cast<int>(want >= chunks ? 1 : chunks / want);
-    const int parts = (chunks + per - 1) / per;
-    const int at_once = plan.k_atoms == 1 ? 4 : plan.k_atoms == 2 ? 2 : 1;
-    int64_t grid = ((static_cast<int64_t>(rows) + at_once - 1) / at_once * parts + 7) / 8;
+    // as many parts of a row as make enough warps for every SM, whole rows beyond that
+    const int64_t sets = (static_cast<int64_t>(rows) + kQuantRows - 1) / kQuantRows;
+    const int64_t want = (int64_t(4096) + sets - 1) / sets;
+    const int per = static_cast<int>(want >= plan.k_atoms ? 1 : plan.k_atoms / want);   // 256-K steps a part
+    const int parts = (plan.k_atoms + per - 1) / per;
+    int64_t grid = (sets * parts + 7) / 8;
     if (grid > 65535) grid = 65535;
-    auto* kernel = gated ? (at_once == 4   ? quantize_groups_kernel<true, 4>
-                            : at_once == 2 ? quantize_groups_kernel<true, 2>
-                                           : quantize_groups_kernel<true, 1>)
-                         : (at_once == 4   ? quantize_groups_kernel<false, 4>
-                            : at_once == 2 ? quantize_groups_kernel<false, 2>
-                                           : quantize_groups_kernel<false, 1>);
+    auto* kernel = gated ? quantize_groups_kernel<true> : quantize_groups_kernel<false>;
     return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(256),
                       static_cast<size_t>(groups + 1) * sizeof(int), s, a, tokens, K, lda, index, offsets, groups,
-                      rows, plan.m_tile, plan.k_atoms, plan.a_block, blocks, parts, per * 32);
+                      rows, plan.m_tile, plan.k_atoms, plan.a_block, blocks, parts, per * 8);
 }
 
 cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx, const StreamPlan& plan,
