@@ -53,7 +53,6 @@ int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8
     a.stages = plan.stages;
     a.cluster = plan.cluster;
     a.accs = plan.accs;
-    a.runs = plan.runs;
     a.a_block = plan.a_block;
     a.tmem_cols = plan.tmem_cols;
     a.wait_limit_ns = wait_limit_ns();

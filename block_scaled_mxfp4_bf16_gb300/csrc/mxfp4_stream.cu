@@ -12,8 +12,7 @@
 // begin the next). A unit cut between CTAs is added up by whichever of them arrives last, in the
 // order of K from the fp32 sums that the others left in the workspace: no CTA waits for another,
 // and the result does not depend on the order of arrival. With few units (decoding) there is no
-// full wave and every SM streams an equal share of the weights. (StreamArgs::runs: no waves, all
-// units cut into one run per CTA; see make_stream_plan.)
+// full wave and every SM streams an equal share of the weights.
 //
 // Warps: 0 copies (weights and token blocks, one mbarrier per stage), 1 tensor memory and the
 // MMAs (two accumulators: the next unit's MMAs run while the last one is stored), 4-11 the
@@ -644,17 +643,18 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
         // experts x 4096 x 2048: 12.0 us against 12.2 unfused and 4 us less of the host's time; 4 rows
         // an expert cost 43.1 against 41.6 (gated 51.8 against 42.6).
         p.fused = mean <= 2;
-        p.m_tile = p.fused ? 32 : mean <= 48 ? 64 : mean <= 256 ? 128 : 192;
-        // Groups of several tiles with short K: no waves, every CTA takes the tiles of a weight tile
-        // one after the other and rereads its weights from L2, where all CTAs' fit (152 x 12 steps
-        // are 32 MB; 6000 rows in 48 groups x 2880 x 2040 53.7 -> 50.0 us, but 16384 rows in 16 groups
-        // x 4096 x 7168, 28 steps, 240 -> 428). In waves the CTAs of a group read a weight at the
-        // same time, once from memory, but then wait for the same few weights together.
-        p.runs = mean > 48 && p.k_atoms <= 12;
+        // 128 tokens a tile, 192 where groups are larger. 7200 rows in 48 groups (150 each) x 2880 x 1024:
+        // 30.3 us with 192, 33.4 with 128; 12800 rows (266 each) 41.1 and 42.1. Tiles of 64 for the small
+        // groups of decoding gained nothing: 480 rows x 4096 x 4096 71.7 us and 70.1 with 128.
+        p.m_tile = p.fused ? 32 : mean <= 128 ? 128 : 192;
     }
     p.cluster = 1;
-    // Large groups: two CTAs to a unit (16384 rows in 16 groups x 4096 x 7168 235 -> 217 us).
-    p.pair = terms == 1 && p.m_tile > 128 && p.n_tiles > 1;
+    // Large groups: two CTAs to a unit, which halves the token bytes an SM takes in, where K is long enough
+    // to pay for what a pair does once a unit: 16384 rows in 16 groups x 4096 x 7168 211 us against 232,
+    // x 4096 120 against 136, x 2048 80 both; 22672 rows in 52 groups x 5664 x 1536 128 against 122, x 160
+    // 108 against 72.
+    constexpr int kPairSteps = 8;
+    p.pair = terms == 1 && p.m_tile > 128 && p.n_tiles > 1 && p.k_atoms >= kPairSteps;
     p.nmc = (p.m_tile + 127) / 128;
     p.a_block = static_cast<uint32_t>(p.m_tile) * 128u + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
     size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 + 8 * kEpiStage +

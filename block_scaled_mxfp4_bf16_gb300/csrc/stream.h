@@ -58,7 +58,6 @@ struct StreamArgs {
     uint32_t* status;
     int groups, rows, N;      // rows: token-block rows (grouped) or tokens * terms (weight-only)
     int m_tile, nmc, n_tiles, k_atoms, stages;
-    int runs;                 // no waves of whole units where units are many (make_stream_plan)
     int accs;                 // accumulators in tensor memory: 2, or 1 for CTAs with one share
     int cluster;              // CTAs that share a unit through their cluster (weight-only), or 1
     uint32_t a_block;
@@ -69,7 +68,7 @@ struct StreamArgs {
 };
 
 struct StreamPlan {
-    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, runs, cluster, accs;
+    int m_tile, nmc, stages, ctas, k_atoms, n_tiles, cluster, accs;
     int pair;                 // two CTAs to a unit of two weight tiles (mxfp4_stream_pair.cu)
     int fused;                // tokens written by the product's own warps, no launch before it
     uint32_t a_block, tmem_cols;

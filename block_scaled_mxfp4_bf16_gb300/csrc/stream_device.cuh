@@ -198,17 +198,14 @@ template <bool kPair = false>
 __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefix, int units) {
     const int grid = walkers<kPair>(), me = walker<kPair>();
     Walk w = {};
-    const bool runs = p.runs && units >= 4 * grid;
-    w.waves = runs ? 0 : units / grid;
+    w.waves = units / grid;
     w.base = w.waves * grid;
     const int64_t steps = static_cast<int64_t>(units - w.base) * p.k_atoms;
     int64_t share = (steps + grid - 1) / grid;
     // a split unit costs what eight steps do (4 us: sums out, arrival, sums in): not for less, and
     // not among more than six CTAs
-    if (!runs) {
-        share = max(share, static_cast<int64_t>((p.k_atoms + 5) / 6));
-        if (share + kSplitSteps > p.k_atoms) share = p.k_atoms;
-    }
+    share = max(share, static_cast<int64_t>((p.k_atoms + 5) / 6));
+    if (share + kSplitSteps > p.k_atoms) share = p.k_atoms;
     int64_t s = min(steps, share * me), s1 = min(steps, s + share);
     if (p.cluster > 1) {   // the CTAs of a cluster share one unit
         const int rank = static_cast<int>(blockIdx.x) % p.cluster;
