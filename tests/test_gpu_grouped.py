@@ -232,3 +232,36 @@ def test_empty_calls_are_no_ops():
     mx.mxfp4_grouped_gemm(torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda"), packed, offsets_of([0, 0]), 128, c=c)
     torch.cuda.synchronize()
     assert bool((store == -7.0).all())
+
+
+# Large groups and K of eight steps or more: two CTAs to a unit. An odd number of weight tiles, ragged N,
+# groups of one row between large ones, rows outside the groups and a C whose rows are not aligned.
+@pytest.mark.parametrize("sizes", [[600, 0, 1, 193, 384], [1030], [150, 129, 400, 17, 0, 0]])
+@pytest.mark.parametrize("N,K,ldc_pad", [(384, 2048, 0), (300, 1800, 1), (137, 2304, 8), (1152, 2056, 2)])
+def test_pairs_of_ctas(sizes, N, K, ldc_pad):
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    first, tail = 2, 3
+    R = first + sum(sizes) + tail
+    packed, w = weights(len(sizes), N, K, seed=9)
+    a = workloads.random_bf16(R, K, seed=3).cuda()
+    c, store = canary_out(R, N, ldc_pad)
+    mx.mxfp4_grouped_gemm(a, packed, offsets_of(sizes, first), N, c=c)
+    assert mx.mxfp4_device_status() == 0
+    assert outside_untouched(c, store)
+    assert bool((c[:first] == -7.0).all()) and bool((c[R - tail:] == -7.0).all()), "rows of no group were written"
+    check(c, quantized(a), w, sizes, first)
+    again, _ = canary_out(R, N, ldc_pad)
+    mx.mxfp4_grouped_gemm(a, packed, offsets_of(sizes, first), N, c=again)
+    assert torch.equal(c.view(torch.int16), again.view(torch.int16)), "not reproducible"
+
+
+@pytest.mark.parametrize("offsets", [[0, 900, 300, 800], [0, 400, 801, 800], [-1, 200, 400, 800], [800, 400, 200, 0]])
+def test_broken_offsets_of_large_groups_leave_c_unwritten(offsets):
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    N, K, tokens = 256, 2048, 800
+    packed, _ = weights(3, N, K, seed=5)
+    a = workloads.random_bf16(tokens, K, seed=4).cuda()
+    c, store = canary_out(tokens, N, 0)
+    mx.mxfp4_grouped_gemm(a, packed, torch.tensor(offsets, dtype=torch.int32).cuda(), N, c=c)
+    assert mx.mxfp4_device_status() == 0
+    assert bool((store == -7.0).all())
