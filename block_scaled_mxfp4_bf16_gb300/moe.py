@@ -10,16 +10,18 @@ from typing import NamedTuple
 
 import torch
 
-from . import (_WS, Mxfp4Error, _check, _check_packed, _dev, _on, _raw_stream, _stream, _workspace, load_library,
-               mxfp4_prepack_b, mxfp4_prepack_b_size)
+from . import (_PACKED_NEED, _WS, Mxfp4Error, _check, _check_packed, _dev, _on, _raw_stream, _stream, _workspace,
+               load_library, mxfp4_prepack_b, mxfp4_prepack_b_size)
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _NEED: dict = {}
+# without the check for a context, which a tensor on the device has already
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _need(query: str, *sizes: int) -> int:
-    """A size query of the library, remembered per argument list and current device: it depends only on those."""
-    key = (query, *sizes, torch.cuda.current_device())
+def _need(query: str, device: int, *sizes: int) -> int:
+    """A size query of the library for the current device, remembered: it depends on its arguments only."""
+    key = (query, device, *sizes)
     need = _NEED.get(key)
     if need is None:
         need = getattr(load_library(), query)(*sizes)
@@ -28,15 +30,15 @@ def _need(query: str, *sizes: int) -> int:
     return need
 
 
-def _begin(t: torch.Tensor, name: str, stream) -> int:
-    """The stream of a call whose first operand is `t`, which must live on the current CUDA device."""
+def _begin(t: torch.Tensor, name: str, stream) -> tuple:
+    """(stream, device) of a call whose first operand is `t`, which must live on the current CUDA device."""
     d = t.get_device()
-    if d < 0 or d != torch.cuda.current_device():
+    if d < 0 or d != _device():
         _dev(t, name)
-    return _raw_stream(d) if stream is None and _raw_stream is not None else _stream(stream)
+    return _raw_stream(d) if stream is None and _raw_stream is not None else _stream(stream), d
 
 
-def _scratch(workspace, need: int, t: torch.Tensor, stream, st: int) -> tuple:
+def _scratch(workspace, need: int, t: torch.Tensor, stream, st: int, device: int) -> tuple:
     """(pointer, bytes) of the caller's workspace, or of the binding's own for this stream."""
     if workspace is not None:
         _on(workspace, t.device, "workspace")
@@ -45,7 +47,7 @@ def _scratch(workspace, need: int, t: torch.Tensor, stream, st: int) -> tuple:
     elif need == 0:
         return None, 0
     else:
-        workspace = _WS.get((t.get_device(), st))
+        workspace = _WS.get((device, st))
         if workspace is None or workspace.nbytes < need:
             workspace = _workspace(t.device, need, stream, st)
     return workspace.data_ptr(), workspace.nbytes
@@ -75,7 +77,7 @@ _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", N
 def _empty(shape: tuple, dtype: torch.dtype, t: torch.Tensor, stream) -> torch.Tensor:
     """An output of a call, on t's (the current) device: its memory belongs to the stream that writes it."""
     if stream is None:
-        if _empty_strided is not None and t.get_device() >= 0:
+        if _empty_strided is not None:
             return _empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
         return torch.empty(shape, dtype=dtype, device=t.device)
     if not isinstance(stream, torch.cuda.Stream):
@@ -96,7 +98,7 @@ def _out(out: torch.Tensor | None, shape: tuple, t: torch.Tensor, name: str, str
 
 def _index(t: torch.Tensor, shape: tuple, like: torch.Tensor, name: str, dtype=_I32) -> int:
     """Pointer of a dense index (or weight) tensor on the operands' device."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != like.get_device():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {list(shape)} on {like.device}")
     return t.data_ptr()
 
@@ -105,15 +107,15 @@ def mxfp4_gemv(x: torch.Tensor, packed_b: torch.Tensor, N: int, y: torch.Tensor 
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Y [M, N] bf16 = x . W^T for a few tokens, x [M, K] kept in bf16 (not quantized), W the MXFP4
     weights of `packed_b` (mxfp4_prepack_b): the weight-only product, on the weights mxfp4_gemm uses."""
-    st = _begin(x, "x", stream)
+    st, device = _begin(x, "x", stream)
     ldx = _bf16_rows(x, "x")
     M, K = x.shape
     need = 0
     if M and N:
         _check_packed(packed_b, N, K, x.device)
-        need = _need("mxfp4_gemv_workspace_size", M, N, K)
+        need = _need("mxfp4_gemv_workspace_size", device, M, N, K)
     y, ldy = _out(y, (M, N), x, "y", stream)
-    ws, ws_bytes = _scratch(workspace, need, x, stream, st)
+    ws, ws_bytes = _scratch(workspace, need, x, stream, st, device)
     status = load_library().mxfp4_gemv(x.data_ptr(), M, K, ldx, packed_b.data_ptr(), N, y.data_ptr(), ldy, ws, ws_bytes,
                                        st)
     if status:
@@ -148,7 +150,7 @@ def mxfp4_grouped_gemm(a: torch.Tensor, packed_b: torch.Tensor, offsets: torch.T
     [E+1] and `rows` [R]: int32 on the device, as mxfp4_moe_route returns them (rows None: row r of
     `a`). gated: a's rows are [g, u] and silu(g) * u is the product's input, K = a.shape[1] / 2.
     Rows of C that belong to no expert are not written."""
-    st = _begin(a, "a", stream)
+    st, device = _begin(a, "a", stream)
     lda = _bf16_rows(a, "a")
     tokens, K = a.shape
     if gated:
@@ -160,7 +162,7 @@ def mxfp4_grouped_gemm(a: torch.Tensor, packed_b: torch.Tensor, offsets: torch.T
     E = packed_b.shape[0]
     if E and N:
         _check_packed(packed_b, N, K, a.device)
-        if packed_b.nbytes != E * _need("mxfp4_prepack_b_size", N, K):
+        if packed_b.nbytes != E * _PACKED_NEED[(N, K)]:
             raise ValueError(f"packed_b's rows must have mxfp4_prepack_b_size({N}, {K}) bytes")
     offsets_ptr = _index(offsets, (E + 1,), a, "offsets")
     if rows is None:
@@ -169,8 +171,8 @@ def mxfp4_grouped_gemm(a: torch.Tensor, packed_b: torch.Tensor, offsets: torch.T
         R = rows.shape[0] if rows.dim() == 1 else -1
         rows_ptr = _index(rows, (R,), a, "rows")
     c, ldc = _out(c, (R, N), a, "c", stream)
-    need = _need("mxfp4_grouped_gemm_workspace_size", R, E, N, K) if R and E and N else 0
-    ws, ws_bytes = _scratch(workspace, need, a, stream, st)
+    need = _need("mxfp4_grouped_gemm_workspace_size", device, R, E, N, K) if R and E and N else 0
+    ws, ws_bytes = _scratch(workspace, need, a, stream, st, device)
     status = load_library().mxfp4_grouped_gemm(a.data_ptr(), tokens, K, lda, rows_ptr, offsets_ptr, E,
                                                packed_b.data_ptr(), N, c.data_ptr(), R, ldc, 1 if gated else 0, ws,
                                                ws_bytes, st)
@@ -198,7 +200,7 @@ def mxfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, work
     """Top-k routing of logits [T, E] (fp32 or bf16): the k largest per token (ties to the lower index;
     -inf and NaN are masks), their softmax weights (over the k, or with renormalize=False over all
     experts), and the token-expert pairs grouped by expert."""
-    st = _begin(logits, "logits", stream)
+    st, device = _begin(logits, "logits", stream)
     dtype = _LOGIT_TYPES.get(logits.dtype)
     if dtype is None:
         raise ValueError("logits must be an fp32 or bf16 tensor")
@@ -206,12 +208,17 @@ def mxfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, work
     T, E = logits.shape
     if not 1 <= k <= min(E, 32):
         raise ValueError(f"k must lie in 1 .. min(E, 32) = {min(E, 32)}")
-    weights = _empty((T, k), _F32, logits, stream)
-    experts = _empty((T, k), _I32, logits, stream)
-    offsets = _empty((E + 1,), _I32, logits, stream)
-    rows = _empty((T * k,), _I32, logits, stream)
-    slots = _empty((T, k), _I32, logits, stream)
-    ws, ws_bytes = _scratch(workspace, _need("mxfp4_moe_route_workspace_size", T, E), logits, stream, st)
+    if stream is None and _empty_strided is not None:
+        weights = _empty_strided((T, k), (k, 1), _F32)
+        experts = _empty_strided((T, k), (k, 1), _I32)
+        offsets = _empty_strided((E + 1,), (1,), _I32)
+        rows = _empty_strided((T * k,), (1,), _I32)
+        slots = _empty_strided((T, k), (k, 1), _I32)
+    else:
+        weights, experts, offsets, rows, slots = (
+            _empty(shape, dtype, logits, stream)
+            for shape, dtype in (((T, k), _F32), ((T, k), _I32), ((E + 1,), _I32), ((T * k,), _I32), ((T, k), _I32)))
+    ws, ws_bytes = _scratch(workspace, _need("mxfp4_moe_route_workspace_size", device, T, E), logits, stream, st, device)
     status = load_library().mxfp4_moe_route(logits.data_ptr(), dtype, T, E, ld, k, 0 if renormalize else 1,
                                             weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(),
                                             rows.data_ptr(), slots.data_ptr(), ws, ws_bytes, st)
@@ -224,7 +231,7 @@ def mxfp4_moe_combine(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tenso
                       stream=None) -> torch.Tensor:
     """out [T, N] bf16 = sum over j of weights[t, j] * y[slots[t, j]] (fp32 sums), y [R, N] bf16 in the
     grouped order; a slot outside [0, R) adds nothing."""
-    st = _begin(y, "y", stream)
+    st, _ = _begin(y, "y", stream)
     ldy = _bf16_rows(y, "y")
     R, N = y.shape
     if slots.dim() != 2:
