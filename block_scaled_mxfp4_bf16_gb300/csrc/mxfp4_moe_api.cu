@@ -47,6 +47,8 @@ int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8
     a.status = di.status;
     a.m_tile = plan.m_tile;
     a.by_m_tile = make_fastdiv(static_cast<uint32_t>(plan.m_tile));
+    a.by_k_atoms = make_fastdiv(static_cast<uint32_t>(plan.k_atoms));
+    a.by_walkers = make_fastdiv(static_cast<uint32_t>(plan.pair ? plan.ctas / 2 : plan.ctas));
     a.nmc = plan.nmc;
     a.n_tiles = plan.n_tiles;
     a.k_atoms = plan.k_atoms;

@@ -63,7 +63,7 @@ struct StreamArgs {
     uint32_t a_block;
     uint32_t tmem_cols;
     int c_vec;                // elements a store: 8 where C's rows are aligned for it, else 1
-    FastDiv by_m_tile;
+    FastDiv by_m_tile, by_k_atoms, by_walkers;   // walkers: CTAs, or pairs of them
     uint64_t wait_limit_ns;
 };
 

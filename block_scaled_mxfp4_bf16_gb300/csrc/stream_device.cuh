@@ -192,16 +192,19 @@ __device__ __forceinline__ void locate(const StreamArgs& p, const int* prefix, i
     w.rows = min(w.per, w.n - i * w.per);
 }
 
+__device__ __forceinline__ bool narrow(int64_t v) { return (v >> 31) == 0; }
+
 // How `units` units fall to the CTAs: full waves of whole units, then the steps of the rest in
-// equal runs, `share` steps each.
+// equal runs, `share` steps each. Every warp works it out before its first copy can start: divisions
+// (three of them of 64 bits) and a bisection of the groups took 1700 clocks.
 template <bool kPair = false>
 __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefix, int units) {
     const int grid = walkers<kPair>(), me = walker<kPair>();
     Walk w = {};
-    w.waves = units / grid;
+    w.waves = static_cast<int>(fast_div(static_cast<uint32_t>(units), p.by_walkers));
     w.base = w.waves * grid;
     const int64_t steps = static_cast<int64_t>(units - w.base) * p.k_atoms;
-    int64_t share = (steps + grid - 1) / grid;
+    int64_t share = narrow(steps + grid) ? fast_div(static_cast<uint32_t>(steps) + grid - 1, p.by_walkers) : (steps + grid - 1) / grid;
     // a split unit costs what eight steps do (4 us: sums out, arrival, sums in): not for less, and
     // not among more than six CTAs
     share = max(share, static_cast<int64_t>((p.k_atoms + 5) / 6));
@@ -217,20 +220,18 @@ __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefi
     }
     w.share = static_cast<int>(share);
     w.left = static_cast<int>(max(s1 - s, int64_t(0)));
-    const int u = static_cast<int>(s / p.k_atoms);
+    const int u = static_cast<int>(narrow(s) ? fast_div(static_cast<uint32_t>(s), p.by_k_atoms) : s / p.k_atoms);
     w.next = w.base + u;
     w.k_next = static_cast<int>(s - static_cast<int64_t>(u) * p.k_atoms);
     w.unit = me;
-    // the group before the first unit's, by bisection
+    // the group before the first unit's, which is as many as the groups that end at or before it
     const int unit = w.waves > 0 ? w.unit : w.next;
-    int lo = 0, hi = p.groups;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] * weight_tiles<kPair>(p) <= unit) lo = mid;
-        else hi = mid;
-    }
-    w.group = lo - 1;
-    w.upto = prefix[lo];
+    int before = 0;
+    for (int g = 1 + static_cast<int>(threadIdx.x & 31); g < p.groups; g += 32)
+        before += prefix[g] * weight_tiles<kPair>(p) <= unit ? 1 : 0;
+    before = static_cast<int>(__reduce_add_sync(0xffffffffu, before));
+    w.group = before - 1;
+    w.upto = prefix[before];
     return w;
 }
 
