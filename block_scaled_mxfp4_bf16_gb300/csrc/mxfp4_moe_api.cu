@@ -35,7 +35,7 @@ StreamArgs stream_args(const void* packed_b, int64_t N, int64_t K, void* c, int6
     a.ldc = ldc;
     a.N = static_cast<int>(N);
     a.K = K;
-    a.c_vec = aligned(c, 16) && ldc % 8 == 0 ? 8 : 1;
+    a.c_wide = aligned(c, 16) && ldc % 8 == 0 ? 1 : 0;
     return a;
 }
 

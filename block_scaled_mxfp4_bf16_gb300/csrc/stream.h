@@ -62,7 +62,7 @@ struct StreamArgs {
     int cluster;              // CTAs that share a unit through their cluster (weight-only), or 1
     uint32_t a_block;
     uint32_t tmem_cols;
-    int c_vec;                // elements a store: 8 where C's rows are aligned for it, else 1
+    int c_wide;               // C's rows are aligned to 16 bytes
     FastDiv by_m_tile, by_k_atoms, by_walkers;   // walkers: CTAs, or pairs of them
     uint64_t wait_limit_ns;
 };

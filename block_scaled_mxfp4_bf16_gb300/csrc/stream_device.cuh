@@ -296,34 +296,62 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                  : "memory");
 }
 
-// A whole unit's accumulator (lane = weight row, column = token) -> bf16 C. A warp owns 32 weight
-// rows; 16 tokens at a time it packs its fragments, transposes them through 1 KB of shared memory and
-// stores kVec elements a lane: one instruction writes 64 contiguous bytes of each of kVec rows of C.
-// Where C's rows are aligned for it kVec is 8, else 1: 22672 rows of 5664 elements after K = 160 take
-// 108 us and 131. Nothing between pays: rows of 5668 took 172 us with 8-byte stores and 170 with single
-// elements, rows of 5666 226 us with 4-byte stores and 170. The 1 KB hold 16 rows of 64 bytes, the 16-byte piece c of
-// row r at c ^ (r / 2 % 4), so that both the 8 rows a matrix is stored to and the pieces eight lanes read
-// touch all banks. (2-byte stores in the lanes of 16-byte ones took four times as long where C's rows
-// are not aligned; 8 tokens at a time, every piece waited for the one before.)
-template <int kVec>
-__device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, int rows, int64_t row0, int n0, int half,
+// A whole unit's accumulator (lane = weight row, column = token) -> bf16 C, 32 tokens at a time; a warp
+// owns 32 weight rows. Two forms, by the alignment of C's rows:
+//   16 bytes : a warp packs its fragments, transposes 16 tokens at a time through 1 KB of shared memory and
+//              stores 8 elements a lane, one instruction 64 contiguous bytes of each of 8 rows of C. The 1 KB
+//              hold 16 rows of 64 bytes, the 16-byte piece c of row r at c ^ (r / 2 % 4), so that both the
+//              8 rows a matrix is stored to and the pieces eight lanes read touch all banks.
+//   less     : a lane stores its weight row's element of one token after the other, 64 contiguous bytes
+//              an instruction. (Stores of 4 or 8 bytes where the rows allow them gained nothing.)
+// What counts is the chain of dependent steps, 650 clocks for 32 tokens when every store had its own branches
+// (28 of them for tensor memory), so whole tiles take a path without a branch, and the two warps
+// of 32 weight rows share the tokens to 16. 22672 rows in 52 groups x 5664 x 160: 71 us with branches, 63
+// without, 60 with even shares; x 5665 90 through shared memory, 86 without it.
+template <bool kWide>
+__device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, int tokens, int64_t row0, int n0, int half,
                                            int lane, uint8_t* stage) {
-    constexpr int kLanes = 32 / kVec;              // lanes per row of C
-    const uint32_t put = smem_addr(stage) + static_cast<uint32_t>((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
-    const int r0 = lane / kLanes, at = (lane % kLanes) * kVec, n = n0 + at;
-    const bool whole = n + kVec <= p.N;
-    auto from = [&](int r) -> const uint8_t* {     // this lane's elements of row r of the 16
-        return stage + r * 64 + ((((at >> 3) ^ (r >> 1)) & 3) << 4) + (at & 7) * 2;
-    };
-    for (int cb = half * 32; cb < rows; cb += 64) {
-        uint32_t lo[16], hi[16];
-        tmem_load_frag32(trow + static_cast<uint32_t>(cb), lo);
-        tmem_load_frag32(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
-        tmem_load_wait();
+    if constexpr (!kWide) {
+        const int n = n0 + lane;
+        uint16_t* cp = p.c + (row0 + half * 32) * p.ldc + n;
+        for (int cb = half * 32; cb < tokens; cb += 64) {
+            uint32_t a[16], b[16];
+            tmem_load_16(trow + static_cast<uint32_t>(cb), a);
+            tmem_load_16(trow + static_cast<uint32_t>(cb) + 16u, b);
+            tmem_load_wait();
+            const int left = n < p.N ? tokens - cb : 0;
+            uint16_t* to = cp;
+            if (left >= 32) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (cb + 16 * h < rows) {
-                __syncwarp();
+                for (int i = 0; i < 32; ++i) {
+                    *to = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(i < 16 ? a[i & 15] : b[i & 15])));
+                    to += p.ldc;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (i < left) *to = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(i < 16 ? a[i & 15] : b[i & 15])));
+                    to += p.ldc;
+                }
+            }
+            cp += 64 * p.ldc;
+        }
+    } else {
+        const int middle = (((tokens + 15) >> 4) + 1) / 2 * 16;    // the two warps of 32 weight rows
+        const int first = half ? middle : 0, rows = half ? tokens : min(middle, tokens);   // take [first, rows)
+        const uint32_t put = smem_addr(stage) + static_cast<uint32_t>((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+        const int r0 = lane >> 2, n = n0 + (lane & 3) * 8;
+        // this lane's piece of row r0, and 512 bytes on that of row r0 + 8
+        const uint8_t* get = stage + r0 * 64 + ((((lane & 3) ^ (r0 >> 1)) & 3) << 4);
+        const bool inside = n0 + 32 <= p.N;        // for the whole warp
+        const int64_t step = 8 * p.ldc;
+        uint16_t* cp = p.c + (row0 + first + r0) * p.ldc + n;
+        for (int cb = first; cb < rows; cb += 32) {
+            uint32_t lo[16], hi[16];
+            tmem_load_frag32(trow + static_cast<uint32_t>(cb), lo);
+            tmem_load_frag32(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
+            tmem_load_wait();
+            auto put16 = [&](int h) {              // tokens cb + 16 h ..
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int i = 2 * h + q;
@@ -334,29 +362,40 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
                                       pack_bf16x2(__uint_as_float(hi[4 * i + 2]), __uint_as_float(hi[4 * i + 3])));
                 }
                 __syncwarp();
-                constexpr int kGo = 16 / kVec < 4 ? 16 / kVec : 4;      // pieces read before the first is stored
+            };
+            __syncwarp();
+            put16(0);
+            uint4 v0 = *reinterpret_cast<const uint4*>(get), v1 = *reinterpret_cast<const uint4*>(get + 512);
+            __syncwarp();
+            if (inside && cb + 32 <= rows) {
+                put16(1);
+                const uint4 v2 = *reinterpret_cast<const uint4*>(get), v3 = *reinterpret_cast<const uint4*>(get + 512);
+                *reinterpret_cast<uint4*>(cp) = v0;
+                *reinterpret_cast<uint4*>(cp + step) = v1;
+                *reinterpret_cast<uint4*>(cp + 2 * step) = v2;
+                *reinterpret_cast<uint4*>(cp + 3 * step) = v3;
+            } else {
+                auto some = [&](int m, const uint4& v, uint16_t* to) {
+                    if (m < rows && n + 8 <= p.N) {
+                        *reinterpret_cast<uint4*>(to) = v;
+                    } else if (m < rows) {
+                        const uint16_t* e = reinterpret_cast<const uint16_t*>(&v);
 #pragma unroll
-                for (int q0 = 0; q0 < 16; q0 += kGo * kVec) {
-                    uint4 v[kGo];
-#pragma unroll
-                    for (int q = 0; q < kGo; ++q) {
-                        const uint8_t* f = from(q0 + q * kVec + r0);
-                        if constexpr (kVec == 8) v[q] = *reinterpret_cast<const uint4*>(f);
-                        else v[q].x = *reinterpret_cast<const uint16_t*>(f);
+                        for (int k = 0; k < 7; ++k)
+                            if (n + k < p.N) to[k] = e[k];
                     }
-#pragma unroll
-                    for (int q = 0; q < kGo; ++q) {
-                        const int r = q0 + q * kVec + r0, m = cb + 16 * h + r;
-                        uint16_t* cp = p.c + (row0 + m) * p.ldc + n;
-                        if (m < rows && whole) {
-                            if constexpr (kVec == 8) *reinterpret_cast<uint4*>(cp) = v[q];
-                            else *cp = static_cast<uint16_t>(v[q].x);
-                        } else if (kVec > 1 && m < rows) {
-                            for (int k = 0; n + k < p.N; ++k) cp[k] = reinterpret_cast<const uint16_t*>(from(r))[k];
-                        }
-                    }
+                };
+                some(cb + r0, v0, cp);
+                some(cb + r0 + 8, v1, cp + step);
+                if (cb + 16 < rows) {
+                    put16(1);
+                    v0 = *reinterpret_cast<const uint4*>(get);
+                    v1 = *reinterpret_cast<const uint4*>(get + 512);
+                    some(cb + r0 + 16, v0, cp + 2 * step);
+                    some(cb + r0 + 24, v1, cp + 3 * step);
                 }
             }
+            cp += 4 * step;
         }
     }
 }
@@ -386,8 +425,8 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
     constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
     if (kTermsPer == 1 && u.nk == p.k_atoms) {
         const int n0 = nt * kTileN + (warp & 3) * 32;
-        if (p.c_vec == 8) store_tile<8>(p, acc, u.rows, u.row0, n0, half, lane, stage);
-        else store_tile<1>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+        if (p.c_wide) store_tile<true>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+        else store_tile<false>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         return;
     }
     const int nl = (warp & 3) * 32 + lane, n = nt * kTileN + nl;
