@@ -8,11 +8,12 @@
 // The group sizes live on the device, so the work is cut there. A unit is (token tile of a group,
 // 128 weight rows) over all of K. One CTA runs per SM; each scans the group sizes once, then takes
 // whole units in waves, CTA i the i-th of every wave, and the units left after the last full wave
-// are cut along K into equal runs of 256-K steps, one run per CTA (a run may end one unit and
-// begin the next). A unit cut between CTAs is added up by whichever of them arrives last, in the
-// order of K from the fp32 sums that the others left in the workspace: no CTA waits for another,
-// and the result does not depend on the order of arrival. With few units (decoding) there is no
-// full wave and every SM streams an equal share of the weights.
+// (where it pays, those of the last full wave too) are cut along K into equal runs of 256-K steps, one
+// run per CTA (a run may end one unit, take another whole and begin the next). A unit cut between
+// CTAs is added up by whichever of them arrives last, in the order of K from the fp32 sums that the
+// others left in the workspace: no CTA waits for another, and the result does not depend on the order
+// of arrival. With few units (decoding) there is no full wave and every SM streams an equal share of
+// the weights.
 //
 // Warps: 0 copies (weights and token blocks, one mbarrier per stage), 1 tensor memory and the
 // MMAs (two accumulators: the next unit's MMAs run while the last one is stored), 4-11 the

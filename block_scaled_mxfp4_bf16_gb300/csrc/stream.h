@@ -17,6 +17,7 @@ constexpr int kStreamEpiThreads = 256;
 constexpr int token_warps(int terms) { return terms > 1 ? 8 : 6; }
 constexpr int stream_threads(int terms, bool fused) { return kStreamThreads + (fused ? 32 * (token_warps(terms) - 2) : 0); }
 constexpr int kSplitSteps = 8;            // 256-K steps that splitting a unit between CTAs has to save
+constexpr int kMergeSteps = 7;            // and that cutting a full wave together with the rest has to save
 constexpr int kStreamMaxStages = 10;
 constexpr int kEpiStage = 1024;           // bytes of shared memory an epilogue warp transposes through
 constexpr int kPairThreads = 640;         // the pair kernel: warps 12-19 write scale factors

@@ -265,3 +265,18 @@ def test_broken_offsets_of_large_groups_leave_c_unwritten(offsets):
     mx.mxfp4_grouped_gemm(a, packed, torch.tensor(offsets, dtype=torch.int32).cuda(), N, c=c)
     assert mx.mxfp4_device_status() == 0
     assert bool((store == -7.0).all())
+
+
+# A few units more than SMs (or pairs): the last full wave is cut into runs together with the rest, so that a
+# run ends one unit, may take one whole and begins another.
+@pytest.mark.parametrize("sizes,N,K", [([60] * 20, 1024, 4096), ([60] * 40, 1000, 4104), ([128, 1, 0, 127] * 11, 1025, 2816),
+                                       ([300] * 10, 1100, 4096), ([190] * 20, 1024, 3584)])
+def test_a_wave_cut_together_with_the_rest(sizes, N, K):
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    packed, w = weights(len(sizes), N, K, seed=11)
+    a = workloads.random_bf16(sum(sizes), K, seed=6).cuda()
+    c = mx.mxfp4_grouped_gemm(a, packed, offsets_of(sizes), N)
+    check(c, quantized(a), w, sizes)
+    for _ in range(3):
+        assert torch.equal(mx.mxfp4_grouped_gemm(a, packed, offsets_of(sizes), N).view(torch.int16), c.view(torch.int16))
+    assert mx.mxfp4_device_status() == 0
