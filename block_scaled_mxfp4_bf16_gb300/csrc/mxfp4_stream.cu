@@ -651,9 +651,9 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     }
     p.cluster = 1;
     // Large groups: two CTAs to a unit, which halves the token bytes an SM takes in, where K is long enough
-    // to pay for what a pair does once a unit: 16384 rows in 16 groups x 4096 x 7168 211 us against 232,
-    // x 4096 120 against 136, x 2048 80 both; 22672 rows in 52 groups x 5664 x 1536 128 against 122, x 160
-    // 108 against 72.
+    // to pay for what a pair does once a unit: 16384 rows in 16 groups x 4096 x 7168 208 us against 232,
+    // x 3584 112 against 122, x 2048 79 against 80, x 1536 68 against 64; 22672 rows in 52 groups x 5664 x
+    // 2560 170 against 181, x 2048 146 against 153, x 1536 120 against 122, but 1408 x 2048 64 against 59.
     constexpr int kPairSteps = 8;
     p.pair = terms == 1 && p.m_tile > 128 && p.n_tiles > 1 && p.k_atoms >= kPairSteps;
     p.nmc = (p.m_tile + 127) / 128;
