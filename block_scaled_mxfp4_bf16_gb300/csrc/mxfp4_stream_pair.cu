@@ -42,8 +42,8 @@ __device__ __forceinline__ void mma_pair_if(uint32_t issue, uint32_t d_tmem, uin
 // by the tcgen05 fences on both sides) and in shared memory that bulk copies wrote: no ordinary store
 // has to be seen, so neither the arrival nor the waits ask for cluster scope, which costs far
 // more than the arrival itself (16384 rows in 16 groups x 4096 x 7168: 595 us with cluster scope,
-// 252 without; 227 with the divisions out of the scale warps' loop, 217 with two sets of them; one
-// CTA per unit takes 235).
+// 252 without; 227 with the divisions out of the scale warps' loop, 217 with two sets of them, 208 with
+// a cheaper walk and the last wave cut together with the rest; one CTA per unit takes 232).
 __device__ __forceinline__ void arrive_first(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
