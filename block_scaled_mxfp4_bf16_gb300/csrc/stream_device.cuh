@@ -347,6 +347,7 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
                 }
             }
             cp += 64 * p.ldc;
+            __syncwarp();                          // tensor memory is read by the whole warp
         }
     } else {
         const int middle = (((tokens + 15) >> 4) + 1) / 2 * 16;    // the two warps of 32 weight rows
@@ -375,7 +376,6 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
                 }
                 __syncwarp();
             };
-            __syncwarp();
             put16(0);
             uint4 v0 = *reinterpret_cast<const uint4*>(get), v1 = *reinterpret_cast<const uint4*>(get + 512);
             __syncwarp();
@@ -400,6 +400,7 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
                 some(cb + r0, v0, cp);
                 some(cb + r0 + 8, v1, cp + step);
                 if (cb + 16 < rows) {
+                    __syncwarp();                  // the matrix stores too take the whole warp
                     put16(1);
                     v0 = *reinterpret_cast<const uint4*>(get);
                     v1 = *reinterpret_cast<const uint4*>(get + 512);
@@ -408,6 +409,7 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
                 }
             }
             cp += 4 * step;
+            __syncwarp();
         }
     }
 }
@@ -524,6 +526,7 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
                 cp += p.ldc;
             }
         }
+        __syncwarp();
     }
 }
 
