@@ -27,7 +27,18 @@ __all__ = [
 
 _LOCK = threading.Lock()
 _LIB = None
-_WS: dict = {}
+
+
+class _DefaultWorkspaces(threading.local):
+    """The calling thread's default workspaces, {(device, stream): tensor}. A call of several kernels
+    enqueues them one by one with the interpreter's lock released, so two threads' calls on one
+    stream interleave: with a workspace in common one would read what the other's first kernel wrote."""
+
+    def __init__(self):
+        self.held: dict = {}
+
+
+_WS = _DefaultWorkspaces()
 
 _vp = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -351,27 +362,33 @@ def mxfp4_workspace_init(ws: torch.Tensor, stream=None) -> None:
            "mxfp4_workspace_init")
 
 
-def _workspace(device: torch.device, nbytes: int, stream, st: int) -> torch.Tensor | None:
-    """A zero-initialised workspace of at least nbytes per (device, stream), grown on demand.
-    One per stream: calls sharing a workspace must be ordered, and calls on different streams
-    need not be. A workspace used on a stream other than the current one is recorded on it, so
-    that growing it never hands its memory to other work while that stream may still use it."""
-    if nbytes == 0:
-        return None
-    dev_index = device.index if device.index is not None else torch.cuda.current_device()
-    key = (dev_index, st)
-    ws = _WS.get(key)
-    if ws is None or ws.numel() < nbytes:
-        ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        if st != torch.cuda.current_stream(dev_index).cuda_stream:
-            ws.record_stream(torch.cuda.ExternalStream(st, device=device))
-        mxfp4_workspace_init(ws, stream)
-        _WS[key] = ws
+def _new_workspace(device: torch.device, nbytes: int, stream, st: int) -> torch.Tensor:
+    """A zero-initialised workspace. One used on a stream other than the current one is recorded on
+    it, so that dropping it never hands its memory to other work while that stream may still use it."""
+    ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    if st != torch.cuda.current_stream(device).cuda_stream:
+        ws.record_stream(torch.cuda.ExternalStream(st, device=device))
+    mxfp4_workspace_init(ws, stream)
     return ws
 
 
-def _gemm_call_args(a, packed_b, N, c, workspace, path, splits, stream, m_tile, a_ready=False) -> tuple:
-    """(C, the checked arguments of one mxfp4_gemm_ex call in C order)."""
+def _workspace(device: torch.device, nbytes: int, stream, st: int) -> torch.Tensor | None:
+    """The calling thread's default workspace of at least nbytes for (device, stream), grown on demand.
+    Calls sharing a workspace must be ordered: calls on different streams need not be, and neither
+    are the kernels of two threads' calls on one stream."""
+    if nbytes == 0:
+        return None
+    key = (device.index if device.index is not None else torch.cuda.current_device(), st)
+    ws = _WS.held.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = _WS.held[key] = _new_workspace(device, nbytes, stream, st)
+    return ws
+
+
+def _gemm_call_args(a, packed_b, N, c, workspace, path, splits, stream, m_tile, a_ready=False,
+                    own_workspace=_workspace) -> tuple:
+    """(C, the checked arguments of one mxfp4_gemm_ex call in C order, its workspace). own_workspace makes
+    the workspace of a call that was given none."""
     L = load_library()
     _dev(a, "a")
     if a.dtype != torch.bfloat16 or a.dim() != 2 or a.stride(1) != 1:
@@ -392,7 +409,7 @@ def _gemm_call_args(a, packed_b, N, c, workspace, path, splits, stream, m_tile, 
     else:
         dev = a.device
         need = _ws_need(dev, M, N, K, path, splits, m_tile)
-        workspace = _workspace(dev, need, stream, st) if need else None
+        workspace = own_workspace(dev, need, stream, st) if need else None
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     flags = GEMM_A_READY if a_ready else 0
@@ -413,8 +430,8 @@ def mxfp4_gemm(a: torch.Tensor, packed_b: torch.Tensor, N: int, c: torch.Tensor 
     return c
 
 
-def _host_call_args(a_host, packed_b, N, c_host, a_dev, c_dev, workspace, stream) -> tuple:
-    """The checked arguments of one mxfp4_gemm_host call, in C order."""
+def _host_call_args(a_host, packed_b, N, c_host, a_dev, c_dev, workspace, stream, own_workspace=_workspace) -> tuple:
+    """(The checked arguments of one mxfp4_gemm_host call in C order, its workspace)."""
     L = load_library()
     # every tensor property is read once: this call sits on the per-step host path
     bf16 = torch.bfloat16
@@ -440,11 +457,11 @@ def _host_call_args(a_host, packed_b, N, c_host, a_dev, c_dev, workspace, stream
     else:
         dev = a_dev.device
         need = _ws_need(dev, M, N, K)
-        workspace = _workspace(dev, need, stream, st) if need else None
+        workspace = own_workspace(dev, need, stream, st) if need else None
     ws_ptr = workspace.data_ptr() if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     return (a_host.data_ptr(), M, K, a_stride[0], packed_b.data_ptr(), N, c_host.data_ptr(), c_stride[0],
-            a_dev.data_ptr(), c_dev.data_ptr(), ws_ptr, ws_bytes, st)
+            a_dev.data_ptr(), c_dev.data_ptr(), ws_ptr, ws_bytes, st), workspace
 
 
 def mxfp4_gemm_host(a_host: torch.Tensor, packed_b: torch.Tensor, N: int, c_host: torch.Tensor,
@@ -452,7 +469,7 @@ def mxfp4_gemm_host(a_host: torch.Tensor, packed_b: torch.Tensor, N: int, c_host
                     stream=None) -> torch.Tensor:
     """mxfp4_gemm_host: A and C in (preferably pinned) host memory, device staging buffers a_dev
     [M, K] and c_dev [M, N] from the caller; asynchronous on `stream`. Returns c_host."""
-    args = _host_call_args(a_host, packed_b, N, c_host, a_dev, c_dev, workspace, stream)
+    args, _ = _host_call_args(a_host, packed_b, N, c_host, a_dev, c_dev, workspace, stream)
     _check(load_library().mxfp4_gemm_host(*args), "mxfp4_gemm_host")
     return c_host
 
@@ -462,7 +479,8 @@ class PreparedCall:
     fixed input and output buffers), prepared in the library (mxfp4_call_create*): its checks,
     plan and host-buffer queries are done once, and each call only enqueues its kernels and
     copies on the stream given when it was prepared. The tensors are kept alive by this object;
-    the caller must not resize or replace their storage while it is in use. Calling it raises
+    the caller must not resize or replace their storage while it is in use. A call given no workspace
+    has one of its own, since any thread may run it beside others' calls. Calling it raises
     Mxfp4Error if the library refuses the run."""
 
     __slots__ = ("_run", "_handle", "_stream", "_where", "_keep", "_destroy")
@@ -490,7 +508,7 @@ def prepare_gemm(a: torch.Tensor, packed_b: torch.Tensor, N: int, c: torch.Tenso
                  stream=None, m_tile: int = 0, a_ready: bool = False) -> PreparedCall:
     """mxfp4_gemm prepared for repeated calls on the same buffers (see PreparedCall); `c` is
     required, the other arguments are those of mxfp4_gemm (a_ready holds for every run)."""
-    c, args, ws = _gemm_call_args(a, packed_b, N, c, workspace, path, splits, stream, m_tile, a_ready)
+    c, args, ws = _gemm_call_args(a, packed_b, N, c, workspace, path, splits, stream, m_tile, a_ready, _new_workspace)
     return PreparedCall(load_library().mxfp4_call_create, args[:-1], args[-1], "mxfp4_call_create",
                         (a, packed_b, c, ws))
 
@@ -502,7 +520,7 @@ def prepare_gemm_host(a_host: torch.Tensor, packed_b: torch.Tensor, N: int, c_ho
     arguments are those of mxfp4_gemm_host. a_host_written: the caller guarantees that a_host is
     written by the host only, never by device work (MXFP4_CALL_A_HOST_WRITTEN), so A crosses the
     link while the work before the call still runs."""
-    args = _host_call_args(a_host, packed_b, N, c_host, a_dev, c_dev, workspace, stream)
+    args, workspace = _host_call_args(a_host, packed_b, N, c_host, a_dev, c_dev, workspace, stream, _new_workspace)
     keep = (a_host, packed_b, c_host, a_dev, c_dev, workspace)
     flags = 1 if a_host_written else 0
     return PreparedCall(load_library().mxfp4_call_create_host, args[:-1] + (flags,), args[-1],

@@ -39,7 +39,7 @@ def _begin(t: torch.Tensor, name: str, stream) -> tuple:
 
 
 def _scratch(workspace, need: int, t: torch.Tensor, stream, st: int, device: int) -> tuple:
-    """(pointer, bytes) of the caller's workspace, or of the binding's own for this stream."""
+    """(pointer, bytes) of the caller's workspace, or of this thread's default one for the stream."""
     if workspace is not None:
         _on(workspace, t.device, "workspace")
         if not workspace.is_contiguous():
@@ -47,7 +47,7 @@ def _scratch(workspace, need: int, t: torch.Tensor, stream, st: int, device: int
     elif need == 0:
         return None, 0
     else:
-        workspace = _WS.get((device, st))
+        workspace = _WS.held.get((device, st))
         if workspace is None or workspace.nbytes < need:
             workspace = _workspace(t.device, need, stream, st)
     return workspace.data_ptr(), workspace.nbytes
