@@ -8,6 +8,7 @@ built, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -372,12 +373,44 @@ def _new_workspace(device: torch.device, nbytes: int, stream, st: int) -> torch.
     return ws
 
 
+def _writing(stream, device: torch.device):
+    """The context in which new tensors belong to the stream of the call (None: the current one) and the
+    current stream is that one."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+_current_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)
+
+
+def _capturing(device: torch.device, stream, st: int) -> bool:
+    """Whether the call's stream is being captured into a graph."""
+    if stream is None or (_raw_stream is not None and _raw_stream(torch.cuda.current_device()) == st):
+        return _current_capturing()
+    with _writing(stream, device):
+        return _current_capturing()
+
+
+def _captured_workspace(device: torch.device, nbytes: int, stream) -> torch.Tensor:
+    """The workspace of one captured call. A graph keeps the address for as long as it is replayed, so
+    this is memory of the graph's own pool, as the temporaries of any captured operation are: later
+    calls never free it, other graphs do not use it, and the operations captured after this one may
+    have it again, since every replay runs them in the same order."""
+    with _writing(stream, device):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _workspace(device: torch.device, nbytes: int, stream, st: int) -> torch.Tensor | None:
     """The calling thread's default workspace of at least nbytes for (device, stream), grown on demand.
     Calls sharing a workspace must be ordered: calls on different streams need not be, and neither
-    are the kernels of two threads' calls on one stream."""
+    are the kernels of two threads' calls on one stream. A captured call gets one to itself."""
     if nbytes == 0:
         return None
+    if _capturing(device, stream, st):
+        return _captured_workspace(device, nbytes, stream)
     key = (device.index if device.index is not None else torch.cuda.current_device(), st)
     ws = _WS.held.get(key)
     if ws is None or ws.numel() < nbytes:

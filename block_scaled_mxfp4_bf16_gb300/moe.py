@@ -10,8 +10,8 @@ from typing import NamedTuple
 
 import torch
 
-from . import (_PACKED_NEED, _WS, Mxfp4Error, _check, _check_packed, _dev, _on, _raw_stream, _stream, _workspace,
-               load_library, mxfp4_prepack_b, mxfp4_prepack_b_size)
+from . import (_PACKED_NEED, _WS, Mxfp4Error, _check, _check_packed, _current_capturing, _dev, _on, _raw_stream, _stream,
+               _workspace, load_library, mxfp4_prepack_b, mxfp4_prepack_b_size)
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _NEED: dict = {}
@@ -39,18 +39,20 @@ def _begin(t: torch.Tensor, name: str, stream) -> tuple:
 
 
 def _scratch(workspace, need: int, t: torch.Tensor, stream, st: int, device: int) -> tuple:
-    """(pointer, bytes) of the caller's workspace, or of this thread's default one for the stream."""
+    """(pointer, bytes) of the caller's workspace or of this thread's default one for the stream, and the
+    tensor, which has to live until the call is enqueued."""
     if workspace is not None:
         _on(workspace, t.device, "workspace")
         if not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous")
     elif need == 0:
-        return None, 0
+        return None, 0, None
     else:
-        workspace = _WS.held.get((device, st))
+        if stream is None and not _current_capturing():
+            workspace = _WS.held.get((device, st))
         if workspace is None or workspace.nbytes < need:
             workspace = _workspace(t.device, need, stream, st)
-    return workspace.data_ptr(), workspace.nbytes
+    return workspace.data_ptr(), workspace.nbytes, workspace
 
 
 def _rows_of(t: torch.Tensor, name: str) -> int:
@@ -115,7 +117,7 @@ def mxfp4_gemv(x: torch.Tensor, packed_b: torch.Tensor, N: int, y: torch.Tensor 
         _check_packed(packed_b, N, K, x.device)
         need = _need("mxfp4_gemv_workspace_size", device, M, N, K)
     y, ldy = _out(y, (M, N), x, "y", stream)
-    ws, ws_bytes = _scratch(workspace, need, x, stream, st, device)
+    ws, ws_bytes, _held = _scratch(workspace, need, x, stream, st, device)
     status = load_library().mxfp4_gemv(x.data_ptr(), M, K, ldx, packed_b.data_ptr(), N, y.data_ptr(), ldy, ws, ws_bytes,
                                        st)
     if status:
@@ -172,7 +174,7 @@ def mxfp4_grouped_gemm(a: torch.Tensor, packed_b: torch.Tensor, offsets: torch.T
         rows_ptr = _index(rows, (R,), a, "rows")
     c, ldc = _out(c, (R, N), a, "c", stream)
     need = _need("mxfp4_grouped_gemm_workspace_size", device, R, E, N, K) if R and E and N else 0
-    ws, ws_bytes = _scratch(workspace, need, a, stream, st, device)
+    ws, ws_bytes, _held = _scratch(workspace, need, a, stream, st, device)
     status = load_library().mxfp4_grouped_gemm(a.data_ptr(), tokens, K, lda, rows_ptr, offsets_ptr, E,
                                                packed_b.data_ptr(), N, c.data_ptr(), R, ldc, 1 if gated else 0, ws,
                                                ws_bytes, st)
@@ -218,7 +220,7 @@ def mxfp4_moe_route(logits: torch.Tensor, k: int, renormalize: bool = True, work
         weights, experts, offsets, rows, slots = (
             _empty(shape, dtype, logits, stream)
             for shape, dtype in (((T, k), _F32), ((T, k), _I32), ((E + 1,), _I32), ((T * k,), _I32), ((T, k), _I32)))
-    ws, ws_bytes = _scratch(workspace, _need("mxfp4_moe_route_workspace_size", device, T, E), logits, stream, st, device)
+    ws, ws_bytes, _held = _scratch(workspace, _need("mxfp4_moe_route_workspace_size", device, T, E), logits, stream, st, device)
     status = load_library().mxfp4_moe_route(logits.data_ptr(), dtype, T, E, ld, k, 0 if renormalize else 1,
                                             weights.data_ptr(), experts.data_ptr(), offsets.data_ptr(),
                                             rows.data_ptr(), slots.data_ptr(), ws, ws_bytes, st)

@@ -24,7 +24,7 @@ def made(monkeypatch):
 
     def empty(*shape, **kw):
         t = real_empty(*shape, **kw)
-        if kw.get("dtype") is torch.uint8:
+        if kw.get("dtype") is torch.uint8 and len(shape) == 1:
             tensors.append(t)
         return t
     monkeypatch.setattr(mx, "load_library", lambda: fake)
@@ -34,8 +34,12 @@ def made(monkeypatch):
     monkeypatch.setattr(moe, "_WS", mx._WS)
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # a CPU tensor's get_device()
-    world = types.SimpleNamespace(tensors=tensors, lib=fake, stream=0)   # stream: the current one
+    world = types.SimpleNamespace(tensors=tensors, lib=fake, stream=0, capturing=False)   # the current stream
+    for module in (mx, moe):
+        monkeypatch.setattr(module, "_raw_stream", lambda device: world.stream)
+        monkeypatch.setattr(module, "_current_capturing", lambda: world.capturing, raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=world.stream))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda st, device=None: st)
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     return world
 
@@ -96,3 +100,38 @@ def test_prepared_calls_have_a_workspace_of_their_own(made, monkeypatch):
             seen.add(args[8])
     assert len(seen) == 3
     del calls
+
+
+@pytest.mark.parametrize("op", ["gemv", "grouped"])
+def test_a_captured_call_has_a_workspace_of_its_own(made, op):
+    # a graph keeps the address: it must be neither the default one, which a larger call replaces, nor
+    # one that is kept for the calls after the capture
+    if op == "gemv":
+        def call():
+            mx.mxfp4_gemv(bf16(3, 256), packed(1, 128, 256)[0], 128, y=bf16(3, 128))
+    else:
+        def call():
+            mx.mxfp4_grouped_gemm(bf16(6, 256), packed(3, 128, 256), i32(0, 2, 4, 6), 128, c=bf16(6, 128))
+    eager = _workspace_argument(made, call)
+    held = dict(mx._WS.held)
+    made.capturing = True
+    kept = len(made.tensors)
+    first = _workspace_argument(made, call)
+    assert len(made.tensors) == kept + 1 and first == made.tensors[-1].data_ptr() != eager
+    assert mx._WS.held == held, "memory of the graph's pool is kept for calls outside it"
+    made.capturing = False
+    assert _workspace_argument(made, call) == eager
+
+
+def test_the_captured_gemm_has_a_workspace_of_its_own(made, monkeypatch):
+    monkeypatch.setattr(mx, "_ws_need", lambda *a: 5000)
+    a, b, c = bf16(8, 512), packed(1, 256, 512)[0], bf16(8, 256)
+
+    def pointer():
+        mx.mxfp4_gemm(a, b, 256, c=c)
+        return made.lib.calls[-1][1][8]
+    eager = pointer()
+    made.capturing = True
+    assert pointer() != eager
+    made.capturing = False
+    assert pointer() == eager

@@ -1,5 +1,6 @@
 """Calls that pass no workspace, on the GPU: several host threads on one stream must get the results that one
-thread gets, whatever order their calls' kernels are enqueued in."""
+thread gets, whatever order their calls' kernels are enqueued in, and a graph captured from such calls must
+keep to memory of its own."""
 import threading
 
 import pytest
@@ -61,3 +62,69 @@ def test_threads_on_one_stream():
             for i, (o, w) in enumerate(zip(outs, want[t])):
                 assert equal(o, w), (t, i)
     assert len(got) == len(sets)
+
+
+def layer(seed, tokens):
+    """A mixture-of-experts pass and a weight-only product, no workspace passed: (call, larger call)."""
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    E, k, hidden, inner = 4, 2, 1024, 256
+    w13, _ = weights(E, 2 * inner, hidden, seed=seed)
+    w2, _ = weights(E, hidden, inner, seed=seed + 1)
+
+    def of(T):
+        x = workloads.random_bf16(T, hidden, seed=seed + T).cuda()
+        logits = torch.randn(T, E, generator=torch.Generator().manual_seed(seed + T)).cuda()
+
+        def call():
+            r = mx.mxfp4_moe_route(logits, k)
+            h = mx.mxfp4_grouped_gemm(x, w13, r.offsets, 2 * inner, rows=r.rows)
+            y = mx.mxfp4_grouped_gemm(h, w2, r.offsets, hidden, gated=True)
+            return [mx.mxfp4_moe_combine(y, r.slots, r.weights), mx.mxfp4_gemv(x[:5], w13[0], 2 * inner),
+                    mx.mxfp4_gemm(x, w13[1], 2 * inner, path=2)]
+        return call
+    return of(tokens), of(20 * tokens)
+
+
+def test_a_larger_call_after_the_capture_leaves_the_graph_its_memory():
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    call, larger = layer(7, 300)
+    stream = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        want = [o.clone() for o in call()]          # warm-up: the stream's default workspace is there
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            outs = call()
+        larger()                                    # replaces the default workspace by a larger one
+        torch.cuda.synchronize()
+        others = [torch.full((n << 20,), 0x5A, dtype=torch.uint8, device="cuda") for n in (1, 1, 2, 4, 8, 16, 32)]
+        for _ in range(3):
+            for o in outs:
+                o.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert equal(outs, want)
+    assert all(bool((o == 0x5A).all()) for o in others), "a replay wrote into another tensor's memory"
+    assert mx.mxfp4_device_status() == 0
+
+
+def test_graphs_of_one_capture_stream_replay_side_by_side():
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    calls = [layer(20 + i, 300)[0] for i in range(2)]
+    wants = [[o.clone() for o in call()] for call in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for call in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):               # the default capture stream, the same for both
+            outs.append(call())
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, wants):
+        assert equal(o, w)
+    assert mx.mxfp4_device_status() == 0
