@@ -363,16 +363,6 @@ def mxfp4_workspace_init(ws: torch.Tensor, stream=None) -> None:
            "mxfp4_workspace_init")
 
 
-def _new_workspace(device: torch.device, nbytes: int, stream, st: int) -> torch.Tensor:
-    """A zero-initialised workspace. One used on a stream other than the current one is recorded on
-    it, so that dropping it never hands its memory to other work while that stream may still use it."""
-    ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-    if st != torch.cuda.current_stream(device).cuda_stream:
-        ws.record_stream(torch.cuda.ExternalStream(st, device=device))
-    mxfp4_workspace_init(ws, stream)
-    return ws
-
-
 def _writing(stream, device: torch.device):
     """The context in which new tensors belong to the stream of the call (None: the current one) and the
     current stream is that one."""
@@ -381,6 +371,15 @@ def _writing(stream, device: torch.device):
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
+
+
+def _new_workspace(device: torch.device, nbytes: int, stream, st: int) -> torch.Tensor:
+    """A zero-initialised workspace, memory of the stream that writes it: it was free of that stream's work
+    when it was handed out, and dropping it hands it to that stream's later work only."""
+    with _writing(stream, device):
+        ws = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
+    mxfp4_workspace_init(ws, stream)
+    return ws
 
 
 _current_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing", torch.cuda.is_current_stream_capturing)

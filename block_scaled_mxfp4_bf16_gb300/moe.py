@@ -11,7 +11,7 @@ from typing import NamedTuple
 import torch
 
 from . import (_PACKED_NEED, _WS, Mxfp4Error, _check, _check_packed, _current_capturing, _dev, _on, _raw_stream, _stream,
-               _workspace, load_library, mxfp4_prepack_b, mxfp4_prepack_b_size)
+               _workspace, _writing, load_library, mxfp4_prepack_b, mxfp4_prepack_b_size)
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _NEED: dict = {}
@@ -82,9 +82,7 @@ def _empty(shape: tuple, dtype: torch.dtype, t: torch.Tensor, stream) -> torch.T
         if _empty_strided is not None:
             return _empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype)
         return torch.empty(shape, dtype=dtype, device=t.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
-    with torch.cuda.stream(stream):
+    with _writing(stream, t.device):
         return torch.empty(shape, dtype=dtype, device=t.device)
 
 
@@ -128,7 +126,7 @@ def mxfp4_gemv(x: torch.Tensor, packed_b: torch.Tensor, N: int, y: torch.Tensor 
 def mxfp4_prepack_experts(bq: torch.Tensor, bs: torch.Tensor, stream=None) -> torch.Tensor:
     """Pre-quantized weights of E experts (e2m1 [E, N, nblk*16], e8m0 [E, N, nblk]) -> uint8
     [E, mxfp4_prepack_b_size(N, K)], each row packed by mxfp4_prepack_b: the weights
-    mxfp4_grouped_gemm reads."""
+    mxfp4_grouped_gemm reads. Their memory belongs to the stream that writes them."""
     if bq.dim() != 3 or bs.dim() != 3 or bq.shape[0] != bs.shape[0]:
         raise ValueError("bq [E, N, nblk*16] and bs [E, N, nblk] must be 3-D with the same E")
     _dev(bq, "bq")
@@ -136,7 +134,8 @@ def mxfp4_prepack_experts(bq: torch.Tensor, bs: torch.Tensor, stream=None) -> to
     size = mxfp4_prepack_b_size(N, K)
     if size == 0:
         raise Mxfp4Error(2, "mxfp4_prepack_b_size")
-    store = torch.empty(E * size + 1024, dtype=torch.uint8, device=bq.device)
+    with _writing(stream, bq.device):
+        store = torch.empty(E * size + 1024, dtype=torch.uint8, device=bq.device)
     off = (-store.data_ptr()) % 1024
     packed = store[off:off + E * size].view(E, size)
     for e in range(E):

@@ -10,6 +10,7 @@ import torch
 
 import block_scaled_mxfp4_bf16_gb300 as mx
 from block_scaled_mxfp4_bf16_gb300 import moe
+from test_binding_checks import dev
 from test_moe_checks import _MoeLib, bf16, i32, packed
 
 CPU = torch.device("cpu")
@@ -26,6 +27,7 @@ def made(monkeypatch):
         t = real_empty(*shape, **kw)
         if kw.get("dtype") is torch.uint8 and len(shape) == 1:
             tensors.append(t)
+            world.owners.append(world.stream)
         return t
     monkeypatch.setattr(mx, "load_library", lambda: fake)
     monkeypatch.setattr(moe, "load_library", lambda: fake)
@@ -34,13 +36,19 @@ def made(monkeypatch):
     monkeypatch.setattr(moe, "_WS", mx._WS)
     monkeypatch.setattr(torch, "empty", empty)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # a CPU tensor's get_device()
-    world = types.SimpleNamespace(tensors=tensors, lib=fake, stream=0, capturing=False)   # the current stream
+    world = types.SimpleNamespace(tensors=tensors, lib=fake, stream=0, capturing=False, owners=[])   # stream: current
     for module in (mx, moe):
         monkeypatch.setattr(module, "_raw_stream", lambda device: world.stream)
         monkeypatch.setattr(module, "_current_capturing", lambda: world.capturing, raising=False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=world.stream))
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda st, device=None: st)
-    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+
+    @contextlib.contextmanager
+    def on(stream):
+        before, world.stream = world.stream, stream
+        yield
+        world.stream = before
+    monkeypatch.setattr(torch.cuda, "stream", on)
     return world
 
 
@@ -135,3 +143,14 @@ def test_the_captured_gemm_has_a_workspace_of_its_own(made, monkeypatch):
     assert pointer() != eager
     made.capturing = False
     assert pointer() == eager
+
+
+def test_memory_belongs_to_the_stream_that_writes_it(made):
+    # what the current stream freed may still be read by work queued there
+    mx._workspace(CPU, 5000, 7, 7)
+    mx._workspace(CPU, 5000, None, 0)
+    assert made.owners == [7, 0]
+    bq, bs = (dev(torch.zeros(3, 128, n, dtype=torch.uint8)) for n in (128, 8))
+    mx.mxfp4_prepack_experts(bq, bs, stream=9)
+    mx.mxfp4_prepack_experts(bq, bs)
+    assert made.owners == [7, 0, 9, 0] and made.stream == 0

@@ -128,3 +128,21 @@ def test_graphs_of_one_capture_stream_replay_side_by_side():
     for o, w in zip(outs, wants):
         assert equal(o, w)
     assert mx.mxfp4_device_status() == 0
+
+
+def test_packed_experts_take_no_memory_the_current_stream_may_still_read():
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    E, N, K = 3, 256, 512
+    bq, bs = mx.mxfp4_quantize(workloads.random_bf16(E * N, K, seed=1).cuda())
+    bq, bs = bq.view(E, N, -1), bs.view(E, N, -1)
+    want = mx.mxfp4_prepack_experts(bq, bs)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    read = torch.arange(want.nbytes + 1024, device="cuda").to(torch.uint8)
+    keep = read.clone()
+    torch.cuda._sleep(20_000_000)            # about 10 ms: the copy is still queued when its source is dropped
+    copy = read.clone()
+    del read
+    got = mx.mxfp4_prepack_experts(bq, bs, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(copy, keep)
