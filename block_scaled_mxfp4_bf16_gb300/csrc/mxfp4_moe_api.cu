@@ -39,6 +39,10 @@ StreamArgs stream_args(const void* packed_b, int64_t N, int64_t K, void* c, int6
     return a;
 }
 
+#ifdef MXFP4_TEST_HOOKS
+decltype(StreamArgs::test_give_up) g_give_up = {-1, 0, 0};
+#endif
+
 int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8_t* ws, int terms, cudaStream_t s) {
     a.tblk = ws;
     a.partial = reinterpret_cast<float*>(ws + plan.off_partial);
@@ -58,6 +62,9 @@ int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8
     a.a_block = plan.a_block;
     a.tmem_cols = plan.tmem_cols;
     a.wait_limit_ns = wait_limit_ns();
+#ifdef MXFP4_TEST_HOOKS
+    a.test_give_up = g_give_up;
+#endif
     const cudaError_t e = launch_stream(plan, a, terms, s);
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
@@ -207,5 +214,12 @@ int mxfp4_moe_combine(const void* y, int64_t R, int64_t N, int64_t ldy, const in
                                          static_cast<uint16_t*>(out), ldo, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
+
+#ifdef MXFP4_TEST_HOOKS
+// Test build only (-DMXFP4_TEST_HOOKS, never the product library): in the streaming products enqueued from
+// now on, one thread of one CTA takes the nth wait of its warp for run out (an epilogue warp's nth share,
+// the nth step of a warp that writes tokens or scale factors). cta -1 turns it off.
+void mxfp4_test_stream_give_up(int cta, int thread, int nth) { g_give_up = {cta, thread, nth}; }
+#endif
 
 }  // extern "C"

@@ -437,7 +437,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
         // no copy may be in flight when the CTA ends (after a failure the MMA warp may have
         // stopped waiting for them): the last fill of every stage
         for (int j = max(0, issued - p.stages); j < issued; ++j)
-            mbar_wait(&full[j % p.stages], (j / p.stages) & 1, lim);
+            if (!mbar_wait(&full[j % p.stages], (j / p.stages) & 1, lim)) break;
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------------- MMAs
@@ -532,7 +532,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
             }
             for (; mine < step + u.nk; mine += kTokenWarps) {
                 const int s = mine % p.stages;
-                if (mine >= p.stages && !mbar_wait(&empty[s], (mine / p.stages - 1) & 1, lim)) {
+                if (mine >= p.stages && !warp_wait(p, &empty[s], (mine / p.stages - 1) & 1, mine)) {
                     stream_fail(p, abort_flag);
                     ok = false;
                     break;
@@ -558,11 +558,11 @@ mxfp4_stream_kernel(const StreamArgs p) {
         const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;   // a cluster's parts
         Walk u = start;
         int nshare = 0;
+        bool live = true;
         while (next_share(p, prefix, u)) {
             const int b = nshare & 1;
-            const bool got = mbar_wait(&acc_full[b], (nshare >> 1) & 1, lim);
-            if (!got) stream_fail(p, abort_flag);
-            if (__any_sync(0xffffffffu, !got || *abort_flag != 0u)) break;
+            live = live && share_ready(p, &acc_full[b], (nshare >> 1) & 1, nshare, abort_flag);
+            if (clustered && !live) break;
             tc_fence_after_sync();
             const uint32_t acc = trow + static_cast<uint32_t>(b * p.m_tile);
             const int n = u.nt * kTileN + nl;
@@ -588,12 +588,12 @@ mxfp4_stream_kernel(const StreamArgs p) {
                         if (m0 + i < tokens) st_cluster_f32(to + static_cast<uint32_t>(m0 + i) * (kTileN * 4u), v[i]);
                 }
             } else {
-                store_unit<kTermsPer, false>(p, u, u.nt, acc, half, warp, lane, last_flag,
-                                             epi_stage + (warp - 4) * kEpiStage);
+                live = store_unit<kTermsPer, false>(p, u, u.nt, acc, half, warp, lane, last_flag,
+                                                    epi_stage + (warp - 4) * kEpiStage, live);
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&acc_empty[b]);
+            if (live && lane == 0) mbar_arrive(&acc_empty[b]);
             ++nshare;
         }
         if (clustered && nshare == 0) cluster_wait();   // failed: the handshake all the same

@@ -145,7 +145,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
             }
         }
         for (int j = max(0, issued - p.stages); j < issued; ++j)
-            mbar_wait(&full[j % p.stages], (j / p.stages) & 1, lim);
+            if (!mbar_wait(&full[j % p.stages], (j / p.stages) & 1, lim)) break;
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------------- MMAs, first CTA
@@ -222,7 +222,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
         while (ok && next_share<true>(p, prefix, u)) {
             const bool wide = u.rows > 128;
             for (; mine < step + u.nk; mine += 2) {
-                if (!mbar_wait(&full[s], phase, lim)) {
+                if (!warp_wait(p, &full[s], phase, mine)) {
                     stream_fail(p, abort_flag);
                     ok = false;
                     break;
@@ -238,7 +238,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
                 }
                 if (mine >= kPairSfSlots) {
                     if (mine < kPairSfSlots + 2) old = mine - kPairSfSlots;   // the set's first wait
-                    if (!mbar_wait(&empty[old], old_phase, lim)) {
+                    if (!warp_wait(p, &empty[old], old_phase, mine)) {
                         stream_fail(p, abort_flag);
                         ok = false;
                         break;
@@ -277,17 +277,16 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
         const uint32_t trow = *tmem_slot + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         Walk u = start;
         int nshare = 0;
+        bool live = true;
         while (next_share<true>(p, prefix, u)) {
             const int b = nshare & 1;
-            const bool got = mbar_wait(&acc_full[b], (nshare >> 1) & 1, lim);
-            if (!got) stream_fail(p, abort_flag);
-            if (__any_sync(0xffffffffu, !got || *abort_flag != 0u)) break;
+            live = live && share_ready(p, &acc_full[b], (nshare >> 1) & 1, nshare, abort_flag);
             tc_fence_after_sync();
-            store_unit<1, true>(p, u, 2 * u.nt + static_cast<int>(rank), trow + static_cast<uint32_t>(b * p.m_tile), half, warp,
-                                lane, last_flag, epi_stage + (warp - 4) * kEpiStage);
+            live = store_unit<1, true>(p, u, 2 * u.nt + static_cast<int>(rank), trow + static_cast<uint32_t>(b * p.m_tile), half,
+                                       warp, lane, last_flag, epi_stage + (warp - 4) * kEpiStage, live);
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) arrive_first(map_to_rank(smem_addr(&acc_empty[b]), 0u));
+            if (live && lane == 0) arrive_first(map_to_rank(smem_addr(&acc_empty[b]), 0u));
             ++nshare;
         }
     }

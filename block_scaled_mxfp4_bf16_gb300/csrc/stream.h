@@ -66,6 +66,11 @@ struct StreamArgs {
     int c_wide;               // C's rows are aligned to 16 bytes
     FastDiv by_m_tile, by_k_atoms, by_walkers;   // walkers: CTAs, or pairs of them
     uint64_t wait_limit_ns;
+#ifdef MXFP4_TEST_HOOKS
+    struct {
+        int cta, thread, nth;
+    } test_give_up;           // test build only: see mxfp4_test_stream_give_up
+#endif
 };
 
 struct StreamPlan {

@@ -272,6 +272,41 @@ __device__ __forceinline__ void stream_fail(const StreamArgs& p, volatile uint32
     *abort_flag = 1u;
 }
 
+// A warp's bounded wait, its nth: one decision for all of its lanes, which may run out of time apart (the
+// warp goes on to instructions and barriers that take all of them).
+__device__ __forceinline__ bool warp_wait(const StreamArgs& p, uint64_t* bar, uint32_t parity, int nth) {
+    bool got = mbar_wait(bar, parity, p.wait_limit_ns);
+#ifdef MXFP4_TEST_HOOKS
+    if (static_cast<int>(blockIdx.x) == p.test_give_up.cta && static_cast<int>(threadIdx.x) == p.test_give_up.thread &&
+        nth == p.test_give_up.nth)
+        got = false;
+#endif
+    return __all_sync(0xffffffffu, got);
+}
+
+// Named barrier over `count` threads that also tells all of them whether any said so.
+__device__ __forceinline__ bool named_barrier_any(uint32_t id, uint32_t count, bool mine) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %3, 0;\n\t"
+        "bar.red.or.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(id), "r"(count), "r"(mine ? 1u : 0u)
+        : "memory");
+    return any != 0u;
+}
+
+// Whether an epilogue warp that is still live takes its nth share: not once it, or a warp of another
+// role, ran out of time.
+__device__ __forceinline__ bool share_ready(const StreamArgs& p, uint64_t* bar, uint32_t parity, int nth,
+                                            volatile uint32_t* abort_flag) {
+    const bool got = warp_wait(p, bar, parity, nth);
+    if (!got) stream_fail(p, abort_flag);
+    return __all_sync(0xffffffffu, got && *abort_flag == 0u);
+}
+
 // 16 columns of this lane from column `col` as fp32: tokens (kTermsPer = 1), or sums over kTermsPer
 // columns each, the smallest terms first.
 template <int kTermsPer>
@@ -432,16 +467,21 @@ __device__ __forceinline__ uint32_t arrive(unsigned long long* counter, unsigned
 // A whole unit goes straight out. Of a unit split between CTAs (or pairs), each but the last to
 // arrive leaves its sums in its slot of the workspace (slot 0 for the unit its run begins in, slot 1
 // for one it reaches later); the last adds all of them in the order of K, its own from tensor memory.
+// live: this warp has not given up. The warps decide that apart, but meet at barriers in a split unit: so a
+// warp that has given up still walks on and calls, and the first of those barriers makes the decision a
+// joint one. Returns whether the warp is still live.
 template <int kTermsPer, bool kPair>
-__device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, int nt, uint32_t acc, int half, int warp,
-                                           int lane, volatile uint32_t* last_flag, uint8_t* stage) {
+__device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, int nt, uint32_t acc, int half, int warp,
+                                           int lane, volatile uint32_t* last_flag, uint8_t* stage, bool live) {
     constexpr int kTok = 16 / kTermsPer;         // tokens per 16 columns
     constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
+    const bool split = u.nk != p.k_atoms;
+    if (!split && !live) return false;
     if (kTermsPer == 1 && u.nk == p.k_atoms) {
         const int n0 = nt * kTileN + (warp & 3) * 32;
         if (p.c_wide) store_tile<true>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         else store_tile<false>(p, acc, u.rows, u.row0, n0, half, lane, stage);
-        return;
+        return true;
     }
     const int nl = (warp & 3) * 32 + lane, n = nt * kTileN + nl;
     const int tokens = u.rows / kTermsPer;       // exact: rows are kTermsPer per token
@@ -449,7 +489,6 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
     const int rank = kPair ? static_cast<int>(blockIdx.x & 1u) : 0;
     const int64_t me = walker<kPair>();
     const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;
-    const bool split = u.nk != p.k_atoms;
     bool last = true;
     int64_t unit_step = 0, c_first = 0, c_last = 0;   // the unit's first step, the walkers that share it
     if (split) {
@@ -462,7 +501,7 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
         unsigned long long* counter = p.counters + (c_first * kRanks + rank);   // a split unit is named by its first walker
         if (threadIdx.x == 128)
             flag[0] = *reinterpret_cast<volatile unsigned long long*>(counter) == (p.tag << 8 | others) ? 1u : 0u;
-        named_barrier(2, kStreamEpiThreads);
+        if (named_barrier_any(2, kStreamEpiThreads, !live)) return false;
         last = flag[0] != 0u;
         if (!last) {
             float* mine = p.partial + (static_cast<size_t>(me * kRanks + rank) * 2 + slot) * slot_floats;
@@ -485,7 +524,7 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
         __threadfence();
         if (last && threadIdx.x == 128) *counter = 0ull;   // as found by a replay of this launch
     }
-    if (!last) return;
+    if (!last) return true;
     for (int cb = half * 16; cb < u.rows; cb += 32) {
         float own[kTok], v[kTok];
         const int m0 = cb / kTermsPer;
@@ -528,6 +567,7 @@ __device__ __forceinline__ void store_unit(const StreamArgs& p, const Walk& u, i
         }
         __syncwarp();
     }
+    return true;
 }
 
 }  // namespace mxfp4
