@@ -333,7 +333,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
     uint64_t* acc_empty = acc_full + 2;                          // [2]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
     volatile uint32_t* abort_flag = tmem_slot + 1;
-    volatile uint32_t* last_flag = tmem_slot + 4;                // [4], each written once
+    volatile uint32_t* last_flag = tmem_slot + 4;                // [2] a slot
     int* warp_sum = reinterpret_cast<int*>(tmem_slot + 8);       // [16]
     uint8_t* epi_stage = reinterpret_cast<uint8_t*>(warp_sum + 16);   // [8 warps][kEpiStage]
     int* prefix = reinterpret_cast<int*>(epi_stage + 8 * kEpiStage);  // [groups + 1] token tiles before a group
@@ -354,6 +354,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
         fence_mbar_init();
     } else if (threadIdx.x == 64) {
         *abort_flag = 0u;
+        last_flag[0] = last_flag[2] = 0u;
         prefix[0] = 0;
         if (!p.offsets) {   // one group
             prefix[1] = tiles_of(p.rows, p.m_tile);
@@ -532,7 +533,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
             }
             for (; mine < step + u.nk; mine += kTokenWarps) {
                 const int s = mine % p.stages;
-                if (mine >= p.stages && !warp_wait(p, &empty[s], (mine / p.stages - 1) & 1, mine)) {
+                if (mine >= p.stages && !warp_agrees(p, mbar_wait(&empty[s], (mine / p.stages - 1) & 1, lim), mine)) {
                     stream_fail(p, abort_flag);
                     ok = false;
                     break;
@@ -608,6 +609,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
         tc_fence_after_sync();
         tmem_dealloc(*tmem_slot, p.tmem_cols);
     }
+    if (warp == 4) arrive_unstored<false>(p, prefix, last_flag);
     if (clustered) {
         // No CTA holds tensor memory while it waits for the others, which may still wait for theirs.
         __syncwarp();

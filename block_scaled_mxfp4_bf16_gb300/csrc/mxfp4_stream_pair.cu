@@ -97,6 +97,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
         fence_mbar_init();
     } else if (threadIdx.x == 64) {
         *abort_flag = 0u;
+        last_flag[0] = last_flag[2] = 0u;
         prefix[0] = 0;
     }
     const int tiles = count_tiles<kPairThreads>(p, prefix, begins, warp_sum, warp, lane);
@@ -222,11 +223,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
         while (ok && next_share<true>(p, prefix, u)) {
             const bool wide = u.rows > 128;
             for (; mine < step + u.nk; mine += 2) {
-                if (!warp_wait(p, &full[s], phase, mine)) {
-                    stream_fail(p, abort_flag);
-                    ok = false;
-                    break;
-                }
+                bool got = mbar_wait(&full[s], phase, lim);
                 const uint8_t* wsf = sW + static_cast<uint32_t>(s) * kWBlock + kBRowsBytes + lane * 16;
                 const uint8_t* tsf = sT + static_cast<uint32_t>(s) * t_stage + t_rows + lane * 16;
                 const uint4 w0 = *reinterpret_cast<const uint4*>(wsf), w1 = *reinterpret_cast<const uint4*>(wsf + kSfChunk);
@@ -238,16 +235,17 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
                 }
                 if (mine >= kPairSfSlots) {
                     if (mine < kPairSfSlots + 2) old = mine - kPairSfSlots;   // the set's first wait
-                    if (!warp_wait(p, &empty[old], old_phase, mine)) {
-                        stream_fail(p, abort_flag);
-                        ok = false;
-                        break;
-                    }
+                    got = mbar_wait(&empty[old], old_phase, lim) && got;
                     if ((old += 2) >= p.stages) {
                         old -= p.stages;
                         old_phase ^= 1u;
                     }
                     tc_fence_after_sync();
+                }
+                if (!warp_agrees(p, got, mine)) {
+                    stream_fail(p, abort_flag);
+                    ok = false;
+                    break;
                 }
                 const uint32_t col = t_sf0 + static_cast<uint32_t>(sf) * kPairSfCols;
                 const uint32_t wv[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
@@ -298,6 +296,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
         tc_fence_after_sync();
         tmem_dealloc_pair(*tmem_slot, p.tmem_cols);
     }
+    if (warp == 4) arrive_unstored<true>(p, prefix, last_flag);
 }
 
 cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {

@@ -41,6 +41,23 @@ __host__ __device__ inline int64_t stream_tile_bound(int64_t rows, int64_t group
     return rows / m_tile + groups + 1;
 }
 
+// The arrival counter of a split unit: a call's tag above the arrivals so far (at most seven, since six
+// walkers at most share a unit and a run's ends add one) and a mark that one of them gave up. A word
+// belongs to a call if its upper bits are the call's tag, which no other call has but a replay of the same
+// launch in a graph; anything else, left there by other uses of the workspace, counts as none. So the counters
+// need no launch that clears them, and every walker arrives, one that gave up too: whoever is last leaves
+// the word cleared for a replay, whatever happened.
+constexpr unsigned long long kArrivalMark = 0x80ull;
+__host__ __device__ inline unsigned long long arrival_word(unsigned long long seen, uint64_t tag) {
+    return (seen >> 8) == tag ? seen : static_cast<unsigned long long>(tag << 8);
+}
+__host__ __device__ inline unsigned long long arrival_add(unsigned long long word, bool gave_up) {
+    return (word + 1) | (gave_up ? kArrivalMark : 0ull);
+}
+// Of the word that an arrival found: whether it is the last of others + 1, and whether nobody gave up before.
+__host__ __device__ inline bool arrival_last(unsigned long long word, uint32_t others) { return (word & 0x7Full) == others; }
+__host__ __device__ inline bool arrival_clean(unsigned long long word) { return (word & kArrivalMark) == 0ull; }
+
 struct StreamArgs {
     const uint8_t* tblk;      // token blocks [tile slot][k_atoms][a_block]
     const uint8_t* wblk;      // packed weights, group_bytes from one group to the next
@@ -49,7 +66,7 @@ struct StreamArgs {
     uint16_t* c;
     int64_t ldc;
     float* partial;           // [2 * CTAs][128 * tokens per tile] fp32 partial sums of split units
-    unsigned long long* counters;   // [CTAs] arrivals per split unit under the call's tag
+    unsigned long long* counters;   // [CTAs] arrivals per split unit (arrival_word)
     uint64_t tag;
     // fused: the activations themselves instead of token blocks
     const uint16_t* a;

@@ -272,10 +272,9 @@ __device__ __forceinline__ void stream_fail(const StreamArgs& p, volatile uint32
     *abort_flag = 1u;
 }
 
-// A warp's bounded wait, its nth: one decision for all of its lanes, which may run out of time apart (the
-// warp goes on to instructions and barriers that take all of them).
-__device__ __forceinline__ bool warp_wait(const StreamArgs& p, uint64_t* bar, uint32_t parity, int nth) {
-    bool got = mbar_wait(bar, parity, p.wait_limit_ns);
+// Whether all lanes of the warp got through their bounded waits, the nth time: one decision, since they may
+// run out of time apart and the warp goes on to instructions and barriers that take all of them.
+__device__ __forceinline__ bool warp_agrees(const StreamArgs& p, bool got, int nth) {
 #ifdef MXFP4_TEST_HOOKS
     if (static_cast<int>(blockIdx.x) == p.test_give_up.cta && static_cast<int>(threadIdx.x) == p.test_give_up.thread &&
         nth == p.test_give_up.nth)
@@ -302,9 +301,9 @@ __device__ __forceinline__ bool named_barrier_any(uint32_t id, uint32_t count, b
 // role, ran out of time.
 __device__ __forceinline__ bool share_ready(const StreamArgs& p, uint64_t* bar, uint32_t parity, int nth,
                                             volatile uint32_t* abort_flag) {
-    const bool got = warp_wait(p, bar, parity, nth);
+    const bool got = warp_agrees(p, mbar_wait(bar, parity, p.wait_limit_ns) && *abort_flag == 0u, nth);
     if (!got) stream_fail(p, abort_flag);
-    return __all_sync(0xffffffffu, got && *abort_flag == 0u);
+    return got;
 }
 
 // 16 columns of this lane from column `col` as fp32: tokens (kTermsPer = 1), or sums over kTermsPer
@@ -449,17 +448,59 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
     }
 }
 
-// One more arrival at a split unit's counter: how many came before. A word belongs to this call if
-// its upper bits are the call's tag, which no other call has; anything else, left there by other
-// uses of the workspace, counts as none. So the counters need no launch that clears them.
-// `seen`: the word as read a moment ago.
-__device__ __forceinline__ uint32_t arrive(unsigned long long* counter, unsigned long long seen, uint64_t tag) {
+// One more arrival at a split unit's counter: the call's word as it was before. `seen`: the word as read a
+// moment ago.
+__device__ __forceinline__ unsigned long long arrive(unsigned long long* counter, unsigned long long seen, uint64_t tag,
+                                                     bool gave_up) {
     while (true) {
-        const unsigned long long mine = (seen >> 8) == tag ? seen : static_cast<unsigned long long>(tag << 8);
-        const unsigned long long was = atomicCAS(counter, seen, mine + 1);
-        if (was == seen) return static_cast<uint32_t>(mine & 0xFFu);
+        const unsigned long long mine = arrival_word(seen, tag);
+        const unsigned long long was = atomicCAS(counter, seen, arrival_add(mine, gave_up));
+        if (was == seen) return mine;
         seen = was;
     }
+}
+
+// A split unit of the walk: its first step, and the walkers that share it.
+struct SplitUnit {
+    int64_t step, first, last;
+};
+__device__ __forceinline__ SplitUnit split_unit(const StreamArgs& p, const Walk& u) {
+    SplitUnit s;
+    s.step = static_cast<int64_t>(u.next - 1 - u.base) * p.k_atoms;   // the walk has passed the unit
+    s.first = s.step / u.share;
+    s.last = (s.step + p.k_atoms - 1) / u.share;
+    return s;
+}
+// Its counter, named by the first of those walkers; each CTA of a pair has its own.
+template <bool kPair>
+__device__ __forceinline__ unsigned long long* counter_of(const StreamArgs& p, const SplitUnit& s) {
+    return p.counters + (kPair ? 2 * s.first + (blockIdx.x & 1u) : s.first);
+}
+
+// This walker's slot for it: 0 for the unit its run begins in, 1 for one it reaches later.
+template <bool kPair>
+__device__ __forceinline__ int slot_of(const SplitUnit& s, const Walk& u) {
+    return s.step > static_cast<int64_t>(u.share) * walker<kPair>() ? 1 : 0;
+}
+// What the epilogue leaves for a split unit, [0] of its slot: whether the others' sums were there already, or
+// that it gave up on the unit.
+constexpr uint32_t kGaveUp = 2u;
+
+// At the kernel's end, by one warp: the arrivals that an epilogue that gave up owes split units, without sums
+// (nobody adds such a unit up).
+template <bool kPair>
+__device__ __noinline__ void arrive_unstored(const StreamArgs& p, const int* prefix, const volatile uint32_t* last_flag) {
+    if (last_flag[0] != kGaveUp && last_flag[2] != kGaveUp) return;
+    Walk u = begin_walk<kPair>(p, prefix, prefix[p.groups] * weight_tiles<kPair>(p));
+    while (next_share<kPair>(p, prefix, u)) {
+        if (u.nk == p.k_atoms || (threadIdx.x & 31) != 0) continue;
+        const SplitUnit s = split_unit(p, u);
+        if (last_flag[2 * slot_of<kPair>(s, u)] != kGaveUp) continue;
+        unsigned long long* counter = counter_of<kPair>(p, s);
+        const unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(counter);
+        if (arrival_last(arrive(counter, seen, p.tag, true), static_cast<uint32_t>(s.last - s.first))) *counter = 0ull;
+    }
+    __syncwarp();
 }
 
 // A CTA's share of a unit from its accumulator (at acc in this warp's quarter of the lanes) to C:
@@ -469,7 +510,7 @@ __device__ __forceinline__ uint32_t arrive(unsigned long long* counter, unsigned
 // for one it reaches later); the last adds all of them in the order of K, its own from tensor memory.
 // live: this warp has not given up. The warps decide that apart, but meet at barriers in a split unit: so a
 // warp that has given up still walks on and calls, and the first of those barriers makes the decision a
-// joint one. Returns whether the warp is still live.
+// joint one (arrive_unstored makes up for the arrivals). Returns whether the warp is still live.
 template <int kTermsPer, bool kPair>
 __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, int nt, uint32_t acc, int half, int warp,
                                            int lane, volatile uint32_t* last_flag, uint8_t* stage, bool live) {
@@ -492,16 +533,20 @@ __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, i
     bool last = true;
     int64_t unit_step = 0, c_first = 0, c_last = 0;   // the unit's first step, the walkers that share it
     if (split) {
-        unit_step = static_cast<int64_t>(u.next - 1 - u.base) * p.k_atoms;   // the walk has passed the unit
-        c_first = unit_step / u.share;
-        c_last = (unit_step + p.k_atoms - 1) / u.share;
-        const uint32_t others = static_cast<uint32_t>(c_last - c_first);
-        const int slot = unit_step > u.share * me ? 1 : 0;
+        const SplitUnit shared = split_unit(p, u);
+        unit_step = shared.step;
+        c_first = shared.first;
+        c_last = shared.last;
+        const uint32_t others = static_cast<uint32_t>(shared.last - shared.first);
+        const int slot = slot_of<kPair>(shared, u);
         volatile uint32_t* flag = last_flag + 2 * slot;
-        unsigned long long* counter = p.counters + (c_first * kRanks + rank);   // a split unit is named by its first walker
+        unsigned long long* counter = counter_of<kPair>(p, shared);
         if (threadIdx.x == 128)
             flag[0] = *reinterpret_cast<volatile unsigned long long*>(counter) == (p.tag << 8 | others) ? 1u : 0u;
-        if (named_barrier_any(2, kStreamEpiThreads, !live)) return false;
+        if (named_barrier_any(2, kStreamEpiThreads, !live)) {
+            if (threadIdx.x == 128) flag[0] = kGaveUp;
+            return false;
+        }
         last = flag[0] != 0u;
         if (!last) {
             float* mine = p.partial + (static_cast<size_t>(me * kRanks + rank) * 2 + slot) * slot_floats;
@@ -517,7 +562,12 @@ __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, i
             if (threadIdx.x == 128) seen = *reinterpret_cast<volatile unsigned long long*>(counter);
             __threadfence();
             named_barrier(2, kStreamEpiThreads);
-            if (threadIdx.x == 128) flag[1] = arrive(counter, seen, p.tag) == others ? 1u : 0u;
+            if (threadIdx.x == 128) {
+                const unsigned long long was = arrive(counter, seen, p.tag, false);
+                const bool all = arrival_last(was, others), clean = arrival_clean(was);
+                flag[1] = all && clean ? 1u : 0u;
+                if (all && !clean) *counter = 0ull;
+            }
             named_barrier(2, kStreamEpiThreads);
             last = flag[1] != 0u;
         }

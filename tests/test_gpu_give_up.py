@@ -24,6 +24,8 @@ def hooks():
     vp, i64, sz, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
     L.mxfp4_test_stream_give_up.argtypes = [i32, i32, i32]
     L.mxfp4_test_stream_give_up.restype = None
+    L.mxfp4_test_stream_tag.argtypes = [ctypes.c_uint64]
+    L.mxfp4_test_stream_tag.restype = None
     L.mxfp4_gemv.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, vp, sz, vp]
     L.mxfp4_grouped_gemm.argtypes = [vp, i64, i64, i64, vp, vp, i64, vp, i64, vp, i64, i64, ctypes.c_uint, vp, sz, vp]
     L.mxfp4_device_status.argtypes = [vp]
@@ -33,6 +35,7 @@ def hooks():
     L.mxfp4_grouped_gemm_workspace_size.argtypes = [i64] * 4
     yield L
     L.mxfp4_test_stream_give_up(-1, 0, 0)
+    L.mxfp4_test_stream_tag(0)
 
 
 def prepared(hooks, sizes, N, K):
@@ -92,3 +95,25 @@ def test_a_wait_that_runs_out_ends_the_kernel(hooks, sizes, N, K, cta, thread, n
         torch.cuda.synchronize()
         assert hooks.mxfp4_device_status(None) == 0
         assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+# Every call has the same tag here, as the replays of one graph do, and the workspace is left as the call before
+# left it: a call must not take the arrivals of one that gave up for its own.
+@pytest.mark.parametrize("sizes,N,K,cta,thread,nth", [c for c in CASES if c[0] != 1 or c[1] != 2112])
+def test_a_replay_after_one_that_gave_up(hooks, sizes, N, K, cta, thread, nth):
+    call, out, want = prepared(hooks, sizes, N, K)
+    hooks.mxfp4_test_stream_tag(0x123456789ABCDE)
+    try:
+        for _ in range(3):
+            hooks.mxfp4_test_stream_give_up(cta, thread, nth)
+            assert call() == 0
+            torch.cuda.synchronize()
+            assert hooks.mxfp4_device_status(None) == TIMEOUT
+            hooks.mxfp4_test_stream_give_up(-1, 0, 0)
+            out.zero_()
+            assert call() == 0
+            torch.cuda.synchronize()
+            assert hooks.mxfp4_device_status(None) == 0
+            assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+    finally:
+        hooks.mxfp4_test_stream_tag(0)
