@@ -41,6 +41,14 @@ __host__ __device__ inline int64_t stream_tile_bound(int64_t rows, int64_t group
     return rows / m_tile + groups + 1;
 }
 
+// Division by a group's token tiles: m = tile_reciprocal(tiles) lies less than one below 2^32 / tiles, so x m / 2^32
+// lies less than x / 2^32 below x / tiles, and the quotient is one too small at most for every x < 2^32.
+__host__ __device__ inline uint32_t tile_reciprocal(int tiles) { return 0xFFFFFFFFu / static_cast<uint32_t>(tiles); }
+__host__ __device__ inline int quotient_by_tiles(int x, int divisor, uint32_t m, int shift) {   // divisor: tiles << shift
+    const int q = static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * m >> 32) >> shift;
+    return x - q * divisor >= divisor ? q + 1 : q;
+}
+
 // The arrival counter of a split unit: a call's tag above the arrivals so far (at most seven, since six
 // walkers at most share a unit and a run's ends add one) and a mark that one of them gave up. A word
 // belongs to a call if its upper bits are the call's tag, which no other call has but a replay of the same

@@ -135,7 +135,7 @@ struct Walk {
     int upto;                  // token tiles up to its end
     int tiles, per, begin, n;  // token tiles, rows per tile, sorted rows [begin, begin + n)
     int slot0;                 // the first tile's token-block tile
-    float inv_tiles;
+    uint32_t by_tiles;         // tile_reciprocal(tiles)
 };
 
 // Who walks: a CTA, or the two CTAs of a pair together, with two neighbouring weight tiles as one.
@@ -165,28 +165,15 @@ __device__ __forceinline__ void locate(const StreamArgs& p, const int* prefix, i
         w.first = before * n_tiles;
         w.end = after * n_tiles;
         w.tiles = after - before;
-        w.inv_tiles = __fdividef(1.f, static_cast<float>(w.tiles));
+        w.by_tiles = tile_reciprocal(w.tiles);
         w.begin = prefix[p.groups + 1 + g];        // the groups' first rows follow the prefix
         w.n = prefix[p.groups + 2 + g] - w.begin;
-        // tile_rows(n, m_tile): 16 ceil(n / (16 tiles)), a small quotient, at most one off in fp32
-        const int unit16 = 16 * w.tiles;
-        int q = __float2int_rz(static_cast<float>(w.n - 1) * w.inv_tiles * 0.0625f);
-        if (q * unit16 >= w.n) --q;
-        else if ((q + 1) * unit16 < w.n) ++q;
-        w.per = 16 * (q + 1);
+        w.per = 16 * (quotient_by_tiles(w.n - 1, 16 * w.tiles, w.by_tiles, 4) + 1);   // tile_rows(n, m_tile)
         w.slot0 = static_cast<int>(fast_div(static_cast<uint32_t>(w.begin), p.by_m_tile)) + g;   // tile_slot(begin, g, 0, m_tile)
     }
     const int r = unit - w.first;
-    int nt = w.tiles == 1 ? r : __float2int_rz(static_cast<float>(r) * w.inv_tiles);   // r / tiles, off by one at most
-    int i = r - nt * w.tiles;
-    if (i < 0) {
-        --nt;
-        i += w.tiles;
-    } else if (i >= w.tiles) {
-        ++nt;
-        i -= w.tiles;
-    }
-    w.nt = nt;
+    w.nt = quotient_by_tiles(r, w.tiles, w.by_tiles, 0);
+    const int i = r - w.nt * w.tiles;
     w.slot = w.slot0 + i;
     w.row0 = w.begin + i * w.per;
     w.rows = min(w.per, w.n - i * w.per);
