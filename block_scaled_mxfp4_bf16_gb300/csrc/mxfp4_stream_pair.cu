@@ -9,8 +9,17 @@
 //
 // Roles as in mxfp4_stream.cu, with the scale factors written into tensor memory by warps 12-19
 // (tcgen05.st, one warp per quarter of the lanes, two sets of them in turn; every CTA needs its own weights' and all tokens').
-// Each CTA's copies complete on its own barrier; its scale warps, having seen that, arrive at the
-// first CTA's barrier, whose thread issues the MMAs for both and commits to both CTAs' barriers.
+// A step is ready when the first CTA's barrier for it is: both CTAs' tensor copies of the codes count their
+// bytes there (cta_group::2), and both CTAs' scale warps arrive there. The first CTA's thread then issues the
+// MMAs for both and commits to both CTAs' barriers.
+//
+// What passes between the CTAs: the codes, by copies whose completion releases them at cluster scope; tensor
+// memory (scale factors, accumulators read), ordered by the tcgen05 fences on both sides of an arrival that
+// is relaxed but of cluster scope. So no ordinary store has to be seen across CTAs and nobody needs a release,
+// which is what costs here: copies that complete on their own CTA's barrier, whose scale warps pass that on
+// with a release at cluster scope, take 385 us instead of 210 for 16384 rows in 16 groups x 4096 x 7168.
+#include <cuda.h>
+
 #include <atomic>
 #include <mutex>
 
@@ -38,14 +47,21 @@ __device__ __forceinline__ void mma_pair_if(uint32_t issue, uint32_t d_tmem, uin
         ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue)
         : "memory");
 }
-// Arrive at a barrier of the first CTA. What passes between the CTAs here lies in tensor memory (ordered
-// by the tcgen05 fences on both sides) and in shared memory that bulk copies wrote: no ordinary store
-// has to be seen, so neither the arrival nor the waits ask for cluster scope, which costs far
-// more than the arrival itself (16384 rows in 16 groups x 4096 x 7168: 595 us with cluster scope,
-// 252 without; 227 with the divisions out of the scale warps' loop, 217 with two sets of them, 208 with
-// a cheaper walk and the last wave cut together with the rest; one CTA per unit takes 232).
+// Arrive at a barrier of the first CTA, on either side of tcgen05 fences: nothing but tensor memory is ordered.
 __device__ __forceinline__ void arrive_first(uint32_t cluster_bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+// A box of a matrix of 1 KB rows, from row `row` on, into this CTA's shared memory; its bytes count at a
+// barrier of either CTA.
+__device__ __forceinline__ void tensor_load_if(uint32_t issue, uint32_t dst, const CUtensorMap* map, int row, uint32_t cluster_bar,
+                                               uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.b32 e, %5, 0;\n\t"
+        "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint"
+        " [%0], [%1, {%6, %2}], [%3], %4;\n\t}"
+        ::"r"(dst), "l"(map), "r"(row), "r"(cluster_bar), "l"(policy), "r"(issue), "r"(0)
+        : "memory");
 }
 // Arrive at the barrier of this offset in both CTAs once the MMAs issued so far are done.
 __device__ __forceinline__ void commit_pair_if(uint32_t issue, uint64_t* bar) {
@@ -58,19 +74,26 @@ __device__ __forceinline__ void commit_pair_if(uint32_t issue, uint64_t* bar) {
         : "memory");
 }
 
+// The packed weights and the token blocks as matrices of 1 KB rows (a weight block is 17 of them, 16 of
+// codes). Half a tile's codes are as many rows as it has sixteens of tokens: boxes of 2, 4 .. 12.
+constexpr int kTokenBoxes = 6;
+struct PairMaps {
+    CUtensorMap weights, tokens[kTokenBoxes];
+};
+
 }  // namespace
 
 __global__ void __launch_bounds__(kPairThreads, 1)
-mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
+mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p, const __grid_constant__ PairMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t t_rows = static_cast<uint32_t>(p.m_tile) * 64u;             // half a tile's code rows, at most
     const uint32_t t_stage = t_rows + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
     uint8_t* sW = smem;                                                        // [stages][kWBlock]
     uint8_t* sT = smem + static_cast<uint32_t>(p.stages) * kWBlock;            // [stages][t_stage]
-    uint64_t* full = reinterpret_cast<uint64_t*>(sT + static_cast<uint32_t>(p.stages) * t_stage);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sT + static_cast<uint32_t>(p.stages) * t_stage);   // a stage's scale factors
     uint64_t* empty = full + kStreamMaxStages;
-    uint64_t* ready = empty + kStreamMaxStages;    // first CTA: a stage of both CTAs, with its scale factors
+    uint64_t* ready = empty + kStreamMaxStages;    // first CTA: both CTAs' codes and scale factors of a stage
     uint64_t* acc_full = ready + kStreamMaxStages;                             // [2]
     uint64_t* acc_empty = acc_full + 2;                                        // [2] first CTA: both CTAs' epilogues
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
@@ -89,7 +112,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
     if (threadIdx.x < p.stages) {
         mbar_init(&full[threadIdx.x], 1);
         mbar_init(&empty[threadIdx.x], 1);
-        mbar_init(&ready[threadIdx.x], 8);         // four scale warps of each CTA
+        mbar_init(&ready[threadIdx.x], 9);         // the codes' bytes, and four scale warps of each CTA
         fence_mbar_init();
     } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
         mbar_init(&acc_full[threadIdx.x - 32], 1);
@@ -109,7 +132,8 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
         // ---------------------------------------------------------------------- copies
         const uint32_t issue = elect_lane();
         const uint64_t pol_t = policy_evict_last(), pol_once = policy_evict_first();
-        const uint32_t sw0 = smem_addr(sW), st0 = smem_addr(sT), full0 = smem_addr(full);
+        const uint32_t sw0 = smem_addr(sW), st0 = smem_addr(sT), full0 = smem_addr(full), own_ready0 = smem_addr(ready);
+        const uint32_t ready0 = map_to_rank(own_ready0, 0u);
         pdl_wait_prior_grid();
         Walk u = start;
         int s = 0, issued = 0;
@@ -118,26 +142,34 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
         while (ok && next_share<true>(p, prefix, u)) {
             const uint64_t pol_w = u.tiles > 1 ? pol_t : pol_once;
             const int nt = min(2 * u.nt + static_cast<int>(rank), p.n_tiles - 1);   // past an odd count: the last again, not stored
-            const uint8_t* w = p.wblk + static_cast<size_t>(u.group) * p.group_bytes +
-                               (static_cast<size_t>(nt) * p.k_atoms + u.k0) * kWBlock;
-            const uint8_t* t = p.tblk + (static_cast<size_t>(u.slot) * p.k_atoms + u.k0) * p.a_block;
-            const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15);
-            const uint32_t half_rows = n16 * 64u, tok_sf = (n16 > 128u ? 4u : 2u) * kSfChunk;
-            const uint32_t sf_off = static_cast<uint32_t>(p.m_tile) * 128u;
+            const uint32_t n16 = static_cast<uint32_t>((u.rows + 15) & ~15), half = n16 >> 4;   // half: 1 KB rows a CTA
+            const uint32_t box = (half - 1u) >> 1, tok_rows = (box + 1u) * 2048u, tok_sf = (n16 > 128u ? 4u : 2u) * kSfChunk;
+            // rows of the matrices: blocks of 17 and of a_block / 1024
+            constexpr int kWRows = kWBlock / 1024;
+            const int64_t w_blk = (static_cast<int64_t>(u.group) * p.n_tiles + nt) * p.k_atoms + u.k0;
+            const int64_t t_blk = static_cast<int64_t>(u.slot) * p.k_atoms + u.k0;
+            const int t_step = static_cast<int>(p.a_block >> 10);
+            int w_row = static_cast<int>(w_blk * kWRows), t_row = static_cast<int>(t_blk * t_step + rank * half);
+            const uint8_t* w_sf = p.wblk + static_cast<size_t>(w_blk) * kWBlock + kBRowsBytes;
+            const uint8_t* t_sf = p.tblk + static_cast<size_t>(t_blk) * p.a_block + static_cast<uint32_t>(p.m_tile) * 128u;
             for (int j = 0; j < u.nk; ++j) {
                 if (issued >= p.stages && !mbar_wait(&empty[s], phase ^ 1u, lim)) {
                     stream_fail(p, abort_flag);
                     ok = false;
                     break;
                 }
-                const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
-                const uint32_t dst = st0 + static_cast<uint32_t>(s) * t_stage;
-                mbar_expect_if(issue, bar, kWBlock + half_rows + tok_sf);
-                bulk_load_if(issue, sw0 + static_cast<uint32_t>(s) * kWBlock, w, kWBlock, bar, pol_w);
-                bulk_load_if(issue, dst, t + rank * half_rows, half_rows, bar, pol_t);
-                bulk_load_if(issue, dst + t_rows, t + sf_off, tok_sf, bar, pol_t);
-                w += kWBlock;
-                t += p.a_block;
+                const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u, both = ready0 + static_cast<uint32_t>(s) * 8u;
+                const uint32_t w_dst = sw0 + static_cast<uint32_t>(s) * kWBlock, t_dst = st0 + static_cast<uint32_t>(s) * t_stage;
+                if (rank == 0u) mbar_expect_if(issue, own_ready0 + static_cast<uint32_t>(s) * 8u, 2u * (kBRowsBytes + tok_rows));
+                mbar_expect_if(issue, bar, kWBlock - kBRowsBytes + tok_sf);
+                bulk_load_if(issue, w_dst + kBRowsBytes, w_sf, kWBlock - kBRowsBytes, bar, pol_w);
+                bulk_load_if(issue, t_dst + t_rows, t_sf, tok_sf, bar, pol_t);
+                tensor_load_if(issue, w_dst, &maps.weights, w_row, both, pol_w);
+                tensor_load_if(issue, t_dst, &maps.tokens[box], t_row, both, pol_t);
+                w_row += kWRows;
+                t_row += t_step;
+                w_sf += kWBlock;
+                t_sf += p.a_block;
                 ++issued;
                 if (++s == p.stages) {
                     s = 0;
@@ -145,8 +177,12 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
                 }
             }
         }
+        // No copy may be in flight when its CTA, or the one whose barrier it counts at, ends: the last fill of every
+        // stage, of both CTAs (the second CTA does not end before the first: see the end).
         for (int j = max(0, issued - p.stages); j < issued; ++j)
-            if (!mbar_wait(&full[j % p.stages], (j / p.stages) & 1, lim)) break;
+            if (!mbar_wait(&full[j % p.stages], (j / p.stages) & 1, lim) ||
+                (rank == 0u && !mbar_wait_cluster(&ready[j % p.stages], (j / p.stages) & 1, lim)))
+                break;
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------------- MMAs, first CTA
@@ -173,13 +209,13 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
                 const uint32_t idesc1 = idesc0 | (2u << 29) | (2u << 4);
                 const int b = nshare & 1;
                 const uint32_t t_acc = tmem + static_cast<uint32_t>(b * p.m_tile);
-                if (nshare >= 2 && !mbar_wait(&acc_empty[b], ((nshare >> 1) - 1) & 1, lim)) {
+                if (nshare >= 2 && !mbar_wait_cluster(&acc_empty[b], ((nshare >> 1) - 1) & 1, lim)) {
                     stream_fail(p, abort_flag);
                     break;
                 }
                 tc_fence_after_sync();
                 for (int j = 0; j < u.nk; ++j) {
-                    if (!mbar_wait(&ready[s], phase, lim)) {
+                    if (!mbar_wait_cluster(&ready[s], phase, lim)) {
                         stream_fail(p, abort_flag);
                         ok = false;
                         break;
@@ -299,6 +335,31 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p) {
     if (warp == 4) arrive_unstored<true>(p, prefix, last_flag);
 }
 
+// The driver's encoder of tensor maps, looked up once (the library does not link the driver).
+using TensorMapEncoder = decltype(&cuTensorMapEncodeTiled);
+static TensorMapEncoder tensor_map_encoder() {
+    static std::atomic<TensorMapEncoder> known{nullptr};
+    TensorMapEncoder f = known.load(std::memory_order_acquire);
+    if (f) return f;
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+        return nullptr;
+    f = reinterpret_cast<TensorMapEncoder>(fn);
+    known.store(f, std::memory_order_release);
+    return f;
+}
+
+// `bytes` from `base` on as rows of 1 KB, copied `box` rows at a time.
+static bool encode_rows(TensorMapEncoder encode, CUtensorMap* map, const uint8_t* base, size_t bytes, int box) {
+    const cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(bytes >> 10)}, strides[1] = {1024};
+    const cuuint32_t boxes[2] = {256, static_cast<cuuint32_t>(box)}, steps[2] = {1, 1};
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<uint8_t*>(base), dims, strides, boxes, steps,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {
     static std::mutex mu;
     static std::atomic<bool> done[64];
@@ -313,6 +374,14 @@ cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, c
         if (e != cudaSuccess) return e;
         done[dev].store(true, std::memory_order_release);
     }
+    const TensorMapEncoder encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    PairMaps maps;
+    bool encoded = encode_rows(encode, &maps.weights, args.wblk, args.group_bytes * static_cast<size_t>(args.groups),
+                               static_cast<int>(kBRowsBytes / 1024));
+    for (int i = 0; i < kTokenBoxes; ++i)   // the token blocks end where the counters begin
+        encoded = encoded && encode_rows(encode, &maps.tokens[i], args.tblk, plan.off_counters, 2 * (i + 1));
+    if (!encoded) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.ctas);
     cfg.blockDim = dim3(kPairThreads);
@@ -327,7 +396,7 @@ cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, c
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mxfp4_stream_pair_kernel, args);
+    return cudaLaunchKernelEx(&cfg, mxfp4_stream_pair_kernel, args, maps);
 }
 
 }  // namespace mxfp4

@@ -449,13 +449,14 @@ __device__ __forceinline__ unsigned long long arrive(unsigned long long* counter
 
 // A split unit of the walk: its first step, and the walkers that share it.
 struct SplitUnit {
-    int64_t step, first, last;
+    int64_t step;
+    int first, last;
 };
 __device__ __forceinline__ SplitUnit split_unit(const StreamArgs& p, const Walk& u) {
     SplitUnit s;
     s.step = static_cast<int64_t>(u.next - 1 - u.base) * p.k_atoms;   // the walk has passed the unit
-    s.first = s.step / u.share;
-    s.last = (s.step + p.k_atoms - 1) / u.share;
+    s.first = static_cast<int>(s.step / u.share);
+    s.last = static_cast<int>((s.step + p.k_atoms - 1) / u.share);
     return s;
 }
 // Its counter, named by the first of those walkers; each CTA of a pair has its own.
@@ -503,6 +504,8 @@ __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, i
                                            int lane, volatile uint32_t* last_flag, uint8_t* stage, bool live) {
     constexpr int kTok = 16 / kTermsPer;         // tokens per 16 columns
     constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
+    // The pair kernel has no registers for two: it spilled 136 bytes then, and 16384 rows took 218 us, not 210.
+    constexpr int kFlight = kPair ? 1 : 2;
     const bool split = u.nk != p.k_atoms;
     if (!split && !live) return false;
     if (kTermsPer == 1 && u.nk == p.k_atoms) {
@@ -515,10 +518,11 @@ __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, i
     const int tokens = u.rows / kTermsPer;       // exact: rows are kTermsPer per token
     const int64_t row0 = u.row0 / kTermsPer;
     const int rank = kPair ? static_cast<int>(blockIdx.x & 1u) : 0;
-    const int64_t me = walker<kPair>();
+    const int me = walker<kPair>();
     const size_t slot_floats = static_cast<size_t>(p.m_tile / kTermsPer) * kTileN;
     bool last = true;
-    int64_t unit_step = 0, c_first = 0, c_last = 0;   // the unit's first step, the walkers that share it
+    int64_t unit_step = 0;                       // the unit's first step
+    int c_first = 0, c_last = 0;                 // the walkers that share it
     if (split) {
         const SplitUnit shared = split_unit(p, u);
         unit_step = shared.step;
@@ -572,22 +576,22 @@ __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, i
         } else {
 #pragma unroll
             for (int i = 0; i < kTok; ++i) v[i] = 0.f;
-            // two walkers' sums are on their way at a time, added in the order of K
-            for (int64_t c0 = c_first; c0 <= c_last; c0 += 2) {
-                float theirs[2][kTok];
+            // kFlight walkers' sums are on their way at a time, added in the order of K
+            for (int c0 = c_first; c0 <= c_last; c0 += kFlight) {
+                float theirs[kFlight][kTok];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int64_t c = c0 + q;
+                for (int q = 0; q < kFlight; ++q) {
+                    const int c = c0 + q;
                     if (c > c_last || c == me) continue;
                     // the unit is the first of c's run unless the run began before it
                     const float* src = p.partial + (static_cast<size_t>(c * kRanks + rank) * 2 +
-                                                    (c * u.share < unit_step ? 1 : 0)) * slot_floats;
+                                                    (static_cast<int64_t>(c) * u.share < unit_step ? 1 : 0)) * slot_floats;
 #pragma unroll
                     for (int i = 0; i < kTok; ++i)
                         theirs[q][i] = m0 + i < tokens ? __ldcg(src + static_cast<size_t>(m0 + i) * kTileN + nl) : 0.f;
                 }
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < kFlight; ++q) {
                     if (c0 + q > c_last) continue;
 #pragma unroll
                     for (int i = 0; i < kTok; ++i) v[i] += c0 + q == me ? own[i] : theirs[q][i];
