@@ -457,14 +457,15 @@ constexpr int64_t kCombineFew = 65536;
 template <int kVec, int kPieces, int kFlight>
 __global__ void __launch_bounds__(256)
 combine_kernel(const uint16_t* __restrict__ y, int64_t rows, int64_t ldy, const int32_t* __restrict__ slots,
-                      const float* __restrict__ weights, int64_t T, int k, int vecs, uint16_t* __restrict__ out, int64_t ldo) {
+                      const float* __restrict__ weights, int64_t T, int k, uint32_t vecs, uint16_t* __restrict__ out, int64_t ldo) {
     pdl_launch_dependents();
     pdl_wait_prior_grid();
-    const int lane = threadIdx.x & 31, parts = (vecs + 32 * kPieces - 1) / (32 * kPieces);
+    // a row has up to 2^31 - 1 pieces, and the last part reaches beyond them: unsigned
+    const uint32_t lane = threadIdx.x & 31u, parts = (vecs + 32u * kPieces - 1u) / (32u * kPieces);
     const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); it < T * parts; it += warps) {
-        const int64_t t = it >> 32 ? it / parts : static_cast<int64_t>(static_cast<uint32_t>(it) / static_cast<uint32_t>(parts));
-        const int piece0 = static_cast<int>(it - t * parts) * 32 * kPieces + lane;
+        const int64_t t = it >> 32 ? it / parts : static_cast<int64_t>(static_cast<uint32_t>(it) / parts);
+        const uint32_t piece0 = static_cast<uint32_t>(it - t * parts) * (32u * kPieces) + lane;
         float acc[kPieces][kVec] = {};
         for (int j0 = 0; j0 < k; j0 += kFlight) {
             int32_t slot[kFlight];
@@ -481,7 +482,7 @@ combine_kernel(const uint16_t* __restrict__ y, int64_t rows, int64_t ldy, const 
                 const uint16_t* row = y + slot[u] * ldy + static_cast<int64_t>(piece0) * kVec;
 #pragma unroll
                 for (int i = 0; i < kPieces; ++i)
-                    if (piece0 + 32 * i < vecs) v[u][i] = __ldcs(reinterpret_cast<const Piece<kVec>*>(row + 32 * kVec * i));
+                    if (piece0 + 32u * i < vecs) v[u][i] = __ldcs(reinterpret_cast<const Piece<kVec>*>(row + 32 * kVec * i));
             }
 #pragma unroll
             for (int u = 0; u < kFlight; ++u) {
@@ -502,7 +503,7 @@ combine_kernel(const uint16_t* __restrict__ y, int64_t rows, int64_t ldy, const 
             uint16_t* e = reinterpret_cast<uint16_t*>(&o);
 #pragma unroll
             for (int q = 0; q < kVec; ++q) e[q] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[i][q]));
-            if (piece0 + 32 * i < vecs) __stcs(reinterpret_cast<Piece<kVec>*>(row + 32 * kVec * i), o);
+            if (piece0 + 32u * i < vecs) __stcs(reinterpret_cast<Piece<kVec>*>(row + 32 * kVec * i), o);
         }
     }
 }
@@ -513,9 +514,9 @@ cudaError_t launch_combine(const uint16_t* y, int64_t rows, int64_t ldy, const i
     const uintptr_t at = reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(out);
     const int64_t step = N | ldy | ldo;
     const int vec = at % 16 == 0 && step % 8 == 0 ? 8 : at % 8 == 0 && step % 4 == 0 ? 4 : at % 4 == 0 && step % 2 == 0 ? 2 : 1;
-    const int vecs = static_cast<int>(N / vec);
+    const uint32_t vecs = static_cast<uint32_t>(N / vec);
     auto launch = [&](auto* kernel, int pieces) {
-        const int64_t parts = (vecs + 32 * pieces - 1) / (32 * pieces), blocks = (T * parts + 7) / 8;
+        const int64_t parts = (N / vec + 32 * pieces - 1) / (32 * pieces), blocks = (T * parts + 7) / 8;
         const dim3 grid(static_cast<unsigned>(blocks < 0x7FFFFFFF ? blocks : 0x7FFFFFFF));
         return launch_pdl(kernel, grid, dim3(256), 0, s, y, rows, ldy, slots, weights, T, k, vecs, out, ldo);
     };
