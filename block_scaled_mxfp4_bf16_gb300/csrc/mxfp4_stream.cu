@@ -197,7 +197,7 @@ __device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
 // the element's last bit, and smaller). Four neighbouring lanes share a block, eight elements w
 // each; emit(t, codes, scale byte) gets each term's four code bytes of the lane. All lanes of the
 // warp call. A block that holds an infinity or NaN gets the e8m0 NaN as its scales: the token's
-// outputs become NaN. Scales stop at 2^-127; what lies below is dropped.
+// outputs become NaN. Scales stop at 2^-127, where half of the spacing, 1/4, leaves at most 2^-129.
 template <typename Emit>
 __device__ __forceinline__ void expand_quarter(const uint4& w, Emit emit) {
     const uint32_t words[4] = {w.x, w.y, w.z, w.w};

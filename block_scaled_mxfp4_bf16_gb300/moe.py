@@ -105,8 +105,9 @@ def _index(t: torch.Tensor, shape: tuple, like: torch.Tensor, name: str, dtype=_
 
 def mxfp4_gemv(x: torch.Tensor, packed_b: torch.Tensor, N: int, y: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
-    """Y [M, N] bf16 = x . W^T for a few tokens, x [M, K] kept in bf16 (not quantized), W the MXFP4
-    weights of `packed_b` (mxfp4_prepack_b): the weight-only product, on the weights mxfp4_gemm uses."""
+    """Y [M, N] bf16 = x . W^T for a few tokens, x [M, K] bf16 and not quantized (an element is held to within
+    2^-22 of its 1x32 block's largest magnitude), W the MXFP4 weights of `packed_b` (mxfp4_prepack_b): the
+    weight-only product, on the weights mxfp4_gemm uses."""
     st, device = _begin(x, "x", stream)
     ldx = _bf16_rows(x, "x")
     M, K = x.shape

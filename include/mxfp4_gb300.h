@@ -445,10 +445,12 @@ int mxfp4_gemm_noalloc(const void *a, int64_t M, int64_t K, int64_t lda,
  * mxfp4_gemv -- the weight-only product Y = X . W^T for a few tokens: W in MXFP4, X kept in bf16.
  * Reads the packed weights of mxfp4_gemm, so a model keeps one copy of them for its prompts
  * (mxfp4_gemm) and for single tokens. Unlike mxfp4_gemm, X is not quantized to 4 bits: every 1x32
- * block of X is expanded into eight e2m1 terms with a scale each, which hold it to within 2^-22
- * of the block's largest magnitude, the terms are extra token rows of the block-scaled MMA, and
- * each token's terms are added in fp32. So y is the fp32 product of the bf16 x and the values
- * the weights stand for, rounded once to bf16.
+ * block of X is expanded into eight e2m1 terms with a scale each, the terms are extra token rows of
+ * the block-scaled MMA, and each token's terms are added in fp32. The terms hold every element to
+ * within 2^-22 of its block's largest magnitude, or 2^-129 where that is more. So y is the fp32
+ * product of x held to that and the values the weights stand for, rounded once to bf16: of an
+ * element that is 2^14 times smaller than its block's largest, eight bits count, and of values
+ * below 2^-129 none.
  *   x        : bf16 [M, K], row stride ldx elements (ldx >= K, ldx % 8 == 0), 16-byte aligned.
  *   packed_b : buffer written by mxfp4_prepack_b for the same N and K, 1024-byte aligned.
  *   y        : out, bf16 [M, N], row stride ldy elements (ldy >= N), 2-byte aligned.
@@ -458,8 +460,8 @@ int mxfp4_gemm_noalloc(const void *a, int64_t M, int64_t K, int64_t lda,
  *              read the weights again, and mxfp4_gemm is the faster product).  K: positive
  *              multiple of 8.
  * M == 0 or N == 0 is a no-op. A token whose x holds an infinity or NaN gets NaN outputs; other
- * tokens are not affected. Values of x below 2^-127 may count as zero. Ordering as mxfp4_gemm: x
- * is read and y written after the work before the call on `stream`, packed_b is requested before.
+ * tokens are not affected. Ordering as mxfp4_gemm: x is read and y written after the work before
+ * the call on `stream`, packed_b is requested before.
  * Runs on the same inputs give the same bits. mxfp4_gemv_workspace_size returns 0 for invalid
  * sizes or without a usable device.
  */
