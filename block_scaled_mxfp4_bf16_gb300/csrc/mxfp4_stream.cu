@@ -99,10 +99,8 @@ quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K
     pdl_wait_prior_grid();   // a, index and offsets may come from the previous grid
     // dependents may start now: what they read early (the offsets) was complete before this grid
     pdl_launch_dependents();
-    if (offsets) {
-        for (int i = threadIdx.x; i <= groups; i += blockDim.x) s_offsets[i] = min(max(__ldcg(offsets + i), 0), rows);
-        __syncthreads();
-    }
+    for (int i = threadIdx.x; i <= groups; i += blockDim.x) s_offsets[i] = min(max(__ldcg(offsets + i), 0), rows);
+    __syncthreads();
     const int lane = threadIdx.x & 31, sub = lane / kQuantWidth;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     const int64_t warps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
@@ -113,21 +111,19 @@ quantize_groups_kernel(const uint16_t* __restrict__ a, int64_t tokens, int64_t K
         const int kb0 = static_cast<int>(it - set * parts) * step;
         const int kb1 = min(k_atoms * 8, kb0 + step);
         const int64_t src = r < rows ? (index ? static_cast<int64_t>(index[r]) : r) : -1;
-        int g = 0, begin = 0, n = offsets ? 0 : rows;
-        if (offsets) {
-            for (int left = groups; left > 0;) {     // offsets[1 .. groups] at or below r
-                const int h = left >> 1;
-                if (s_offsets[g + h + 1] <= r) {
-                    g += h + 1;
-                    left -= h + 1;
-                } else {
-                    left = h;
-                }
+        int g = 0, begin = 0, n = 0;
+        for (int left = groups; left > 0;) {         // offsets[1 .. groups] at or below r
+            const int h = left >> 1;
+            if (s_offsets[g + h + 1] <= r) {
+                g += h + 1;
+                left -= h + 1;
+            } else {
+                left = h;
             }
-            if (g < groups) {                        // else past the last group
-                begin = s_offsets[g];
-                n = max(0, s_offsets[g + 1] - begin);
-            }
+        }
+        if (g < groups) {                            // else past the last group
+            begin = s_offsets[g];
+            n = max(0, s_offsets[g + 1] - begin);
         }
         const bool mine = r >= begin && r < begin + n;   // the row belongs to a group
         const int per = tile_rows(n, m_tile);
