@@ -682,9 +682,7 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     const int64_t steps = (terms > 1 ? all_units : tiles * p.n_tiles) * static_cast<int64_t>(p.k_atoms);
     p.ctas = p.cluster > 1 ? static_cast<int>(all_units) * p.cluster : static_cast<int>(steps < sm_count ? steps : sm_count);
     if (p.pair) p.ctas = p.ctas < 2 ? 2 : p.ctas / 2 * 2;
-    int64_t share = (steps + p.ctas - 1) / p.ctas;                                      // as begin_walk
-    if (share < (p.k_atoms + 5) / 6) share = (p.k_atoms + 5) / 6;
-    const bool whole = all_units <= p.ctas && share + kSplitSteps > p.k_atoms;
+    const bool whole = all_units <= p.ctas && split_share((steps + p.ctas - 1) / p.ctas, p.k_atoms) == p.k_atoms;
     const bool one_share = terms > 1 && (p.cluster > 1 || whole);
     p.accs = one_share ? 1 : 2;
     const int per_cta = (p.k_atoms + p.cluster - 1) / p.cluster;

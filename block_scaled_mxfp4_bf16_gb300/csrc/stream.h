@@ -41,6 +41,14 @@ __host__ __device__ inline int64_t stream_tile_bound(int64_t rows, int64_t group
     return rows / m_tile + groups + 1;
 }
 
+// Steps a walker takes of split units, `even` if they were dealt out evenly. A split unit costs what eight steps do
+// (4 us: sums out, arrival, sums in), so whole units where cutting them would not save that, and no unit goes
+// to more than six walkers, or seven where a run ends in it.
+__host__ __device__ inline int64_t split_share(int64_t even, int k_atoms) {
+    const int64_t least = (k_atoms + 5) / 6, share = even > least ? even : least;
+    return share + kSplitSteps > k_atoms ? k_atoms : share;
+}
+
 // Division by a group's token tiles: m = tile_reciprocal(tiles) lies less than one below 2^32 / tiles, so x m / 2^32
 // lies less than x / 2^32 below x / tiles, and the quotient is one too small at most for every x < 2^32.
 __host__ __device__ inline uint32_t tile_reciprocal(int tiles) { return 0xFFFFFFFFu / static_cast<uint32_t>(tiles); }

@@ -194,11 +194,8 @@ __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefi
         return narrow(steps + grid) ? fast_div(static_cast<uint32_t>(steps) + grid - 1, p.by_walkers) : (steps + grid - 1) / grid;
     };
     int64_t steps = static_cast<int64_t>(rest) * p.k_atoms;
-    // a split unit costs what eight steps do (4 us: sums out, arrival, sums in): not for less, and
-    // not among more than six CTAs
     const int64_t even = per_walker(steps);
-    int64_t share = max(even, static_cast<int64_t>((p.k_atoms + 5) / 6));
-    if (share + kSplitSteps > p.k_atoms) share = p.k_atoms;
+    int64_t share = split_share(even, p.k_atoms);
     // With a full wave cut into runs together with the rest, a CTA finds the others' sums of its last unit
     // ready, and the exchange costs less: 8192 rows in 16 groups x 4096 x 2816 88.7 -> 74 us, 16 x 23301 x
     // 5040 weight-only 19.5 -> 16.2 (where it has to save four steps only, 2880 x 2304 46 -> 60).
