@@ -640,7 +640,10 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
         const int64_t mean = (rows + groups - 1) / groups;
         // Fused: the tokens of a tile are quantized again for each of its weight tiles. 1 token, 8 of 64
         // experts x 4096 x 2048: 12.0 us against 12.2 unfused and 4 us less of the host's time; 4 rows
-        // an expert cost 43.1 against 41.6 (gated 51.8 against 42.6).
+        // an expert cost 43.1 against 41.6 (gated 51.8 against 42.6). The rule sees the mean only: where one
+        // expert has most of the rows, its tokens are quantized and its weights read again for every 32 of
+        // them: 128 rows of 64 experts x 4096 x 2048 40.9 against 42.2 dealt out evenly, 30.5 against 25.9 with
+        // a skew of e^2, 14.9 against 16.1 all to one (gated 22.9 against 16.0).
         p.fused = mean <= 2;
         // 128 tokens a tile, 192 where groups are larger. 7200 rows in 48 groups (150 each) x 2880 x 1024:
         // 30.3 us with 192, 33.4 with 128; 12800 rows (266 each) 41.1 and 42.1. Tiles of 64 for the small
@@ -649,10 +652,11 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     }
     p.cluster = 1;
     // Large groups: two CTAs to a unit, which halves the token bytes an SM takes in, where K is long enough
-    // to pay for what a pair does once a unit: 16384 rows in 16 groups x 4096 x 7168 208 us against 232,
-    // x 3584 112 against 122, x 2048 79 against 80, x 1536 68 against 64; 22672 rows in 52 groups x 5664 x
-    // 2560 170 against 181, x 2048 146 against 153, x 1536 120 against 122, but 1408 x 2048 64 against 59.
-    constexpr int kPairSteps = 8;
+    // to pay for what a pair does once a unit: 16384 rows in 16 groups x 4096 x 7168 205 us against 230,
+    // x 3584 114 against 126, x 2048 75 against 82, x 1536 62 against 65, x 1024 52 against 51; 22672 rows in
+    // 52 groups x 5664 x 2560 177 against 192, x 2048 150 against 162, x 1536 121 against 127, but 1408 x
+    // 2048 62.8 against 62.6.
+    constexpr int kPairSteps = 6;
     p.pair = terms == 1 && p.m_tile > 128 && p.n_tiles > 1 && p.k_atoms >= kPairSteps;
     p.nmc = (p.m_tile + 127) / 128;
     p.a_block = static_cast<uint32_t>(p.m_tile) * 128u + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
