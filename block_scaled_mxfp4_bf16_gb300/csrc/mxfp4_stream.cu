@@ -605,7 +605,6 @@ mxfp4_stream_kernel(const StreamArgs p) {
         tc_fence_after_sync();
         tmem_dealloc(*tmem_slot, p.tmem_cols);
     }
-    if (warp == 4) arrive_unstored<false>(p, prefix, last_flag);
     if (clustered) {
         // No CTA holds tensor memory while it waits for the others, which may still wait for theirs.
         __syncwarp();
@@ -619,6 +618,8 @@ mxfp4_stream_kernel(const StreamArgs p) {
                 p.c[(unit_row0 + m) * p.ldc + unit_n] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
             }
         }
+    } else if (threadIdx.x == 128) {
+        arrive_unstored(p, last_flag);
     }
 }
 

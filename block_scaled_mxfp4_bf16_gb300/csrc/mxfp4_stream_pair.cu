@@ -332,7 +332,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p, const __grid_cons
         tc_fence_after_sync();
         tmem_dealloc_pair(*tmem_slot, p.tmem_cols);
     }
-    if (warp == 4) arrive_unstored<true>(p, prefix, last_flag);
+    if (threadIdx.x == 128) arrive_unstored(p, last_flag);
 }
 
 // The driver's encoder of tensor maps, looked up once (the library does not link the driver).

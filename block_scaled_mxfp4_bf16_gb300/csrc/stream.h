@@ -51,7 +51,10 @@ __host__ __device__ inline int64_t split_share(int64_t even, int k_atoms) {
 
 // Division by a group's token tiles: m = tile_reciprocal(tiles) lies less than one below 2^32 / tiles, so x m / 2^32
 // lies less than x / 2^32 below x / tiles, and the quotient is one too small at most for every x < 2^32.
-__host__ __device__ inline uint32_t tile_reciprocal(int tiles) { return 0xFFFFFFFFu / static_cast<uint32_t>(tiles); }
+__host__ __device__ inline uint32_t tile_reciprocal(int tiles) {
+    if (tiles == 1) return 0xFFFFFFFFu;      // as the division has it, which decoding need not wait for
+    return 0xFFFFFFFFu / static_cast<uint32_t>(tiles);
+}
 __host__ __device__ inline int quotient_by_tiles(int x, int divisor, uint32_t m, int shift) {   // divisor: tiles << shift
     const int q = static_cast<int>(static_cast<uint64_t>(static_cast<uint32_t>(x)) * m >> 32) >> shift;
     return x - q * divisor >= divisor ? q + 1 : q;

@@ -467,25 +467,22 @@ template <bool kPair>
 __device__ __forceinline__ int slot_of(const SplitUnit& s, const Walk& u) {
     return s.step > static_cast<int64_t>(u.share) * walker<kPair>() ? 1 : 0;
 }
-// What the epilogue leaves for a split unit, [0] of its slot: whether the others' sums were there already, or
-// that it gave up on the unit.
-constexpr uint32_t kGaveUp = 2u;
+// What the epilogue leaves for a split unit in the two words of its slot: whether the others' sums were there already,
+// or, if it gave up on the unit, this above the others' number, and the unit's counter.
+constexpr uint32_t kGaveUp = 0x100u;
 
-// At the kernel's end, by one warp: the arrivals that an epilogue that gave up owes split units, without sums
-// (nobody adds such a unit up).
-template <bool kPair>
-__device__ __noinline__ void arrive_unstored(const StreamArgs& p, const int* prefix, const volatile uint32_t* last_flag) {
-    if (last_flag[0] != kGaveUp && last_flag[2] != kGaveUp) return;
-    Walk u = begin_walk<kPair>(p, prefix, prefix[p.groups] * weight_tiles<kPair>(p));
-    while (next_share<kPair>(p, prefix, u)) {
-        if (u.nk == p.k_atoms || (threadIdx.x & 31) != 0) continue;
-        const SplitUnit s = split_unit(p, u);
-        if (last_flag[2 * slot_of<kPair>(s, u)] != kGaveUp) continue;
-        unsigned long long* counter = counter_of<kPair>(p, s);
+// At the kernel's end, by one thread: the arrivals that an epilogue that gave up owes split units, without sums
+// (nobody adds such a unit up). They stand last because their code costs time wherever the other calls run past
+// it: in front of the cluster's sums 0.1 us of 11 x 2880 x 2040's 6.2.
+__device__ __forceinline__ void arrive_unstored(const StreamArgs& p, const volatile uint32_t* last_flag) {
+#pragma unroll 1
+    for (int slot = 0; slot < 2; ++slot) {
+        const uint32_t word = last_flag[2 * slot];
+        if (word < kGaveUp) continue;
+        unsigned long long* counter = p.counters + last_flag[2 * slot + 1];
         const unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(counter);
-        if (arrival_last(arrive(counter, seen, p.tag, true), static_cast<uint32_t>(s.last - s.first))) *counter = 0ull;
+        if (arrival_last(arrive(counter, seen, p.tag, true), word - kGaveUp)) *counter = 0ull;
     }
-    __syncwarp();
 }
 
 // A CTA's share of a unit from its accumulator (at acc in this warp's quarter of the lanes) to C:
@@ -532,7 +529,10 @@ __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, i
         if (threadIdx.x == 128)
             flag[0] = *reinterpret_cast<volatile unsigned long long*>(counter) == (p.tag << 8 | others) ? 1u : 0u;
         if (named_barrier_any(2, kStreamEpiThreads, !live)) {
-            if (threadIdx.x == 128) flag[0] = kGaveUp;
+            if (threadIdx.x == 128) {
+                flag[1] = static_cast<uint32_t>(counter - p.counters);
+                flag[0] = kGaveUp + others;
+            }
             return false;
         }
         last = flag[0] != 0u;
