@@ -69,8 +69,9 @@ __device__ __forceinline__ void sort_keys(uint32_t (&key)[kPer]) {
 // the largest is the one with the lowest index and the expert is read off it. fp32 logits: a key
 // has no room for the index. It is looked up at the end, in the winning lane's unsorted keys; where
 // a winning key comes twice, the token is done again in rounds that compare the indexes too.
-// Bound by instructions: about 300 a token and warp for 256 experts and k = 8 (rounds that search
-// all of a lane's keys took 650).
+// 570 instructions a token and warp for 256 experts and k = 8, half of the issue slots: what holds it back
+// is their order (a warp-wide maximum a round) as much as their number. Past 256 experts the keys, the
+// logits and their copy for ties do not fit 64 registers: some 70 bytes of spills.
 template <int kPer, bool kBf16>
 __device__ __forceinline__ void top_k(const RouteArgs& p, const uint32_t (&logit)[kPer], int lane, uint32_t* key_out,
                                       int* expert_out, float* weight_out) {

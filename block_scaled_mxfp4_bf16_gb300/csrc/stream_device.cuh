@@ -197,8 +197,9 @@ __device__ __forceinline__ Walk begin_walk(const StreamArgs& p, const int* prefi
     const int64_t even = per_walker(steps);
     int64_t share = split_share(even, p.k_atoms);
     // With a full wave cut into runs together with the rest, a CTA finds the others' sums of its last unit
-    // ready, and the exchange costs less: 8192 rows in 16 groups x 4096 x 2816 88.7 -> 74 us, 16 x 23301 x
-    // 5040 weight-only 19.5 -> 16.2 (where it has to save four steps only, 2880 x 2304 46 -> 60).
+    // ready, and the exchange costs less: 8192 rows in 16 groups x 4096 x 2816 83 -> 65 us, 16 x 23301 x 5040
+    // weight-only 19.8 -> 17.1 (where it has to save four steps only, 1200 rows in 4 groups x 2880 x 2304
+    // 16.4 -> 20.4).
     if (w.waves > 0 && rest > 0 && even + kMergeSteps < min(share + kSplitSteps, static_cast<int64_t>(p.k_atoms))) {
         --w.waves;
         steps += static_cast<int64_t>(grid) * p.k_atoms;
