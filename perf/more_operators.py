@@ -311,7 +311,7 @@ def _exact_act(name, z):
     if name == "silu":
         return z * torch.sigmoid(z)
     if name == "gelu":
-        return z * torch.special.ndtr(z)
+        return z * torch.special.erfc(-z / 2 ** 0.5) / 2   # Phi without a difference of near values
     # (1 + tanh t) / 2 = sigmoid(2 t)
     return z * torch.sigmoid(2 * (2 / math.pi) ** 0.5 * (z + 0.044715 * z ** 3))
 
