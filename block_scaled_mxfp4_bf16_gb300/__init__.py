@@ -23,7 +23,9 @@ __all__ = [
     "mxfp4_gemm_plan", "mxfp4_gemm_plan_model", "mxfp4_device_status", "mxfp4_selftest_timeout", "mxfp4_version",
     "PreparedCall", "prepare_gemm", "prepare_gemm_host", "TokenBlocks", "mxfp4_token_tile", "mxfp4_token_blocks_size",
     "mxfp4_quantize_tokens", "mxfp4_gemm_tokens", "mxfp4_gemm_unpacked", "mxfp4_gemv", "mxfp4_grouped_gemm",
-    "mxfp4_prepack_experts", "MoeRouting", "mxfp4_moe_route", "mxfp4_moe_combine",
+    "mxfp4_prepack_experts", "MoeRouting", "mxfp4_moe_route", "mxfp4_moe_combine", "mxfp4_linear",
+    "mxfp4_prepack_gated_size", "mxfp4_prepack_gated", "mxfp4_prepack_gated_experts", "mxfp4_gated_linear",
+    "mxfp4_grouped_gated_linear",
 ]
 
 _LOCK = threading.Lock()
@@ -153,6 +155,24 @@ def load_library() -> ctypes.CDLL:
             L.mxfp4_moe_route.restype = _int
             L.mxfp4_moe_combine.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _int, _vp, _i64, _vp]
             L.mxfp4_moe_combine.restype = _int
+            L.mxfp4_linear_workspace_size.argtypes = [_i64, _i64, _i64]
+            L.mxfp4_linear_workspace_size.restype = _sz
+            L.mxfp4_linear.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _int, _int, _vp, _i64, _vp, _i64, _vp, _sz,
+                                       _vp]
+            L.mxfp4_linear.restype = _int
+            L.mxfp4_prepack_gated_size.argtypes = [_i64, _i64]
+            L.mxfp4_prepack_gated_size.restype = _sz
+            L.mxfp4_prepack_gated.argtypes = [_vp, _vp, _i64, _i64, _vp, _vp]
+            L.mxfp4_prepack_gated.restype = _int
+            L.mxfp4_gated_linear_workspace_size.argtypes = [_i64, _i64, _i64]
+            L.mxfp4_gated_linear_workspace_size.restype = _sz
+            L.mxfp4_gated_linear.argtypes = [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _int, _int, _vp, _i64, _vp, _sz, _vp]
+            L.mxfp4_gated_linear.restype = _int
+            L.mxfp4_grouped_gated_linear_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
+            L.mxfp4_grouped_gated_linear_workspace_size.restype = _sz
+            L.mxfp4_grouped_gated_linear.argtypes = [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _int, _int,
+                                                     _vp, _i64, _i64, _vp, _sz, _vp]
+            L.mxfp4_grouped_gated_linear.restype = _int
             _LIB = L
     return _LIB
 
@@ -662,3 +682,5 @@ def mxfp4_selftest_timeout(limit_us: int, stream=None) -> None:
 
 from .moe import (MoeRouting, mxfp4_gemv, mxfp4_grouped_gemm, mxfp4_moe_combine, mxfp4_moe_route,  # noqa: E402
                   mxfp4_prepack_experts)
+from .linear import (mxfp4_gated_linear, mxfp4_grouped_gated_linear, mxfp4_linear, mxfp4_prepack_gated,  # noqa: E402
+                     mxfp4_prepack_gated_experts, mxfp4_prepack_gated_size)

@@ -5,6 +5,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 namespace mxfp4 {
 
 constexpr int kMaxStages = 8;
@@ -82,7 +84,10 @@ constexpr int kResMaxItemsPerThread = 2;   // 1x32 blocks of A per quantizing th
 constexpr int kResManyItemsPerThread = 6;
 // Rows of the 128-row weight tile each cluster rank owns in the split-K reduction, and the
 // fp32 words one owned row takes per source in the receive buffer (tokens rounded up to 4).
-__host__ __device__ inline int res_rows_per_owner(int splits) { return (kTileN + splits - 1) / splits; }
+// row_unit: 1, or 16 for gated weights, so that an owner has both rows of every feature it has one of.
+__host__ __device__ inline int res_rows_per_owner(int splits, int row_unit = 1) {
+    return ((kTileN + splits - 1) / splits + row_unit - 1) / row_unit * row_unit;
+}
 __host__ __device__ inline int res_row_words(int m_valid) { return (m_valid + 3) / 4 * 4; }
 
 // Tiling of one mxfp4_gemm call.
@@ -103,6 +108,7 @@ struct GemmPlan {
                        // declared it ready and the plan leaves the SM room for it)
     int many_items;    // weight-resident path: more than kResMaxItemsPerThread blocks of A per
                        // quantizing thread (only with a_early)
+    int row_unit;      // weight-resident path: an owner's rows are a multiple of this (gated weights: 16)
     int ctas;
     uint32_t a_block;  // bytes of one token block
     // shared-memory layout (bytes from a 1 KB-aligned base): weight stages at 0, token blocks
@@ -164,6 +170,27 @@ struct ResidentArgs {
 #endif
 };
 
+// What happens to a product's sums before they are stored (epilogue.cuh).
+constexpr int kEpiPlain = 0, kEpiLinear = 1, kEpiGated = 2;
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
+struct Epilogue {
+    const void* bias;          // bf16 or fp32, or null. Linear: [N]; gated: the gate's [features], then the up's
+    int bias_bf16;
+    int act;
+    const uint16_t* residual;  // linear: bf16, row stride ldr, or null
+    int64_t ldr;
+    int features;              // gated: columns of the output
+};
+// A kernel's arguments, with an epilogue's where the instantiation has one.
+template <typename Args>
+struct WithEpilogue : Args {
+    Epilogue epi;
+};
+template <typename Args, int kEpi>
+using EpilogueArgs = std::conditional_t<kEpi == kEpiPlain, Args, WithEpilogue<Args>>;
+// Packed rows of gated weights of I features (epilogue.cuh): eight of the gate's, eight of the up projection's.
+__host__ __device__ inline int64_t gated_rows(int64_t I) { return (I + 7) / 8 * 16; }
+
 // Device properties the planner needs (cached per device).
 struct DeviceInfo {
     int device;
@@ -174,12 +201,20 @@ struct DeviceInfo {
 };
 
 int device_info(DeviceInfo* out);   // MXFP4_OK or an error status
+int cuda_fail(cudaError_t e);       // records e for mxfp4_last_cuda_error, returns MXFP4_ERR_CUDA
+uint64_t wait_limit_ns();           // limit of every bounded wait
 // cluster_caps: if not null, cluster_caps[s] (s = 1..kMaxSplits) is how many clusters of s CTAs
 // can be resident at once, used instead of asking the current device (no CUDA call is made).
 // a_ready: the caller declared A ready (MXFP4_GEMM_A_READY), which can change the weight-resident
 // plan (GemmPlan::a_early).
 int make_plan(int64_t M, int64_t N, int64_t K, int path_req, int splits_req, int mtile_req, int sm_count,
-              GemmPlan* plan, const int* cluster_caps = nullptr, bool a_ready = false);
+              GemmPlan* plan, const int* cluster_caps = nullptr, bool a_ready = false, int row_unit = 1);
+// The automatic plan of a product whose owners' rows are a multiple of row_unit, from a per-thread table.
+int cached_linear_plan(const DeviceInfo& di, int64_t M, int64_t N, int64_t K, int row_unit, GemmPlan* plan);
+// Enqueue a planned GEMM, its sums through an epilogue of this kind (kEpiPlain: epi is not used).
+int run_gemm(const GemmPlan& plan, const DeviceInfo& di, const void* a, int64_t M, int64_t K, int64_t lda,
+             const void* packed_b, int64_t N, void* c, int64_t ldc, uint8_t* ws, cudaStream_t s,
+             bool quantize_a = true, bool a_ready = false, int kind = 0, const Epilogue* epi = nullptr);
 size_t packed_b_bytes(int64_t N, int64_t K);
 
 // Exact unsigned 32-bit division by a divisor fixed at launch: the round-up multiplier with one
@@ -223,8 +258,13 @@ cudaError_t launch_stage_rows(const void* src, int64_t lda, void* dst, int64_t r
 // Pre-quantized B (natural layout) -> weight blocks [n_tiles][k_atoms][kWBlock].
 cudaError_t launch_prepack(const uint8_t* bq, const uint8_t* bs, int64_t N, int64_t K, uint8_t* out,
                            cudaStream_t s);
+// The same for gated weights: 2 I rows, the gate's and then the up projection's, interleaved by eight (epilogue.cuh).
+cudaError_t launch_prepack_gated(const uint8_t* bq, const uint8_t* bs, int64_t I, int64_t K, uint8_t* out, cudaStream_t s);
 cudaError_t launch_gemm(const GemmPlan& plan, const GemmArgs& args, cudaStream_t s);
 cudaError_t launch_gemm_resident(const GemmPlan& plan, const ResidentArgs& args, cudaStream_t s);
+// The same with an epilogue, kind: kEpiLinear or kEpiGated.
+cudaError_t launch_gemm(const GemmPlan& plan, const WithEpilogue<GemmArgs>& args, int kind, cudaStream_t s);
+cudaError_t launch_gemm_resident(const GemmPlan& plan, const WithEpilogue<ResidentArgs>& args, int kind, cudaStream_t s);
 // Clusters of `cluster_size` weight-resident CTAs with this much shared memory resident at once.
 int max_active_clusters_resident(int cluster_size, size_t smem_bytes);
 cudaError_t launch_timeout_selftest(uint32_t* status, uint64_t limit_ns, cudaStream_t s);

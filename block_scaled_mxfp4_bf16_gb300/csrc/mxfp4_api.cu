@@ -210,7 +210,7 @@ static int plan_resident_layout(GemmPlan& p, bool one_per_sm, int max_items = kR
     p.off_a = static_cast<uint32_t>(p.atoms_max) * kWBlock;
     p.off_araw = 0;
     p.off_recv = p.off_a + static_cast<uint32_t>(p.atoms_max) * p.a_block;
-    const size_t recv_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * res_rows_per_owner(p.splits) *
+    const size_t recv_bytes = p.splits > 1 ? static_cast<size_t>(p.splits) * res_rows_per_owner(p.splits, p.row_unit) *
                                                  res_row_words(p.m_tile) * sizeof(float)
                                            : 0;
     p.off_bar = static_cast<uint32_t>(align_up(p.off_recv + recv_bytes, 16));
@@ -252,9 +252,10 @@ static bool res_early_ok(const GemmPlan& q) {
 }
 
 static int make_resident_plan(int64_t M, int64_t N, int64_t K, int splits_req, int mtile_req, int sm_count,
-                              GemmPlan* P, const int* cluster_caps, bool a_ready) {
+                              GemmPlan* P, const int* cluster_caps, bool a_ready, int row_unit) {
     GemmPlan p = {};
     p.path = 3;
+    p.row_unit = row_unit;
     if (mtile_req != 0 && mtile_req != 16 && mtile_req != 32) return MXFP4_ERR_ARG;
     p.k_atoms = static_cast<int>(cdiv(K, kAtomK));
     p.m_tile = M <= 16 || p.k_atoms <= 2 ? 16 : kResMaxMTile;
@@ -338,11 +339,12 @@ static int token_tile(int64_t M, int64_t K, int mtile_req) {
 }
 
 int make_plan(int64_t M, int64_t N, int64_t K, int path_req, int splits_req, int mtile_req, int sm_count,
-              GemmPlan* P, const int* cluster_caps, bool a_ready) {
+              GemmPlan* P, const int* cluster_caps, bool a_ready, int row_unit) {
     GemmPlan p = {};
     if (M <= 0 || N <= 0 || K <= 0) return MXFP4_ERR_SHAPE;
     if (mtile_req < 0 || mtile_req > kMaxMTile || mtile_req % 16 != 0) return MXFP4_ERR_ARG;
-    if (path_req == 3) return make_resident_plan(M, N, K, splits_req, mtile_req, sm_count, P, cluster_caps, a_ready);
+    if (path_req == 3)
+        return make_resident_plan(M, N, K, splits_req, mtile_req, sm_count, P, cluster_caps, a_ready, row_unit);
     p.m_tile = token_tile(M, K, mtile_req);
     p.nmc = (p.m_tile + 127) / 128;
     p.m_tiles = static_cast<int>(cdiv(M, p.m_tile));
@@ -355,7 +357,7 @@ int make_plan(int64_t M, int64_t N, int64_t K, int path_req, int splits_req, int
     // Up to 32 tokens the weight-resident kernel is the automatic choice wherever its K slices
     // fit (it measured faster than both other paths on every such workload).
     if (path_req == 0 && M <= 32 && mtile_req == 0 &&
-        make_resident_plan(M, N, K, splits_req, 0, sm_count, P, cluster_caps, a_ready) == MXFP4_OK)
+        make_resident_plan(M, N, K, splits_req, 0, sm_count, P, cluster_caps, a_ready, row_unit) == MXFP4_OK)
         return MXFP4_OK;
     // Fused quantization puts A's load and quantization on the GEMM's critical path (behind the
     // dependency wait), while the two-kernel path overlaps them with the weight prologue but adds
@@ -442,10 +444,11 @@ int make_plan(int64_t M, int64_t N, int64_t K, int path_req, int splits_req, int
 // a small per-thread table instead of running the planner on every call (about 0.5 us of host
 // time a call on the benchmark's workloads).
 static int cached_plan(const DeviceInfo& di, int64_t M, int64_t N, int64_t K, int path_req, int splits_req,
-                       int mtile_req, GemmPlan* P, bool a_ready = false) {
+                       int mtile_req, GemmPlan* P, bool a_ready = false, int row_unit = 1) {
     struct Entry {
         int device, path, splits, mtile;
         bool a_ready;
+        int row_unit;
         int64_t M, N, K;
         GemmPlan plan;
         bool used;
@@ -456,17 +459,21 @@ static int cached_plan(const DeviceInfo& di, int64_t M, int64_t N, int64_t K, in
     for (int i = 0; i < kEntries; ++i) {
         const Entry& e = table[i];
         if (e.used && e.M == M && e.N == N && e.K == K && e.device == di.device && e.path == path_req &&
-            e.splits == splits_req && e.mtile == mtile_req && e.a_ready == a_ready) {
+            e.splits == splits_req && e.mtile == mtile_req && e.a_ready == a_ready && e.row_unit == row_unit) {
             *P = e.plan;
             return MXFP4_OK;
         }
     }
-    const int st = make_plan(M, N, K, path_req, splits_req, mtile_req, di.sm_count, P, nullptr, a_ready);
+    const int st = make_plan(M, N, K, path_req, splits_req, mtile_req, di.sm_count, P, nullptr, a_ready, row_unit);
     if (st != MXFP4_OK) return st;
     Entry& e = table[next];
     next = (next + 1) % kEntries;
-    e = Entry{di.device, path_req, splits_req, mtile_req, a_ready, M, N, K, *P, true};
+    e = Entry{di.device, path_req, splits_req, mtile_req, a_ready, row_unit, M, N, K, *P, true};
     return MXFP4_OK;
+}
+
+int cached_linear_plan(const DeviceInfo& di, int64_t M, int64_t N, int64_t K, int row_unit, GemmPlan* P) {
+    return cached_plan(di, M, N, K, 0, 0, 0, P, false, row_unit);
 }
 
 static uint64_t g_wait_limit_ns = 1000000000ull;   // 1 s per bounded wait
@@ -491,11 +498,11 @@ static int check_gemm_args(const void* a, int64_t M, int64_t K, int64_t lda, con
 
 // Enqueue one planned GEMM: the quantize kernel into `ws` for the two-kernel path, then the GEMM.
 // quantize_a = false: the two-kernel plan's token blocks are already in `ws` (the GEMM alone).
-static int run_gemm(const GemmPlan& plan, const DeviceInfo& di, const void* a, int64_t M, int64_t K, int64_t lda,
-                    const void* packed_b, int64_t N, void* c, int64_t ldc, uint8_t* ws, cudaStream_t s,
-                    bool quantize_a = true, bool a_ready = false) {
+int run_gemm(const GemmPlan& plan, const DeviceInfo& di, const void* a, int64_t M, int64_t K, int64_t lda,
+             const void* packed_b, int64_t N, void* c, int64_t ldc, uint8_t* ws, cudaStream_t s, bool quantize_a,
+             bool a_ready, int kind, const Epilogue* epi) {
     if (plan.path == 3) {
-        ResidentArgs r = {};
+        WithEpilogue<ResidentArgs> r = {};
         r.a = static_cast<const uint16_t*>(a);
         r.lda = lda;
         r.bblk = static_cast<const uint8_t*>(packed_b);
@@ -521,7 +528,9 @@ static int run_gemm(const GemmPlan& plan, const DeviceInfo& di, const void* a, i
 #ifdef MXFP4_TEST_HOOKS
         r.token_dump = static_cast<uint8_t*>(g_token_dump);
 #endif
-        cudaError_t e = launch_gemm_resident(plan, r, s);
+        if (kind != kEpiPlain) r.epi = *epi;
+        const cudaError_t e = kind == kEpiPlain ? launch_gemm_resident(plan, static_cast<const ResidentArgs&>(r), s)
+                                                : launch_gemm_resident(plan, r, kind, s);
         return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
     }
     if (plan.path == 2 && quantize_a) {
@@ -529,7 +538,7 @@ static int run_gemm(const GemmPlan& plan, const DeviceInfo& di, const void* a, i
                                                plan.m_tiles, plan.k_atoms, plan.a_block, a_ready, s);
         if (e != cudaSuccess) return cuda_fail(e);
     }
-    GemmArgs g = {};
+    WithEpilogue<GemmArgs> g = {};
     g.a = static_cast<const uint16_t*>(a);
     g.lda = lda;
     g.ablk = ws;
@@ -562,11 +571,14 @@ static int run_gemm(const GemmPlan& plan, const DeviceInfo& di, const void* a, i
     g.sf_stores = plan.sf_stores;
     g.a_ready = a_ready ? 1 : 0;
     g.c_vec4 = (ldc % 4 == 0 && aligned(c, 8)) ? 1 : 0;
+    if (kind == kEpiGated) g.c_vec4 = (ldc % 2 == 0 && aligned(c, 4)) ? 1 : 0;   // two features a store
+    if (kind == kEpiLinear && epi->residual && (epi->ldr % 4 != 0 || !aligned(epi->residual, 8))) g.c_vec4 = 0;
     g.wait_limit_ns = g_wait_limit_ns;
 #ifdef MXFP4_TEST_HOOKS
     g.token_dump = static_cast<uint8_t*>(g_token_dump);
 #endif
-    cudaError_t e = launch_gemm(plan, g, s);
+    if (kind != kEpiPlain) g.epi = *epi;
+    const cudaError_t e = kind == kEpiPlain ? launch_gemm(plan, static_cast<const GemmArgs&>(g), s) : launch_gemm(plan, g, kind, s);
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
 
@@ -628,7 +640,7 @@ const char* mxfp4_status_string(int status) {
 
 int mxfp4_last_cuda_error(void) { return t_last_cuda_error; }
 
-int mxfp4_version(void) { return 205; }
+int mxfp4_version(void) { return 206; }
 
 int mxfp4_quantize(const void* x, int64_t rows, int64_t K, int64_t ld, void* q, void* scales, void* stream) {
     if (rows < 0 || K < 0) return MXFP4_ERR_ARG;

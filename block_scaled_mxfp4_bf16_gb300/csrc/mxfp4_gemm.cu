@@ -41,6 +41,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "epilogue.cuh"
 #include "internal.h"
 #include "mma_desc.cuh"
 #include "ptx.cuh"
@@ -181,9 +182,10 @@ __device__ __forceinline__ void quantize_slice(const QuantSlice& q, int qt, cons
 // kWide (with it): its tiles of more than 128 tokens, two issuers sharing every step (below),
 // kSfStores (with it): scale factors written into tensor memory by epilogue warps (below);
 // the other instantiation takes the path and the issue scheme from its arguments.
-template <bool kTwoKernel, bool kWide, bool kSfStores>
+// kEpi: what the sums go through before they are stored (epilogue.cuh).
+template <bool kTwoKernel, bool kWide, bool kSfStores, int kEpi>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-mxfp4_gemm_kernel(const GemmArgs p) {
+mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
     static_assert(kTwoKernel || (!kWide && !kSfStores), "the fused path copies its own scale factors");
     const bool fused = kTwoKernel ? false : p.fused != 0;
     extern __shared__ uint8_t smem_raw[];
@@ -577,7 +579,25 @@ mxfp4_gemm_kernel(const GemmArgs p) {
     __syncwarp();
     if (S == 1) {
         // one K slice: tensor memory -> bf16 C directly, one output column per thread
-        if (warp >= 3 && ok) {
+        if constexpr (kEpi != kEpiPlain) {
+            if (warp >= 3 && ok) {
+                pdl_wait_prior_grid();             // the residual and the bias may be the previous grid's
+                for (int cb = half * 32; cb < m_valid; cb += 64) {
+                    const int cnt = min(32, m_valid - cb);
+                    uint32_t r[32];
+                    if constexpr (kEpi == kEpiLinear) {
+                        uint16_t res[32];
+                        residual_run(p.epi, p.N, n, m0 + cb, cnt, res);
+                        load_acc32(trow + cb, cb + 16 < m_valid, nacc, acc2, r);
+                        store_run(p.epi, p.N, n, m0 + cb, cnt, reinterpret_cast<float(&)[32]>(r), res, p.c, p.ldc);
+                    } else {
+                        load_acc32(trow + cb, cb + 16 < m_valid, nacc, acc2, r);
+                        store_run_gated(p.epi, 0, n, m0 + cb, cnt, reinterpret_cast<float(&)[32]>(r), p.c, p.ldc);
+                    }
+                    __syncwarp();
+                }
+            }
+        } else if (warp >= 3 && ok) {
             for (int cb = half * 32; cb < m_valid; cb += 64) {
                 uint32_t r[32];
                 load_acc32(trow + cb, cb + 16 < m_valid, nacc, acc2, r);
@@ -656,11 +676,14 @@ mxfp4_gemm_kernel(const GemmArgs p) {
         // word reports it). The bytes it still lacks belong to a peer that failed before posting:
         // a peer that posted has its copy land well within the limit.
         const bool owner = warp >= 3 && r1 > r0;
-        const bool got = !owner || mbar_wait_cluster(red_bar, 0, lim);
+        bool got = !owner || mbar_wait_cluster(red_bar, 0, lim);
         if (!got) fail(p, flags);
+        // lanes may run out of time apart, but exchange what they have below
+        if (kEpi == kEpiGated) got = __all_sync(0xffffffffu, got);
         __syncwarp();
         cluster_arrive();
         if (threadIdx.x == 96) MXFP4_PHASE(9);
+        if (kEpi != kEpiPlain && owner) pdl_wait_prior_grid();   // for the residual and the bias
         if (owner && got) {
             // a thread sums 4 consecutive columns of rows lm, lm+8, lm+16, lm+24 over the sources
             // in rank order; the four rows' values of a source are loaded before any is added
@@ -698,6 +721,13 @@ mxfp4_gemm_kernel(const GemmArgs p) {
                 for (int u = 0; u < kRows; ++u) {
                     const int lm = lm0 + u * kEpiWarps;
                     if (lm >= nrows) break;
+                    if constexpr (kEpi == kEpiLinear) {
+                        store_quad(p.epi, p.N, n4, m0 + r0 + lm, acc[u], p.c, p.ldc, p.c_vec4 != 0);
+                        continue;
+                    } else if constexpr (kEpi == kEpiGated) {
+                        store_quad_gated(p.epi, n4, m0 + r0 + lm, acc[u], p.c, p.ldc, p.c_vec4 != 0);
+                        continue;
+                    }
                     uint16_t* crow = p.c + static_cast<int64_t>(m0 + r0 + lm) * p.ldc;
                     const uint32_t lo = pack_bf16x2(acc[u].x, acc[u].y), hi = pack_bf16x2(acc[u].z, acc[u].w);
                     if (v4) {
@@ -767,17 +797,18 @@ mxfp4_gemm_kernel(const GemmArgs p) {
             tmem_dealloc(tmem_base, p.tmem_cols);
         }
         if (warp >= 3 && r1 > r0) {
-            if (!mbar_wait_cluster(red_bar, 0, lim)) {   // rows missing: no sum, no stores
-                fail(p, flags);
-                return;
-            }
+            bool got = mbar_wait_cluster(red_bar, 0, lim);
+            if (!got) fail(p, flags);
+            if (kEpi == kEpiGated) got = __all_sync(0xffffffffu, got);   // one decision: see above
+            if (!got) return;          // rows missing: no sum, no stores
             if (threadIdx.x == 96) MXFP4_PHASE(9);
             // owner: a thread sums 4 consecutive rows of one column over the sources in rank order
             const int et = threadIdx.x - 96;
             const int nrows = r1 - r0;
             const int cn = et & (kTileN - 1);
             const int nn = n0 + cn;
-            if (nn < p.N) {
+            if (kEpi != kEpiPlain) pdl_wait_prior_grid();        // for the residual and the bias
+            if (kEpi != kEpiPlain || nn < p.N) {
                 for (int lm = (et / kTileN) * 4; lm < nrows; lm += 4 * (kEpiThreads / kTileN)) {
                     float4 acc = *reinterpret_cast<const float4*>(sRecv + cn * stride + lm);
                     for (int src = 1; src < S; ++src) {
@@ -786,6 +817,17 @@ mxfp4_gemm_kernel(const GemmArgs p) {
                         acc.y += v.y;
                         acc.z += v.z;
                         acc.w += v.w;
+                    }
+                    if constexpr (kEpi == kEpiLinear) {
+                        float run[4] = {acc.x, acc.y, acc.z, acc.w};
+                        uint16_t res[4];
+                        residual_run(p.epi, p.N, nn, m0 + r0 + lm, min(4, nrows - lm), res);
+                        store_run(p.epi, p.N, nn, m0 + r0 + lm, min(4, nrows - lm), run, res, p.c, p.ldc);
+                        continue;
+                    } else if constexpr (kEpi == kEpiGated) {
+                        const float run[4] = {acc.x, acc.y, acc.z, acc.w};
+                        store_run_gated(p.epi, 0, nn, m0 + r0 + lm, min(4, nrows - lm), run, p.c, p.ldc);
+                        continue;
                     }
                     uint16_t* cp = p.c + static_cast<int64_t>(m0 + r0 + lm) * p.ldc + nn;
                     const float vals[4] = {acc.x, acc.y, acc.z, acc.w};
@@ -840,6 +882,7 @@ mxfp4_gemm_kernel(const GemmArgs p) {
         tmem_dealloc(tmem_base, p.tmem_cols);
     }
     if (warp >= 3) {
+        if (kEpi != kEpiPlain) pdl_wait_prior_grid();   // for the residual and the bias
         // owner: a thread sums 4 consecutive columns of one row over the sources in rank order
         const int et = threadIdx.x - 96;
         const int nrows = r1 - r0;
@@ -854,6 +897,13 @@ mxfp4_gemm_kernel(const GemmArgs p) {
                 acc.y += v.y;
                 acc.z += v.z;
                 acc.w += v.w;
+            }
+            if constexpr (kEpi == kEpiLinear) {
+                store_quad(p.epi, p.N, n4, m0 + r0 + lm, acc, p.c, p.ldc, p.c_vec4 != 0);
+                continue;
+            } else if constexpr (kEpi == kEpiGated) {
+                store_quad_gated(p.epi, n4, m0 + r0 + lm, acc, p.c, p.ldc, p.c_vec4 != 0);
+                continue;
             }
             uint16_t* crow = p.c + static_cast<int64_t>(m0 + r0 + lm) * p.ldc;
             const uint32_t lo = pack_bf16x2(acc.x, acc.y), hi = pack_bf16x2(acc.z, acc.w);
@@ -881,7 +931,21 @@ __global__ void timeout_selftest_kernel(uint32_t* status, uint64_t limit_ns) {
     }
 }
 
+namespace {
+// The instantiations with one epilogue.
+template <int kEpi>
+struct GemmKernels {
+    using Kernel = void (*)(const EpilogueArgs<GemmArgs, kEpi>);
+    static constexpr Kernel fused = mxfp4_gemm_kernel<false, false, false, kEpi>;
+    static constexpr Kernel copies = mxfp4_gemm_kernel<true, false, false, kEpi>;
+    static constexpr Kernel stores = mxfp4_gemm_kernel<true, false, true, kEpi>;
+    static constexpr Kernel halves = mxfp4_gemm_kernel<true, true, true, kEpi>;
+};
+}  // namespace
+
+template <int kEpi>
 static cudaError_t set_kernel_attributes() {
+    using K = GemmKernels<kEpi>;
     static std::mutex mu;
     static std::atomic<bool> attr_set[64] = {};
     int dev = 0;
@@ -891,8 +955,7 @@ static cudaError_t set_kernel_attributes() {
     if (attr_set[dev].load(std::memory_order_acquire)) return cudaSuccess;
     std::lock_guard<std::mutex> lock(mu);
     if (!attr_set[dev].load(std::memory_order_relaxed)) {
-        for (auto* kernel : {mxfp4_gemm_kernel<false, false, false>, mxfp4_gemm_kernel<true, false, false>,
-                             mxfp4_gemm_kernel<true, false, true>, mxfp4_gemm_kernel<true, true, true>}) {
+        for (auto* kernel : {K::fused, K::copies, K::stores, K::halves}) {
             cudaFuncAttributes fa = {};
             e = cudaFuncGetAttributes(&fa, kernel);
             if (e != cudaSuccess) return e;
@@ -908,7 +971,8 @@ static cudaError_t set_kernel_attributes() {
 }
 
 int max_active_clusters(int cluster_size, size_t smem_bytes) {
-    if (set_kernel_attributes() != cudaSuccess) return 0;
+    using K = GemmKernels<kEpiPlain>;
+    if (set_kernel_attributes<kEpiPlain>() != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster_size);
     cfg.blockDim = dim3(kGemmThreads);
@@ -921,8 +985,7 @@ int max_active_clusters(int cluster_size, size_t smem_bytes) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int best = -1;   // the same resources in every instantiation; the smallest count if they ever differ
-    for (auto* kernel : {mxfp4_gemm_kernel<false, false, false>, mxfp4_gemm_kernel<true, false, false>,
-                         mxfp4_gemm_kernel<true, false, true>, mxfp4_gemm_kernel<true, true, true>}) {
+    for (auto* kernel : {K::fused, K::copies, K::stores, K::halves}) {
         int n = 0;
         if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
             cudaGetLastError();
@@ -933,8 +996,10 @@ int max_active_clusters(int cluster_size, size_t smem_bytes) {
     return best;
 }
 
-cudaError_t launch_gemm(const GemmPlan& plan, const GemmArgs& args, cudaStream_t s) {
-    cudaError_t e = set_kernel_attributes();
+template <int kEpi>
+static cudaError_t launch_gemm_as(const GemmPlan& plan, const EpilogueArgs<GemmArgs, kEpi>& args, cudaStream_t s) {
+    using K = GemmKernels<kEpi>;
+    cudaError_t e = set_kernel_attributes<kEpi>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.ctas);
@@ -950,10 +1015,16 @@ cudaError_t launch_gemm(const GemmPlan& plan, const GemmArgs& args, cudaStream_t
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = plan.splits > 1 ? 2 : 1;
-    if (args.fused) return cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<false, false, false>, args);
-    if (args.m_tile > 128 && args.issuers == 2) return cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<true, true, true>, args);
-    return args.sf_stores ? cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<true, false, true>, args)
-                          : cudaLaunchKernelEx(&cfg, mxfp4_gemm_kernel<true, false, false>, args);
+    if (args.fused) return cudaLaunchKernelEx(&cfg, K::fused, args);
+    if (args.m_tile > 128 && args.issuers == 2) return cudaLaunchKernelEx(&cfg, K::halves, args);
+    return cudaLaunchKernelEx(&cfg, args.sf_stores ? K::stores : K::copies, args);
+}
+
+cudaError_t launch_gemm(const GemmPlan& plan, const GemmArgs& args, cudaStream_t s) {
+    return launch_gemm_as<kEpiPlain>(plan, args, s);
+}
+cudaError_t launch_gemm(const GemmPlan& plan, const WithEpilogue<GemmArgs>& args, int kind, cudaStream_t s) {
+    return kind == kEpiGated ? launch_gemm_as<kEpiGated>(plan, args, s) : launch_gemm_as<kEpiLinear>(plan, args, s);
 }
 
 cudaError_t launch_timeout_selftest(uint32_t* status, uint64_t limit_ns, cudaStream_t s) {

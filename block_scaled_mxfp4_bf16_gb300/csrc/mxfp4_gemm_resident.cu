@@ -32,6 +32,7 @@
 #include <initializer_list>
 #include <mutex>
 
+#include "epilogue.cuh"
 #include "internal.h"
 #include "mma_desc.cuh"
 #include "ptx.cuh"
@@ -109,9 +110,10 @@ __device__ __forceinline__ void quantize_item(const AItem& it, const uint32_t (&
 
 // kMany: up to kResManyItemsPerThread blocks of A per quantizing thread, loaded three at a time
 // (plans that read A before the dependency wait); otherwise at most two, all loaded at once.
-template <bool kMany>
+// kEpi: what the sums go through before they are stored (epilogue.cuh).
+template <bool kMany, int kEpi>
 __global__ void __launch_bounds__(kResThreads, 1)
-mxfp4_gemm_resident_kernel(const ResidentArgs p) {
+mxfp4_gemm_resident_kernel(const EpilogueArgs<ResidentArgs, kEpi> p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     uint8_t* sB = smem;                               // weight blocks, one per 256-K step
@@ -142,7 +144,7 @@ mxfp4_gemm_resident_kernel(const ResidentArgs p) {
     const int atoms_max = base + (rem > 0 ? 1 : 0);
     const int m_valid = (p.M - m0) < p.m_tile ? (p.M - m0) : p.m_tile;
     const uint64_t lim = p.wait_limit_ns;
-    const int R = res_rows_per_owner(S);              // weight rows each rank owns
+    const int R = res_rows_per_owner(S, kEpi == kEpiGated ? 16 : 1);   // weight rows each rank owns
     const int words = res_row_words(m_valid);         // fp32 per owned row per source
     const int own0 = split * R;
     const int own_rows = max(0, min(R, kTileN - own0));
@@ -351,18 +353,67 @@ mxfp4_gemm_resident_kernel(const ResidentArgs p) {
     // still be posting into this CTA. Warps 8..11, done with A, join the epilogue warps in it when
     // the owned (row, group) pairs outnumber the epilogue's 128 threads.
     const int G = words / 4;                          // groups of 4 tokens
-    const bool sum_helpers = S > 1 && own_rows * G > 128;
+    // gated: a thread sums both rows of a feature
+    const int own_sums = kEpi == kEpiGated ? own_rows / 2 : own_rows;
+    const bool sum_helpers = S > 1 && own_sums * G > 128;
     const int sum_threads = sum_helpers ? 256 : 128;
     auto owner_sum = [&](const int t0, const bool ok_in) {
         const bool got = mbar_wait_cluster(red_bar, 0, lim);
         if (!got) res_fail(p, abort_flag);
         if (threadIdx.x == 128) RES_PHASE(9);
-        if (got && ok_in) {
+        if constexpr (kEpi == kEpiGated) {
+            if (!(got && ok_in)) return;
+            const float4* rv = reinterpret_cast<const float4*>(sRecv);
+            for (int t = t0; t < own_sums * G; t += sum_threads) {
+                const int g = t / own_sums;
+                const int fr = t - g * own_sums;
+                const int r = (fr >> 3) * 16 + (fr & 7);      // the gate's row; the up projection's is 8 further
+                const int f = gated_feature(n0 + own0 + r);
+                float zg[4] = {0.f, 0.f, 0.f, 0.f}, zu[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int s0 = 0; s0 < S; s0 += 4) {
+                    float4 x[4], y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (s0 + i < S) {
+                            x[i] = rv[((s0 + i) * G + g) * R + r];
+                            y[i] = rv[((s0 + i) * G + g) * R + r + 8];
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (s0 + i < S) {
+                            zg[0] += x[i].x;
+                            zg[1] += x[i].y;
+                            zg[2] += x[i].z;
+                            zg[3] += x[i].w;
+                            zu[0] += y[i].x;
+                            zu[1] += y[i].y;
+                            zu[2] += y[i].z;
+                            zu[3] += y[i].w;
+                        }
+                    }
+                }
+                if (f < p.epi.features) {
+                    const float bg = bias_at(p.epi, f), bu = bias_at(p.epi, p.epi.features + f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) zg[i] += bg;
+                    activate(p.epi.act, zg);
+                    uint16_t* cp = p.c + static_cast<int64_t>(m0 + 4 * g) * p.ldc + f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (4 * g + i < m_valid) *cp = to_bf16(zg[i] * (zu[i] + bu));
+                        cp += p.ldc;
+                    }
+                }
+            }
+        } else if (got && ok_in) {
             const float4* rv = reinterpret_cast<const float4*>(sRecv);
             for (int t = t0; t < own_rows * G; t += sum_threads) {
                 const int g = t / own_rows;
                 const int r = t - g * own_rows;
                 const int n = n0 + own0 + r;
+                uint16_t res[4];
+                if constexpr (kEpi == kEpiLinear) residual_run(p.epi, p.N, n, m0 + 4 * g, min(4, m_valid - 4 * g), res);
                 float4 acc = rv[g * R + r];
                 for (int s0 = 1; s0 < S; s0 += 8) {
                     float4 x[8];
@@ -379,7 +430,10 @@ mxfp4_gemm_resident_kernel(const ResidentArgs p) {
                         }
                     }
                 }
-                if (n < p.N) {
+                if constexpr (kEpi == kEpiLinear) {
+                    float run[4] = {acc.x, acc.y, acc.z, acc.w};
+                    store_run(p.epi, p.N, n, m0 + 4 * g, min(4, m_valid - 4 * g), run, res, p.c, p.ldc);
+                } else if (n < p.N) {
                     uint16_t* cp = p.c + static_cast<int64_t>(m0 + 4 * g) * p.ldc + n;
                     const float vals[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
@@ -458,7 +512,14 @@ mxfp4_gemm_resident_kernel(const ResidentArgs p) {
 
     if (S == 1) {
         // one K slice: accumulator -> bf16 C, one output column per thread
-        if (ok && n0 + nl < p.N) {
+        // (the residual and the bias may be the previous grid's: every warp but 1 and 2 has waited for it)
+        if constexpr (kEpi == kEpiLinear) {
+            uint16_t res[32];
+            residual_run(p.epi, p.N, n0 + nl, m0, m_valid, res);
+            if (ok) store_run(p.epi, p.N, n0 + nl, m0, m_valid, reinterpret_cast<float(&)[32]>(v), res, p.c, p.ldc);
+        } else if constexpr (kEpi == kEpiGated) {
+            if (ok) store_run_gated(p.epi, 0, n0 + nl, m0, m_valid, reinterpret_cast<float(&)[32]>(v), p.c, p.ldc);
+        } else if (ok && n0 + nl < p.N) {
             uint16_t* cp = p.c + static_cast<int64_t>(m0) * p.ldc + n0 + nl;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -499,6 +560,7 @@ mxfp4_gemm_resident_kernel(const ResidentArgs p) {
 #endif
 }
 
+template <int kEpi>
 static cudaError_t set_resident_attributes() {
     static std::mutex mu;
     static std::atomic<bool> attr_set[64] = {};
@@ -509,8 +571,8 @@ static cudaError_t set_resident_attributes() {
     if (attr_set[dev].load(std::memory_order_acquire)) return cudaSuccess;
     std::lock_guard<std::mutex> lock(mu);
     if (!attr_set[dev].load(std::memory_order_relaxed)) {
-        for (const void* fn : {reinterpret_cast<const void*>(mxfp4_gemm_resident_kernel<false>),
-                               reinterpret_cast<const void*>(mxfp4_gemm_resident_kernel<true>)}) {
+        for (const void* fn : {reinterpret_cast<const void*>(mxfp4_gemm_resident_kernel<false, kEpi>),
+                               reinterpret_cast<const void*>(mxfp4_gemm_resident_kernel<kEpi == kEpiPlain, kEpi>)}) {
             cudaFuncAttributes fa = {};
             e = cudaFuncGetAttributes(&fa, fn);
             if (e != cudaSuccess) return e;
@@ -526,7 +588,7 @@ static cudaError_t set_resident_attributes() {
 }
 
 int max_active_clusters_resident(int cluster_size, size_t smem_bytes) {
-    if (set_resident_attributes() != cudaSuccess) return 0;
+    if (set_resident_attributes<kEpiPlain>() != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster_size);
     cfg.blockDim = dim3(kResThreads);
@@ -539,15 +601,16 @@ int max_active_clusters_resident(int cluster_size, size_t smem_bytes) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, mxfp4_gemm_resident_kernel<false>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&n, mxfp4_gemm_resident_kernel<false, kEpiPlain>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         return 0;
     }
     return n;
 }
 
-cudaError_t launch_gemm_resident(const GemmPlan& plan, const ResidentArgs& args, cudaStream_t s) {
-    cudaError_t e = set_resident_attributes();
+template <int kEpi>
+static cudaError_t launch_resident_as(const GemmPlan& plan, const EpilogueArgs<ResidentArgs, kEpi>& args, cudaStream_t s) {
+    cudaError_t e = set_resident_attributes<kEpi>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(plan.ctas);
@@ -563,8 +626,17 @@ cudaError_t launch_gemm_resident(const GemmPlan& plan, const ResidentArgs& args,
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = plan.splits > 1 ? 2 : 1;
-    if (plan.many_items) return cudaLaunchKernelEx(&cfg, mxfp4_gemm_resident_kernel<true>, args);
-    return cudaLaunchKernelEx(&cfg, mxfp4_gemm_resident_kernel<false>, args);
+    // (only a call that declares A ready has such a plan, and none with an epilogue does)
+    if (kEpi == kEpiPlain && plan.many_items)
+        return cudaLaunchKernelEx(&cfg, mxfp4_gemm_resident_kernel<kEpi == kEpiPlain, kEpi>, args);
+    return cudaLaunchKernelEx(&cfg, mxfp4_gemm_resident_kernel<false, kEpi>, args);
+}
+
+cudaError_t launch_gemm_resident(const GemmPlan& plan, const ResidentArgs& args, cudaStream_t s) {
+    return launch_resident_as<kEpiPlain>(plan, args, s);
+}
+cudaError_t launch_gemm_resident(const GemmPlan& plan, const WithEpilogue<ResidentArgs>& args, int kind, cudaStream_t s) {
+    return kind == kEpiGated ? launch_resident_as<kEpiGated>(plan, args, s) : launch_resident_as<kEpiLinear>(plan, args, s);
 }
 
 }  // namespace mxfp4

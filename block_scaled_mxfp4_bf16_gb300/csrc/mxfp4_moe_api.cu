@@ -45,24 +45,7 @@ uint64_t g_tag = 0;
 #endif
 
 int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8_t* ws, int terms, cudaStream_t s) {
-    a.tblk = ws;
-    a.partial = reinterpret_cast<float*>(ws + plan.off_partial);
-    a.counters = reinterpret_cast<unsigned long long*>(ws + plan.off_counters);
-    a.tag = next_call_tag();
-    a.status = di.status;
-    a.m_tile = plan.m_tile;
-    a.by_m_tile = make_fastdiv(static_cast<uint32_t>(plan.m_tile));
-    a.by_k_atoms = make_fastdiv(static_cast<uint32_t>(plan.k_atoms));
-    a.by_walkers = make_fastdiv(static_cast<uint32_t>(plan.pair ? plan.ctas / 2 : plan.ctas));
-    a.nmc = plan.nmc;
-    a.n_tiles = plan.n_tiles;
-    a.k_atoms = plan.k_atoms;
-    a.stages = plan.stages;
-    a.cluster = plan.cluster;
-    a.accs = plan.accs;
-    a.a_block = plan.a_block;
-    a.tmem_cols = plan.tmem_cols;
-    a.wait_limit_ns = wait_limit_ns();
+    fill_stream_args(plan, di, ws, &a);
 #ifdef MXFP4_TEST_HOOKS
     a.test_give_up = g_give_up;
     if (g_tag) a.tag = g_tag;

@@ -160,12 +160,14 @@ quantize_blocks4_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t K,
 // Weight prepack: one thread per (row, block) of the padded [n_tiles*128, k_atoms*256] matrix;
 // copies 16 bytes of e2m1 into the swizzled rows and the scale byte into its chunk. Input rows
 // are the natural layout: nblk = ceil(K/32) blocks of 16 code bytes and one scale byte each.
+// kGated: N = 2 I rows, the gate's and then the up projection's, which the packed matrix interleaves by eight.
+template <bool kGated>
 __global__ void __launch_bounds__(256)
 prepack_kernel(const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bs, int64_t N, int64_t K,
                uint8_t* __restrict__ out, int k_atoms) {
     const int64_t nblk = (K + 31) / 32;
     const int64_t row_items = 8 * static_cast<int64_t>(k_atoms);
-    const int64_t rows_cover = (N + kTileN - 1) / kTileN * kTileN;
+    const int64_t rows_cover = ((kGated ? gated_rows(N / 2) : N) + kTileN - 1) / kTileN * kTileN;
     const int64_t items = rows_cover * row_items;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
     for (int64_t it = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; it < items; it += stride) {
@@ -176,9 +178,14 @@ prepack_kernel(const uint8_t* __restrict__ bq, const uint8_t* __restrict__ bs, i
         uint8_t* blk = out + (static_cast<size_t>(r / kTileN) * k_atoms + static_cast<size_t>(kbp >> 3)) * kWBlock;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
         uint8_t sc = 0;
-        if (r < N && kbp < nblk) {
-            v = __ldg(reinterpret_cast<const uint4*>(bq + r * (nblk * 16) + kbp * 16));
-            sc = bs[r * nblk + kbp];
+        int64_t from = r;                         // the row of B, N or more: none
+        if (kGated) {
+            const int64_t f = (r >> 4) * 8 + (r & 7);
+            from = f < N / 2 ? f + ((r & 8) ? N / 2 : 0) : N;
+        }
+        if (from < N && kbp < nblk) {
+            v = __ldg(reinterpret_cast<const uint4*>(bq + from * (nblk * 16) + kbp * 16));
+            sc = bs[from * nblk + kbp];
         }
         *reinterpret_cast<uint4*>(blk + swz_chunk_offset(rr, c)) = v;
         blk[kBRowsBytes + block_sf_offset(rr, c)] = sc;
@@ -269,7 +276,15 @@ cudaError_t launch_prepack(const uint8_t* bq, const uint8_t* bs, int64_t N, int6
     const int threads = 256;
     const int k_atoms = static_cast<int>((K + kAtomK - 1) / kAtomK);
     const int64_t rows_cover = (N + kTileN - 1) / kTileN * kTileN;
-    prepack_kernel<<<grid_for(rows_cover * 8 * k_atoms, threads), threads, 0, s>>>(bq, bs, N, K, out, k_atoms);
+    prepack_kernel<false><<<grid_for(rows_cover * 8 * k_atoms, threads), threads, 0, s>>>(bq, bs, N, K, out, k_atoms);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_prepack_gated(const uint8_t* bq, const uint8_t* bs, int64_t I, int64_t K, uint8_t* out, cudaStream_t s) {
+    const int threads = 256;
+    const int k_atoms = static_cast<int>((K + kAtomK - 1) / kAtomK);
+    const int64_t rows_cover = (gated_rows(I) + kTileN - 1) / kTileN * kTileN;
+    prepack_kernel<true><<<grid_for(rows_cover * 8 * k_atoms, threads), threads, 0, s>>>(bq, bs, 2 * I, K, out, k_atoms);
     return cudaGetLastError();
 }
 

@@ -313,9 +313,10 @@ __device__ __forceinline__ void write_step(const StreamArgs& p, const Walk& u, i
 
 // kFused: tiles of few rows, whose tokens warps of their own (2, 3 and from 12 on) quantize or expand
 // straight into the stages, a step each in turn: no token blocks in memory and no launch before this one.
-template <int kTermsPer, bool kFused>
+// kEpi: what the sums go through before they are stored (epilogue.cuh).
+template <int kTermsPer, bool kFused, int kEpi>
 __global__ void __launch_bounds__(stream_threads(kTermsPer, kFused), 1)
-mxfp4_stream_kernel(const StreamArgs p) {
+mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p) {
     constexpr int kThreads = stream_threads(kTermsPer, kFused);
     constexpr int kTokenWarps = token_warps(kTermsPer);
     extern __shared__ uint8_t smem_raw[];
@@ -585,7 +586,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
                         if (m0 + i < tokens) st_cluster_f32(to + static_cast<uint32_t>(m0 + i) * (kTileN * 4u), v[i]);
                 }
             } else {
-                live = store_unit<kTermsPer, false>(p, u, u.nt, acc, half, warp, lane, last_flag,
+                live = store_unit<kTermsPer, false, kEpi>(p, u, u.nt, acc, half, warp, lane, last_flag,
                                                     epi_stage + (warp - 4) * kEpiStage, live);
             }
             tc_fence_before_sync();
@@ -626,7 +627,7 @@ mxfp4_stream_kernel(const StreamArgs p) {
 // ------------------------------------------------------------------------ plan and launches
 
 int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count,
-                     int (*clusters_of)(int), StreamPlan* out) {
+                     int (*clusters_of)(int), StreamPlan* out, int m_tile) {
     StreamPlan p = {};
     p.k_atoms = static_cast<int>((K + kAtomK - 1) / kAtomK);
     p.n_tiles = static_cast<int>((N + kTileN - 1) / kTileN);
@@ -650,6 +651,10 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
         // 30.3 us with 192, 33.4 with 128; 12800 rows (266 each) 41.1 and 42.1. Tiles of 64 for the small
         // groups of decoding gained nothing: 480 rows x 4096 x 4096 71.7 us and 70.1 with 128.
         p.m_tile = p.fused ? 32 : mean <= 128 ? 128 : 192;
+        if (m_tile) {
+            p.fused = 0;
+            p.m_tile = m_tile;
+        }
     }
     p.cluster = 1;
     // Large groups: two CTAs to a unit, which halves the token bytes an SM takes in, where K is long enough
@@ -679,7 +684,8 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     const size_t recv = static_cast<size_t>(p.cluster > 1 ? p.cluster : 0) * (p.m_tile / terms) * kTileN * sizeof(float);
     extra += recv;
     if (p.pair) extra += kStreamMaxStages * 8 + 64;   // a third set of barriers, more warps' sums
-    const uint32_t t_stage = p.pair ? p.a_block - static_cast<uint32_t>(p.m_tile) * 64u : p.a_block;   // a CTA's part of a token block
+    const uint32_t t_stage =
+        p.pair ? pair_code_bytes(p.m_tile) + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk : p.a_block;   // a CTA's part of a token block
     p.stages = static_cast<int>((kSmemLimit - extra) / (kWBlock + t_stage));
     if (p.stages > kStreamMaxStages) p.stages = kStreamMaxStages;
     // One share per CTA: one accumulator, and no more stages than it has steps, so that the next call's
@@ -753,7 +759,7 @@ cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx
                       make_fastdiv(static_cast<uint32_t>(plan.k_atoms) * 8u));
 }
 
-template <int kTermsPer, bool kFused>
+template <int kTermsPer, bool kFused, int kEpi>
 static cudaError_t allow_shared_memory() {
     static std::mutex mu;
     static std::atomic<bool> done[64];
@@ -763,7 +769,7 @@ static cudaError_t allow_shared_memory() {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
     std::lock_guard<std::mutex> lock(mu);
-    e = cudaFuncSetAttribute(mxfp4_stream_kernel<kTermsPer, kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(mxfp4_stream_kernel<kTermsPer, kFused, kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(kSmemLimit));
     if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
     return e;
@@ -799,8 +805,8 @@ int stream_clusters(int size) {
         cudaLaunchConfig_t cfg = stream_config(dim3(size), dim3(kStreamThreads), kSmemLimit, nullptr, size, attr);
         cfg.attrs = attr + 1;
         cfg.numAttrs = 1;
-        if (allow_shared_memory<kTerms, false>() != cudaSuccess ||
-            cudaOccupancyMaxActiveClusters(&n, mxfp4_stream_kernel<kTerms, false>, &cfg) != cudaSuccess) {
+        if (allow_shared_memory<kTerms, false, kEpiPlain>() != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, mxfp4_stream_kernel<kTerms, false, kEpiPlain>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             n = 0;
         }
@@ -809,20 +815,52 @@ int stream_clusters(int size) {
     return known[dev][size] - 1;
 }
 
-template <int kTermsPer, bool kFused>
-static cudaError_t launch_stream_as(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {
-    const cudaError_t e = allow_shared_memory<kTermsPer, kFused>();
+template <int kTermsPer, bool kFused, int kEpi>
+static cudaError_t launch_stream_as(const StreamPlan& plan, const EpilogueArgs<StreamArgs, kEpi>& args, cudaStream_t s) {
+    const cudaError_t e = allow_shared_memory<kTermsPer, kFused, kEpi>();
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = stream_config(dim3(plan.ctas), dim3(stream_threads(kTermsPer, kFused)),
                                                  plan.smem_bytes, s, plan.cluster, attr);
-    return cudaLaunchKernelEx(&cfg, mxfp4_stream_kernel<kTermsPer, kFused>, args);
+    return cudaLaunchKernelEx(&cfg, mxfp4_stream_kernel<kTermsPer, kFused, kEpi>, args);
 }
 
 cudaError_t launch_stream(const StreamPlan& plan, const StreamArgs& args, int terms, cudaStream_t s) {
     if (plan.pair) return launch_stream_pair(plan, args, s);
-    if (terms == 1) return plan.fused ? launch_stream_as<1, true>(plan, args, s) : launch_stream_as<1, false>(plan, args, s);
-    return plan.fused ? launch_stream_as<kTerms, true>(plan, args, s) : launch_stream_as<kTerms, false>(plan, args, s);
+    if (terms == 1)
+        return plan.fused ? launch_stream_as<1, true, kEpiPlain>(plan, args, s)
+                          : launch_stream_as<1, false, kEpiPlain>(plan, args, s);
+    return plan.fused ? launch_stream_as<kTerms, true, kEpiPlain>(plan, args, s)
+                      : launch_stream_as<kTerms, false, kEpiPlain>(plan, args, s);
+}
+
+cudaError_t launch_stream(const StreamPlan& plan, const WithEpilogue<StreamArgs>& args, int kind, cudaStream_t s) {
+    if (plan.pair) return launch_stream_pair(plan, args, kind, s);
+    if (kind == kEpiLinear) return launch_stream_as<1, false, kEpiLinear>(plan, args, s);
+    return plan.fused ? launch_stream_as<1, true, kEpiGated>(plan, args, s)
+                      : launch_stream_as<1, false, kEpiGated>(plan, args, s);
+}
+
+void fill_stream_args(const StreamPlan& plan, const DeviceInfo& di, uint8_t* ws, StreamArgs* out) {
+    StreamArgs& a = *out;
+    a.tblk = ws;
+    a.partial = reinterpret_cast<float*>(ws + plan.off_partial);
+    a.counters = reinterpret_cast<unsigned long long*>(ws + plan.off_counters);
+    a.tag = next_call_tag();
+    a.status = di.status;
+    a.m_tile = plan.m_tile;
+    a.by_m_tile = make_fastdiv(static_cast<uint32_t>(plan.m_tile));
+    a.by_k_atoms = make_fastdiv(static_cast<uint32_t>(plan.k_atoms));
+    a.by_walkers = make_fastdiv(static_cast<uint32_t>(plan.pair ? plan.ctas / 2 : plan.ctas));
+    a.nmc = plan.nmc;
+    a.n_tiles = plan.n_tiles;
+    a.k_atoms = plan.k_atoms;
+    a.stages = plan.stages;
+    a.cluster = plan.cluster;
+    a.accs = plan.accs;
+    a.a_block = plan.a_block;
+    a.tmem_cols = plan.tmem_cols;
+    a.wait_limit_ns = wait_limit_ns();
 }
 
 }  // namespace mxfp4

@@ -83,11 +83,12 @@ struct PairMaps {
 
 }  // namespace
 
+template <int kEpi>
 __global__ void __launch_bounds__(kPairThreads, 1)
-mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p, const __grid_constant__ PairMaps maps) {
+mxfp4_stream_pair_kernel(const __grid_constant__ EpilogueArgs<StreamArgs, kEpi> p, const __grid_constant__ PairMaps maps) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    const uint32_t t_rows = static_cast<uint32_t>(p.m_tile) * 64u;             // half a tile's code rows, at most
+    const uint32_t t_rows = pair_code_bytes(p.m_tile);                         // half a tile's code rows, at most
     const uint32_t t_stage = t_rows + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
     uint8_t* sW = smem;                                                        // [stages][kWBlock]
     uint8_t* sT = smem + static_cast<uint32_t>(p.stages) * kWBlock;            // [stages][t_stage]
@@ -122,6 +123,11 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p, const __grid_cons
         *abort_flag = 0u;
         last_flag[0] = last_flag[2] = 0u;
         prefix[0] = 0;
+        if (kEpi != kEpiPlain && !p.offsets) {   // one group
+            prefix[1] = tiles_of(p.rows, p.m_tile);
+            begins[0] = 0;
+            begins[1] = p.rows;
+        }
     }
     const int tiles = count_tiles<kPairThreads>(p, prefix, begins, warp_sum, warp, lane);
     const Walk start = begin_walk<true>(p, prefix, tiles * weight_tiles<true>(p));
@@ -316,7 +322,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ StreamArgs p, const __grid_cons
             const int b = nshare & 1;
             live = live && share_ready(p, &acc_full[b], (nshare >> 1) & 1, nshare, abort_flag);
             tc_fence_after_sync();
-            live = store_unit<1, true>(p, u, 2 * u.nt + static_cast<int>(rank), trow + static_cast<uint32_t>(b * p.m_tile), half,
+            live = store_unit<1, true, kEpi>(p, u, 2 * u.nt + static_cast<int>(rank), trow + static_cast<uint32_t>(b * p.m_tile), half,
                                        warp, lane, last_flag, epi_stage + (warp - 4) * kEpiStage, live);
             tc_fence_before_sync();
             __syncwarp();
@@ -360,7 +366,8 @@ static bool encode_rows(TensorMapEncoder encode, CUtensorMap* map, const uint8_t
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {
+template <int kEpi>
+static cudaError_t launch_pair_as(const StreamPlan& plan, const EpilogueArgs<StreamArgs, kEpi>& args, cudaStream_t s) {
     static std::mutex mu;
     static std::atomic<bool> done[64];
     int dev = 0;
@@ -369,7 +376,7 @@ cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, c
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!done[dev].load(std::memory_order_acquire)) {
         std::lock_guard<std::mutex> lock(mu);
-        e = cudaFuncSetAttribute(mxfp4_stream_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(mxfp4_stream_pair_kernel<kEpi>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(kSmemLimit));
         if (e != cudaSuccess) return e;
         done[dev].store(true, std::memory_order_release);
@@ -396,7 +403,14 @@ cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, c
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mxfp4_stream_pair_kernel, args, maps);
+    return cudaLaunchKernelEx(&cfg, mxfp4_stream_pair_kernel<kEpi>, args, maps);
+}
+
+cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {
+    return launch_pair_as<kEpiPlain>(plan, args, s);
+}
+cudaError_t launch_stream_pair(const StreamPlan& plan, const WithEpilogue<StreamArgs>& args, int kind, cudaStream_t s) {
+    return kind == kEpiGated ? launch_pair_as<kEpiGated>(plan, args, s) : launch_pair_as<kEpiLinear>(plan, args, s);
 }
 
 }  // namespace mxfp4

@@ -5,10 +5,6 @@
 
 namespace mxfp4 {
 
-// The C ABI's shared state (mxfp4_api.cu).
-int cuda_fail(cudaError_t e);             // records e for mxfp4_last_cuda_error, returns MXFP4_ERR_CUDA
-uint64_t wait_limit_ns();                 // limit of every bounded wait
-
 constexpr int kMaxGroups = 1024;          // groups (experts) one launch can address
 constexpr int kStreamThreads = 384;       // warps 0-3: copies, MMAs, two spare; warps 4-11: epilogue
 constexpr int kStreamEpiThreads = 256;
@@ -23,6 +19,10 @@ constexpr int kEpiStage = 1024;           // bytes of shared memory an epilogue 
 constexpr int kPairThreads = 640;         // the pair kernel: warps 12-19 write scale factors
 constexpr int kPairSfSlots = 5;           // steps whose scale factors are in tensor memory at once
 constexpr uint32_t kPairSfCols = 24;      // columns of one step: 8 weights, 16 tokens
+// Bytes of a stage that a CTA of a pair needs for its half of a tile's codes: boxes move 2 KB at a time.
+__host__ __device__ inline uint32_t pair_code_bytes(int m_tile) {
+    return (static_cast<uint32_t>(m_tile) * 64u + 2047u) / 2048u * 2048u;
+}
 constexpr int kTerms = 8;                 // e2m1 terms an activation is expanded into (weight-only)
 
 // A group of n rows is cut into tiles_of(n) token tiles of tile_rows(n) rows (a multiple of 16,
@@ -124,8 +124,9 @@ int stream_clusters(int size);
 
 // Plan for `rows` token-block rows in `groups` groups; terms: 1 (grouped) or kTerms; clusters_of:
 // stream_clusters, or a model of it.
+// m_tile: tokens per tile (a multiple of 16, up to 192) where the caller has chosen them, or 0.
 int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count,
-                     int (*clusters_of)(int), StreamPlan* plan);
+                     int (*clusters_of)(int), StreamPlan* plan, int m_tile = 0);
 
 // a [tokens, K] rows -> token blocks of the sorted rows: row r of the blocks is a[index ? index[r] : r].
 cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,
@@ -137,6 +138,11 @@ cudaError_t launch_expand_terms(const uint16_t* x, int M, int64_t K, int64_t ldx
 uint64_t next_call_tag();
 cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s);
 cudaError_t launch_stream(const StreamPlan& plan, const StreamArgs& args, int terms, cudaStream_t s);
+// The products with an epilogue (terms 1), kind: kEpiLinear (not fused) or kEpiGated.
+cudaError_t launch_stream_pair(const StreamPlan& plan, const WithEpilogue<StreamArgs>& args, int kind, cudaStream_t s);
+cudaError_t launch_stream(const StreamPlan& plan, const WithEpilogue<StreamArgs>& args, int kind, cudaStream_t s);
+// The plan's part of the arguments, and the launch: the workspace holds token blocks, counters and partial sums.
+void fill_stream_args(const StreamPlan& plan, const DeviceInfo& di, uint8_t* ws, StreamArgs* a);
 
 // Routing and combination (moe.cu).
 struct RouteArgs {

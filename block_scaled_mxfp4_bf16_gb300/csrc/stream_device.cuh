@@ -1,6 +1,7 @@
 // Device code that the streaming products share: the groups' tiling, the walk over a CTA's (or a CTA
 // pair's) units, tcgen05 operations of one elected lane, and the epilogue's pieces.
 #pragma once
+#include "epilogue.cuh"
 #include "mma_desc.cuh"
 #include "quant_device.cuh"
 #include "stream.h"
@@ -319,11 +320,27 @@ __device__ __forceinline__ void tmem_load_frag32(uint32_t taddr, uint32_t (&v)[1
         : "r"(taddr)
         : "memory");
 }
+// The same of 16 columns.
+__device__ __forceinline__ void tmem_load_frag16(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+        : "r"(taddr)
+        : "memory");
+}
 // Four 8x8 matrices of 16-bit values, stored transposed: lane 8m + r gives the address of row r
 // (a column of the fragments) of matrix m, eight values.
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
                  ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+// And read the same way.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&v)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
                  : "memory");
 }
 
@@ -433,6 +450,154 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
     }
 }
 
+// Eight consecutive elements of a row of C or of the residual, of which those from column `from` up to `to`
+// exist: whole in one piece (16-byte aligned), else one by one.
+__device__ __forceinline__ uint4 load_piece(const uint16_t* at, int from, int to) {
+    if (from + 8 <= to) return __ldcg(reinterpret_cast<const uint4*>(at));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        if (from + k < to) w[k >> 1] |= static_cast<uint32_t>(__ldcg(at + k)) << (16 * (k & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_piece(uint16_t* at, const uint4& v, int from, int to) {
+    if (from + 8 <= to) {
+        *reinterpret_cast<uint4*>(at) = v;
+        return;
+    }
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 7; ++k)
+        if (from + k < to) at[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
+}
+
+// store_tile with an epilogue, 16 tokens at a time. n0: the warp's first weight row; bias0: the group's first bias
+// element (gated). Where rows are aligned to 16 bytes (the residual's too):
+//   linear: as store_tile; the residual takes the same way back, whole pieces to shared memory and from there as
+//           fragments, so that it is added before the one rounding.
+//   gated : a thread's fragments hold the gate's and the up projection's row of two features (lanes 0-15 and 16-31
+//           of the warp's) and two tokens; a token's 16 features are two pieces of shared memory, 32 bytes, the pieces of
+//           tokens 4-7 and 12-15 swapped, so that the eight rows a matrix is stored to touch all banks.
+template <int kEpi, bool kWide>
+__device__ __forceinline__ void store_tile_epi(const WithEpilogue<StreamArgs>& p, uint32_t trow, int tokens, int64_t row0, int n0,
+                                               int64_t bias0, int half, int lane, uint8_t* stage) {
+    if constexpr (!kWide) {
+        for (int cb = half * 16; cb < tokens; cb += 32) {
+            const int cnt = min(16, tokens - cb);
+            uint32_t r[16];
+            if constexpr (kEpi == kEpiLinear) {
+                uint16_t res[16];
+                residual_run(p.epi, p.N, n0 + lane, row0 + cb, cnt, res);
+                tmem_load_16(trow + static_cast<uint32_t>(cb), r);
+                tmem_load_wait();
+                store_run(p.epi, p.N, n0 + lane, row0 + cb, cnt, reinterpret_cast<float(&)[16]>(r), res, p.c, p.ldc);
+            } else {
+                tmem_load_16(trow + static_cast<uint32_t>(cb), r);
+                tmem_load_wait();
+                store_run_gated(p.epi, bias0, n0 + lane, row0 + cb, cnt, reinterpret_cast<float(&)[16]>(r), p.c, p.ldc);
+            }
+            __syncwarp();
+        }
+        return;
+    }
+    const int middle = (((tokens + 15) >> 4) + 1) / 2 * 16;    // the two warps of 32 weight rows
+    const int first = half ? middle : 0, rows = half ? tokens : min(middle, tokens);   // take [first, rows)
+    const int q = lane >> 2;
+    if constexpr (kEpi == kEpiLinear) {
+        const uint32_t put = smem_addr(stage) + static_cast<uint32_t>((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
+        uint8_t* get = stage + q * 64 + ((((lane & 3) ^ (q >> 1)) & 3) << 4);
+        const int n = n0 + (lane & 3) * 8;         // this lane's piece of row q, and 512 bytes on that of row q + 8
+        float b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = n0 + q + 8 * i < p.N ? bias_at(p.epi, n0 + q + 8 * i) : 0.f;
+        const bool res = p.epi.residual != nullptr;
+        const uint16_t* rp = p.epi.residual + (row0 + first + q) * p.epi.ldr + n;
+        uint16_t* cp = p.c + (row0 + first + q) * p.ldc + n;
+        for (int cb = first; cb < rows; cb += 16) {
+            const bool one = cb + q < rows, two = cb + q + 8 < rows;
+            uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
+            if (res && one) r0 = load_piece(rp, n, p.N);
+            if (res && two) r1 = load_piece(rp + 8 * p.epi.ldr, n, p.N);
+            uint32_t lo[8], hi[8];
+            tmem_load_frag16(trow + static_cast<uint32_t>(cb), lo);
+            tmem_load_frag16(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
+            if (res) {
+                *reinterpret_cast<uint4*>(get) = r0;
+                *reinterpret_cast<uint4*>(get + 512) = r1;
+                __syncwarp();
+            }
+            tmem_load_wait();
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)           // eight of the first 8 tokens, eight of the next
+                v[i] = __uint_as_float((i & 4) ? hi[(i >> 3) * 4 + (i & 3)] : lo[(i >> 3) * 4 + (i & 3)]) + b[(i >> 1) & 3];
+            activate(p.epi.act, v);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float* w = v + 8 * h;
+                if (res) {
+                    uint32_t r[4];
+                    ldmatrix_x4_trans(put + static_cast<uint32_t>(h) * 512u, r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        w[2 * i] += bf16_lo(r[i]);
+                        w[2 * i + 1] += bf16_hi(r[i]);
+                    }
+                    __syncwarp();
+                }
+                stmatrix_x4_trans(put + static_cast<uint32_t>(h) * 512u, pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
+                                  pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
+            }
+            __syncwarp();
+            const uint4 v0 = *reinterpret_cast<const uint4*>(get), v1 = *reinterpret_cast<const uint4*>(get + 512);
+            if (one) store_piece(cp, v0, n, p.N);
+            if (two) store_piece(cp + 8 * p.ldc, v1, n, p.N);
+            rp += 16 * p.epi.ldr;
+            cp += 16 * p.ldc;
+            __syncwarp();
+        }
+    } else {
+        const int f0 = n0 >> 1;                    // the warp's 16 features
+        const int I = p.epi.features;
+        // matrix lane / 8: tokens 0-7 or 8-15, features 0-7 or 8-15; row lane % 8: a token of them
+        const int tok = (lane >> 4) * 8 + (lane & 7);
+        const uint32_t put = smem_addr(stage) + static_cast<uint32_t>(tok * 32 + ((((lane >> 3) ^ (tok >> 2)) & 1) << 4));
+        const int t = lane >> 1, f = f0 + (lane & 1) * 8;      // this lane's piece: token t, features f .. f + 7
+        const uint8_t* get = stage + t * 32 + (((lane ^ (t >> 2)) & 1) << 4);
+        float bg[2], bu[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int at = f0 + q + 8 * i;
+            bg[i] = at < I ? bias_at(p.epi, bias0 + at) : 0.f;
+            bu[i] = at < I ? bias_at(p.epi, bias0 + I + at) : 0.f;
+        }
+        uint16_t* cp = p.c + (row0 + first + t) * p.ldc + f;
+        for (int cb = first; cb < rows; cb += 16) {
+            uint32_t lo[8], hi[8];
+            tmem_load_frag16(trow + static_cast<uint32_t>(cb), lo);
+            tmem_load_frag16(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
+            tmem_load_wait();
+            float g[8], u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {          // tokens 8 (i / 4), features 8 (i / 2 % 2)
+                const uint32_t* from = (i & 2) ? hi : lo;
+                g[i] = __uint_as_float(from[(i >> 2) * 4 + (i & 1)]) + bg[(i >> 1) & 1];
+                u[i] = __uint_as_float(from[(i >> 2) * 4 + 2 + (i & 1)]) + bu[(i >> 1) & 1];
+            }
+            activate(p.epi.act, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] *= u[i];
+            stmatrix_x4_trans(put, pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
+                              pack_bf16x2(g[6], g[7]));
+            __syncwarp();
+            const uint4 v = *reinterpret_cast<const uint4*>(get);
+            if (cb + t < rows) store_piece(cp, v, f, I);
+            cp += 16 * p.ldc;
+            __syncwarp();
+        }
+    }
+}
+
 // One more arrival at a split unit's counter: the call's word as it was before. `seen`: the word as read a
 // moment ago.
 __device__ __forceinline__ unsigned long long arrive(unsigned long long* counter, unsigned long long seen, uint64_t tag,
@@ -494,8 +659,8 @@ __device__ __forceinline__ void arrive_unstored(const StreamArgs& p, const volat
 // live: this warp has not given up. The warps decide that apart, but meet at barriers in a split unit: so a
 // warp that has given up still walks on and calls, and the first of those barriers makes the decision a
 // joint one (arrive_unstored makes up for the arrivals). Returns whether the warp is still live.
-template <int kTermsPer, bool kPair>
-__device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, int nt, uint32_t acc, int half, int warp,
+template <int kTermsPer, bool kPair, int kEpi>
+__device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>& p, const Walk& u, int nt, uint32_t acc, int half, int warp,
                                            int lane, volatile uint32_t* last_flag, uint8_t* stage, bool live) {
     constexpr int kTok = 16 / kTermsPer;         // tokens per 16 columns
     constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
@@ -505,7 +670,11 @@ __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, i
     if (!split && !live) return false;
     if (kTermsPer == 1 && u.nk == p.k_atoms) {
         const int n0 = nt * kTileN + (warp & 3) * 32;
-        if (p.c_wide) store_tile<true>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+        if constexpr (kEpi != kEpiPlain) {
+            const int64_t bias0 = static_cast<int64_t>(u.group) * 2 * p.epi.features;
+            if (p.c_wide) store_tile_epi<kEpi, true>(p, acc, u.rows, u.row0, n0, bias0, half, lane, stage);
+            else store_tile_epi<kEpi, false>(p, acc, u.rows, u.row0, n0, bias0, half, lane, stage);
+        } else if (p.c_wide) store_tile<true>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         else store_tile<false>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         return true;
     }
@@ -596,7 +765,14 @@ __device__ __forceinline__ bool store_unit(const StreamArgs& p, const Walk& u, i
                 }
             }
         }
-        if (n < p.N) {
+        if constexpr (kEpi == kEpiLinear) {
+            uint16_t res[kTok];
+            residual_run(p.epi, p.N, n, row0 + m0, min(kTok, tokens - m0), res);
+            store_run(p.epi, p.N, n, row0 + m0, min(kTok, tokens - m0), v, res, p.c, p.ldc);
+        } else if constexpr (kEpi == kEpiGated) {
+            store_run_gated(p.epi, static_cast<int64_t>(u.group) * 2 * p.epi.features, n, row0 + m0,
+                            min(kTok, tokens - m0), v, p.c, p.ldc);
+        } else if (n < p.N) {
             uint16_t* cp = p.c + (row0 + m0) * p.ldc + n;
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {

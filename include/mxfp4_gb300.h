@@ -67,7 +67,8 @@ int mxfp4_last_cuda_error(void);
  * calls (mxfp4_call_create, mxfp4_call_create_host, mxfp4_call_run, mxfp4_call_destroy), the
  * scale_stores field of mxfp4_plan_info, mxfp4_gemm_unpacked. 2.04: mxfp4_gemm_options.flags
  * (MXFP4_GEMM_A_READY) and mxfp4_plan_info.a_early. 2.05: mxfp4_gemv, mxfp4_grouped_gemm,
- * mxfp4_moe_route, mxfp4_moe_combine. */
+ * mxfp4_moe_route, mxfp4_moe_combine. 2.06: mxfp4_linear, mxfp4_prepack_gated, mxfp4_gated_linear,
+ * mxfp4_grouped_gated_linear. */
 int mxfp4_version(void);
 
 /*
@@ -541,6 +542,82 @@ int mxfp4_moe_route(const void *logits, int dtype, int64_t T, int64_t E, int64_t
  */
 int mxfp4_moe_combine(const void *y, int64_t R, int64_t N, int64_t ldy, const int32_t *slots, const float *weights,
                       int64_t T, int k, void *out, int64_t ldo, void *stream);
+
+/*
+ * mxfp4_linear -- mxfp4_gemm with what follows a product in a layer, in its epilogue:
+ *   out[m, n] = act(z[m, n] + bias[n]) + residual[m, n],   z = MXFP4(X) . MXFP4(B)^T,
+ * everything after the products in fp32, rounded once to bf16.
+ *   x, M, K, ldx, packed_b, N: as mxfp4_gemm's a, M, K, lda, packed_b, N (X quantized inside the call).
+ *   bias      : device fp32 (bias_dtype MXFP4_F32) or bf16 (MXFP4_BF16) [N], aligned to its type, or
+ *               NULL (bias_dtype is then not used).
+ *   activation: MXFP4_ACT_NONE; MXFP4_ACT_RELU max(z, 0); MXFP4_ACT_SILU z / (1 + e^-z);
+ *               MXFP4_ACT_GELU z Phi(z), Phi the normal distribution function; MXFP4_ACT_GELU_TANH
+ *               z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2.
+ *   residual  : bf16 [M, N], row stride ldr (ldr >= N), 2-byte aligned, or NULL (ldr is then not used).
+ *   out       : bf16 [M, N], row stride ldo (ldo >= N), 2-byte aligned. It may be the residual itself (the
+ *               same pointer and stride: every element is read by the thread that writes it); otherwise
+ *               it must not overlap any input.
+ *   workspace : ws_bytes >= mxfp4_linear_workspace_size(M, N, K), 256-byte aligned; may be NULL when
+ *               that size is 0. Its previous contents do not matter. Calls sharing it must be ordered.
+ * M == 0 or N == 0 is a no-op. Ordering as mxfp4_gemm: x, bias and residual are read and out is written
+ * after the work before the call on `stream`, packed_b is requested before. Infinities and NaN in the
+ * bias or the residual go through the formula. Runs on the same inputs give the same bits; z is within
+ * the rounding of its fp32 sums of mxfp4_gemm's, whose plan the call need not take.
+ */
+#define MXFP4_ACT_NONE 0
+#define MXFP4_ACT_RELU 1
+#define MXFP4_ACT_SILU 2
+#define MXFP4_ACT_GELU 3
+#define MXFP4_ACT_GELU_TANH 4
+size_t mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K);
+int mxfp4_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const void *packed_b, int64_t N,
+                 const void *bias, int bias_dtype, int activation, const void *residual, int64_t ldr,
+                 void *out, int64_t ldo, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * mxfp4_prepack_gated -- one-time relayout of the two projections in front of a gated block's product,
+ * for mxfp4_gated_linear.
+ *   bq, bs : as for mxfp4_prepack_b, of 2I rows: the gate projection's I rows, then the up projection's.
+ *   packed : out, mxfp4_prepack_gated_size(I, K) bytes, 1024-byte aligned: mxfp4_prepack_b's layout of
+ *            16 ceil(I / 8) rows, eight of the gate's, then the same eight features' of the up projection,
+ *            and so on; rows past I are zero padding. Must not overlap bq or bs.
+ * Errors as mxfp4_prepack_b. mxfp4_prepack_gated_size returns 0 for invalid sizes (I > 2^30 among them).
+ */
+size_t mxfp4_prepack_gated_size(int64_t I, int64_t K);
+int mxfp4_prepack_gated(const void *bq, const void *bs, int64_t I, int64_t K, void *packed, void *stream);
+
+/*
+ * mxfp4_gated_linear -- the first half of a gated feed-forward block: both projections, the activation
+ * and the product in one kernel,
+ *   out[m, i] = act(zg[m, i] + bias[i]) * (zu[m, i] + bias[I + i]),   zg, zu = MXFP4(X) . MXFP4(Wg, Wu)^T,
+ * in fp32 and rounded once to bf16. (The second half is mxfp4_linear with a residual.)
+ *   packed_gu : written by mxfp4_prepack_gated for the same I and K, 1024-byte aligned.
+ *   bias      : [2I], the gate's and then the up projection's, or NULL; types and alignment, the
+ *               activations, x, out, the workspace (mxfp4_gated_linear_workspace_size(M, I, K)), the
+ *               ordering and the errors as for mxfp4_linear. out must not overlap any input.
+ */
+size_t mxfp4_gated_linear_workspace_size(int64_t M, int64_t I, int64_t K);
+int mxfp4_gated_linear(const void *x, int64_t M, int64_t K, int64_t ldx, const void *packed_gu, int64_t I,
+                       const void *bias, int bias_dtype, int activation, void *out, int64_t ldo,
+                       void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * mxfp4_grouped_gated_linear -- mxfp4_gated_linear for rows sorted by group (a mixture of experts' first
+ * products; the second is mxfp4_grouped_gemm on its output):
+ *   out[r, i] = act(zg[r, i] + bias[g, i]) * (zu[r, i] + bias[g, I + i]) for the rows r of group g.
+ *   a, tokens, K, lda, rows, offsets, groups, R: as for mxfp4_grouped_gemm (without its flags).
+ *   packed_gu : the groups' packed weights one after the other, each written by mxfp4_prepack_gated.
+ *   bias      : [groups, 2I] or NULL, activation: as for mxfp4_gated_linear.
+ *   out       : bf16 [R, I], row stride ldo (ldo >= I), 2-byte aligned. Rows before offsets[0] and from
+ *               offsets[groups] on are not written; offsets that break their rule leave out unwritten.
+ *   workspace : mxfp4_grouped_gated_linear_workspace_size(R, groups, I, K).
+ * Limits, ordering and errors as mxfp4_grouped_gemm. R == 0, I == 0 or groups == 0 is a no-op.
+ */
+size_t mxfp4_grouped_gated_linear_workspace_size(int64_t R, int64_t groups, int64_t I, int64_t K);
+int mxfp4_grouped_gated_linear(const void *a, int64_t tokens, int64_t K, int64_t lda, const int32_t *rows,
+                               const int32_t *offsets, int64_t groups, const void *packed_gu, int64_t I,
+                               const void *bias, int bias_dtype, int activation, void *out, int64_t R,
+                               int64_t ldo, void *workspace, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
