@@ -18,15 +18,16 @@
 
 namespace mxfp4 {
 
-// 2^x and 1 / x by the hardware's approximations, both within 2^-22 of the value.
+// 2^x and 1 / x by the hardware's approximations, both within 2^-22 of the value; results below 2^-126 are zeros (without
+// .ftz each takes instructions more: gelu_tanh 4.1 us a tile of 128 x 192, not 3).
 __device__ __forceinline__ float fast_exp2(float x) {
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float fast_rcp(float x) {
     float y;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -91,32 +92,42 @@ __device__ __forceinline__ uint16_t to_bf16(float v) { return __bfloat16_as_usho
 __device__ __forceinline__ int gated_feature(int n) { return (n >> 4) * 8 + (n & 7); }
 __device__ __forceinline__ bool gated_up(int n) { return (n & 8) != 0; }
 
+// What an epilogue adds is loaded before the sums are waited for: loaded after them, one row's residual after another
+// (the stores between may be to the same memory, so the compiler keeps the order), 256x4096x7168 took 21.3 us, not 11.8.
+
 // ---- a lane's run of tokens: v[i] is the sum of weight row n (lane nl of its warp's 32) and token row0 + i,
 // for i < cnt. All lanes of the warp call, with rows past the last among them; cnt is the warp's.
 
-// Linear: the residual's values of the run (residual_run, to be asked for before the sums are waited for),
-// then the rest (store_run).
+// Linear: the bias and the residual of a run.
 template <int kN>
-__device__ __forceinline__ void residual_run(const Epilogue& e, int N, int n, int64_t row0, int cnt, uint16_t (&r)[kN]) {
-    if (!e.residual || n >= N) return;
-    const uint16_t* at = e.residual + row0 * e.ldr + n;
+struct TokenRun {
+    float bias;
+    uint16_t residual[kN];
+};
+template <int kN>
+__device__ __forceinline__ void load_run(const Epilogue& e, int N, int n, int64_t row0, int cnt, TokenRun<kN>& r) {
+    r.bias = 0.f;
+    if (n >= N) return;
+    if (e.residual) {
+        const uint16_t* at = e.residual + row0 * e.ldr + n;
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        r[i] = i < cnt ? __ldcg(at) : static_cast<uint16_t>(0);
-        at += e.ldr;
+        for (int i = 0; i < kN; ++i) {
+            r.residual[i] = i < cnt ? __ldcg(at) : static_cast<uint16_t>(0);
+            at += e.ldr;
+        }
     }
+    r.bias = bias_at(e, n);
 }
 template <int kN>
 __device__ __forceinline__ void store_run(const Epilogue& e, int N, int n, int64_t row0, int cnt, float (&v)[kN],
-                                          const uint16_t (&r)[kN], uint16_t* c, int64_t ldc) {
+                                          const TokenRun<kN>& r, uint16_t* c, int64_t ldc) {
     if (n >= N) return;
-    const float b = bias_at(e, n);
 #pragma unroll
-    for (int i = 0; i < kN; ++i) v[i] += b;
+    for (int i = 0; i < kN; ++i) v[i] += r.bias;
     activate(e.act, v);
     if (e.residual) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) v[i] += __uint_as_float(static_cast<uint32_t>(r[i]) << 16);
+        for (int i = 0; i < kN; ++i) v[i] += __uint_as_float(static_cast<uint32_t>(r.residual[i]) << 16);
     }
     uint16_t* to = c + row0 * ldc + n;
 #pragma unroll
@@ -125,21 +136,32 @@ __device__ __forceinline__ void store_run(const Epilogue& e, int N, int n, int64
         to += ldc;
     }
 }
-// Gated: the lanes of a feature's two rows exchange every other token's sum, so that the gate's lane has both of
-// the even tokens and the up projection's of the odd ones. bias0: the group's first bias element.
+// Gated: the biases of the feature of row n (0 where it has none), from bias0, the group's first, on.
+struct GatedBias {
+    float gate, up;
+};
+__device__ __forceinline__ GatedBias load_gated_bias(const Epilogue& e, int64_t bias0, int f) {
+    GatedBias b = {0.f, 0.f};
+    if (f < e.features) {
+        b.gate = bias_at(e, bias0 + f);
+        b.up = bias_at(e, bias0 + e.features + f);
+    }
+    return b;
+}
+// The lanes of a feature's two rows exchange every other token's sum, so that the gate's lane has both of the even
+// tokens and the up projection's of the odd ones.
 template <int kN>
-__device__ __forceinline__ void store_run_gated(const Epilogue& e, int64_t bias0, int n, int64_t row0, int cnt,
+__device__ __forceinline__ void store_run_gated(const Epilogue& e, const GatedBias& b, int n, int64_t row0, int cnt,
                                                 const float (&v)[kN], uint16_t* c, int64_t ldc) {
     const bool up = gated_up(n);
     const int f = gated_feature(n);
     const bool real = f < e.features;
-    const float bg = real ? bias_at(e, bias0 + f) : 0.f, bu = real ? bias_at(e, bias0 + e.features + f) : 0.f;
     float g[kN / 2], u[kN / 2];
 #pragma unroll
     for (int i = 0; i < kN / 2; ++i) {
         const float got = __shfl_xor_sync(0xffffffffu, up ? v[2 * i] : v[2 * i + 1], 8);
-        g[i] = (up ? got : v[2 * i]) + bg;
-        u[i] = (up ? v[2 * i + 1] : got) + bu;
+        g[i] = (up ? got : v[2 * i]) + b.gate;
+        u[i] = (up ? v[2 * i + 1] : got) + b.up;
     }
     activate(e.act, g);
     uint16_t* to = c + (row0 + (up ? 1 : 0)) * ldc + f;
@@ -150,35 +172,36 @@ __device__ __forceinline__ void store_run_gated(const Epilogue& e, int64_t bias0
     }
 }
 
-// ---- four neighbouring weight rows n4 .. n4 + 3 (n4 a multiple of 4) of one token row
-__device__ __forceinline__ void store_quad(const Epilogue& e, int N, int n4, int64_t row, const float4& z, uint16_t* c,
-                                           int64_t ldc, bool v4) {
-    float v[4] = {z.x, z.y, z.z, z.w};
-    float r[4] = {0.f, 0.f, 0.f, 0.f};
-    v4 = v4 && n4 + 3 < N;
-    if (e.residual) {
-        const uint16_t* at = e.residual + row * e.ldr + n4;
-        if (v4) {          // the residual's rows are aligned as C's are
-            const uint2 w = __ldcg(reinterpret_cast<const uint2*>(at));
-            r[0] = bf16_lo(w.x);
-            r[1] = bf16_hi(w.x);
-            r[2] = bf16_lo(w.y);
-            r[3] = bf16_hi(w.y);
-        } else {
+// ---- four neighbouring weight rows n4 .. n4 + 3 (n4 a multiple of 4) of a token row
+// Linear: their biases, and the residual's four elements of one row. v4: C's and the residual's rows are aligned to
+// 8 bytes.
+__device__ __forceinline__ float4 quad_bias(const Epilogue& e, int N, int n4) {
+    float b[4];
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-                if (n4 + t < N) r[t] = __uint_as_float(static_cast<uint32_t>(__ldcg(at + t)) << 16);
-        }
-    }
+    for (int t = 0; t < 4; ++t) b[t] = n4 + t < N ? bias_at(e, n4 + t) : 0.f;
+    return make_float4(b[0], b[1], b[2], b[3]);
+}
+__device__ __forceinline__ uint2 quad_residual(const Epilogue& e, int N, int n4, int64_t row, bool v4) {
+    const uint16_t* at = e.residual + row * e.ldr + n4;
+    if (v4 && n4 + 3 < N) return __ldcg(reinterpret_cast<const uint2*>(at));
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int t = 0; t < 4; ++t) v[t] += n4 + t < N ? bias_at(e, n4 + t) : 0.f;
+    for (int t = 0; t < 4; ++t)
+        if (n4 + t < N) w[t] = __ldcg(at + t);
+    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+}
+__device__ __forceinline__ void store_quad(const Epilogue& e, int N, int n4, int64_t row, const float4& z, const float4& b,
+                                           const uint2& r, uint16_t* c, int64_t ldc, bool v4) {
+    float v[4] = {z.x + b.x, z.y + b.y, z.z + b.z, z.w + b.w};
     activate(e.act, v);
     if (e.residual) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] += r[t];
+        v[0] += bf16_lo(r.x);
+        v[1] += bf16_hi(r.x);
+        v[2] += bf16_lo(r.y);
+        v[3] += bf16_hi(r.y);
     }
     uint16_t* to = c + row * ldc + n4;
-    if (v4) {
+    if (v4 && n4 + 3 < N) {
         *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
     } else {
 #pragma unroll
@@ -188,28 +211,91 @@ __device__ __forceinline__ void store_quad(const Epilogue& e, int N, int n4, int
 }
 // Gated: lanes hold consecutive fours of a row, so the other row of their features is two lanes away; the gate's
 // lane takes the first two features, the up projection's the last two. All lanes of the warp call.
-__device__ __forceinline__ void store_quad_gated(const Epilogue& e, int n4, int64_t row, const float4& z, uint16_t* c,
-                                                 int64_t ldc, bool v2) {
+__device__ __forceinline__ int quad_feature(int n4) { return gated_feature(n4) + (gated_up(n4) ? 2 : 0); }
+__device__ __forceinline__ void store_quad_gated(const Epilogue& e, const GatedBias (&b)[2], int n4, int64_t row,
+                                                 const float4& z, uint16_t* c, int64_t ldc, bool v2) {
     const bool up = gated_up(n4);
-    const float a = __shfl_xor_sync(0xffffffffu, up ? z.x : z.z, 2), b = __shfl_xor_sync(0xffffffffu, up ? z.y : z.w, 2);
-    const int f = gated_feature(n4) + (up ? 2 : 0);
-    float g[2] = {up ? a : z.x, up ? b : z.y}, u[2] = {up ? z.z : a, up ? z.w : b};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        if (f + t < e.features) {
-            g[t] += bias_at(e, f + t);
-            u[t] += bias_at(e, e.features + f + t);
-        }
-    }
+    const float s = __shfl_xor_sync(0xffffffffu, up ? z.x : z.z, 2), t = __shfl_xor_sync(0xffffffffu, up ? z.y : z.w, 2);
+    const int f = quad_feature(n4);
+    float g[2] = {(up ? s : z.x) + b[0].gate, (up ? t : z.y) + b[1].gate};
+    const float u[2] = {(up ? z.z : s) + b[0].up, (up ? z.w : t) + b[1].up};
     activate(e.act, g);
     uint16_t* to = c + row * ldc + f;
     if (v2 && f + 1 < e.features) {
         *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(g[0] * u[0], g[1] * u[1]);
     } else {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-            if (f + t < e.features) to[t] = to_bf16(g[t] * u[t]);
+        for (int k = 0; k < 2; ++k)
+            if (f + k < e.features) to[k] = to_bf16(g[k] * u[k]);
     }
 }
+
+// kN (8 or 16) accumulator columns of this thread's lane, summed over the `nacc` accumulators, acc2 columns apart.
+__device__ __forceinline__ void tmem_load_columns(uint32_t taddr, uint32_t (&r)[16]) { tmem_load_16(taddr, r); }
+__device__ __forceinline__ void tmem_load_columns(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+// Until the wait the loaded registers are not to be read, moved or given to other values, so it names them, and no
+// loop's edge lies between.
+__device__ __forceinline__ void tmem_columns_wait(uint32_t (&r)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])
+                 :
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_columns_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+template <int kN>
+__device__ __forceinline__ void load_sums(uint32_t taddr, int nacc, uint32_t acc2, float (&v)[kN]) {
+    uint32_t r[kN];
+    __syncwarp();                                  // reads of tensor memory take the whole warp, and whole
+    tmem_load_columns(taddr, r);
+    tmem_columns_wait(r);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) v[i] = __uint_as_float(r[i]);
+    for (int a = 1; a < nacc; ++a) {
+        tmem_load_columns(taddr + static_cast<uint32_t>(a) * acc2, r);
+        tmem_columns_wait(r);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) v[i] += __uint_as_float(r[i]);
+    }
+}
+
+// Whole sums of a lane's weight row n from tensor memory to C, kN tokens at a time: of `tokens` (the first is row0 of
+// C) those from `first` on, every step-th kN of them. load_first asks for what the first run adds. The whole warp calls
+// both. 16 tokens, not 32: with 137 and 168 registers a thread instead of 80, no second CTA of the weight-resident
+// kernel, and no block of the quantizer beside the streaming one, fits the SM (8x2112x7168 4.20 us, not 3.6).
+template <int kEpi, int kN = 16>
+struct LaneStore {
+    std::conditional_t<kEpi == kEpiLinear, TokenRun<kN>, GatedBias> add;
+
+    __device__ __forceinline__ void load_first(const Epilogue& e, int64_t bias0, int N, int n, int64_t row0, int tokens,
+                                               int first) {
+        if constexpr (kEpi == kEpiLinear) load_run(e, N, n, row0 + first, tokens - first, add);
+        else add = load_gated_bias(e, bias0, gated_feature(n));
+    }
+    __device__ __forceinline__ void store(const Epilogue& e, int N, int n, int64_t row0, int tokens, int first, int step,
+                                          uint32_t taddr, int nacc, uint32_t acc2, uint16_t* c, int64_t ldc) {
+        for (int cb = first; cb < tokens; cb += step) {
+            float v[kN];
+            load_sums(taddr + static_cast<uint32_t>(cb), nacc, acc2, v);
+            if constexpr (kEpi == kEpiLinear) {
+                store_run(e, N, n, row0 + cb, tokens - cb, v, add, c, ldc);
+                if (cb + step < tokens) load_run(e, N, n, row0 + cb + step, tokens - cb - step, add);
+            } else {
+                store_run_gated(e, add, n, row0 + cb, tokens - cb, v, c, ldc);
+            }
+            __syncwarp();
+        }
+    }
+};
 
 }  // namespace mxfp4

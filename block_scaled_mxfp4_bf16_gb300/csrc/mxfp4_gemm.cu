@@ -184,7 +184,7 @@ __device__ __forceinline__ void quantize_slice(const QuantSlice& q, int qt, cons
 // the other instantiation takes the path and the issue scheme from its arguments.
 // kEpi: what the sums go through before they are stored (epilogue.cuh).
 template <bool kTwoKernel, bool kWide, bool kSfStores, int kEpi>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kGemmThreads, kEpi == kEpiPlain ? 1 : 2)
 mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
     static_assert(kTwoKernel || (!kWide && !kSfStores), "the fused path copies its own scale factors");
     const bool fused = kTwoKernel ? false : p.fused != 0;
@@ -297,6 +297,7 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
     pdl_launch_dependents();
     uint32_t tmem_base = 0;
     bool ok = true;
+    [[maybe_unused]] LaneStore<kEpi> lane_store;   // with an epilogue, one K slice
 
     const uint8_t* bsrc = p.bblk + (static_cast<size_t>(nt) * p.k_atoms + a0) * kWBlock;
     const uint8_t* asrc = p.ablk + (static_cast<size_t>(mt) * p.k_atoms + a0) * a_block;
@@ -559,6 +560,14 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
                 if (++s == stages) { s = 0; phase ^= 1u; }
             }
         }
+        if constexpr (kEpi != kEpiPlain) {
+            // what the epilogue adds may be the previous grid's; one K slice: asked for while the MMAs run
+            pdl_wait_prior_grid();
+            if (S == 1) {
+                const int row_n = n0 + (warp & 3) * 32 + lane;
+                lane_store.load_first(p.epi, 0, p.N, row_n, m0, m_valid, ((warp - 3) >> 2 & 1) * 16);
+            }
+        }
         const bool waited = mbar_wait(acc_full, 0, lim);
         tc_fence_after_sync();
         if (et == 0) MXFP4_PHASE(6);
@@ -580,23 +589,8 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
     if (S == 1) {
         // one K slice: tensor memory -> bf16 C directly, one output column per thread
         if constexpr (kEpi != kEpiPlain) {
-            if (warp >= 3 && ok) {
-                pdl_wait_prior_grid();             // the residual and the bias may be the previous grid's
-                for (int cb = half * 32; cb < m_valid; cb += 64) {
-                    const int cnt = min(32, m_valid - cb);
-                    uint32_t r[32];
-                    if constexpr (kEpi == kEpiLinear) {
-                        uint16_t res[32];
-                        residual_run(p.epi, p.N, n, m0 + cb, cnt, res);
-                        load_acc32(trow + cb, cb + 16 < m_valid, nacc, acc2, r);
-                        store_run(p.epi, p.N, n, m0 + cb, cnt, reinterpret_cast<float(&)[32]>(r), res, p.c, p.ldc);
-                    } else {
-                        load_acc32(trow + cb, cb + 16 < m_valid, nacc, acc2, r);
-                        store_run_gated(p.epi, 0, n, m0 + cb, cnt, reinterpret_cast<float(&)[32]>(r), p.c, p.ldc);
-                    }
-                    __syncwarp();
-                }
-            }
+            if (warp >= 3 && ok)
+                lane_store.store(p.epi, p.N, n, m0, m_valid, half * 16, 32, trow, nacc, acc2, p.c, p.ldc);
         } else if (warp >= 3 && ok) {
             for (int cb = half * 32; cb < m_valid; cb += 64) {
                 uint32_t r[32];
@@ -676,6 +670,25 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
         // word reports it). The bytes it still lacks belong to a peer that failed before posting:
         // a peer that posted has its copy land well within the limit.
         const bool owner = warp >= 3 && r1 > r0;
+        constexpr int kRows = 4;
+        [[maybe_unused]] float4 b4;                // what the epilogue adds, of the first rows
+        [[maybe_unused]] uint2 res[kRows];
+        [[maybe_unused]] GatedBias b2[2];
+        if constexpr (kEpi != kEpiPlain) {
+            const int n4 = n0 + lane * 4, lm = warp - 3;
+            if constexpr (kEpi == kEpiLinear) {
+                if (owner) {
+                    b4 = quad_bias(p.epi, p.N, n4);
+#pragma unroll
+                    for (int u = 0; u < kRows; ++u)
+                        if (p.epi.residual && lm + u * kEpiWarps < r1 - r0)
+                            res[u] = quad_residual(p.epi, p.N, n4, m0 + r0 + lm + u * kEpiWarps, p.c_vec4 != 0);
+                }
+            } else if (owner) {
+                b2[0] = load_gated_bias(p.epi, 0, quad_feature(n4));
+                b2[1] = load_gated_bias(p.epi, 0, quad_feature(n4) + 1);
+            }
+        }
         bool got = !owner || mbar_wait_cluster(red_bar, 0, lim);
         if (!got) fail(p, flags);
         // lanes may run out of time apart, but exchange what they have below
@@ -683,7 +696,6 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
         __syncwarp();
         cluster_arrive();
         if (threadIdx.x == 96) MXFP4_PHASE(9);
-        if (kEpi != kEpiPlain && owner) pdl_wait_prior_grid();   // for the residual and the bias
         if (owner && got) {
             // a thread sums 4 consecutive columns of rows lm, lm+8, lm+16, lm+24 over the sources
             // in rank order; the four rows' values of a source are loaded before any is added
@@ -693,9 +705,18 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
             const int nl4 = (et & 31) * 4;
             const int n4 = n0 + nl4;
             const bool v4 = p.c_vec4 && n4 + 3 < p.N;
-            constexpr int kRows = 4;
             for (int lm0 = et >> 5; lm0 < nrows; lm0 += kRows * kEpiWarps) {
                 float4 acc[kRows];
+                [[maybe_unused]] uint2 now[kRows];
+                if constexpr (kEpi == kEpiLinear) {          // the next rows' residual while these are summed
+#pragma unroll
+                    for (int u = 0; u < kRows; ++u) {
+                        const int lm = lm0 + (kRows + u) * kEpiWarps;
+                        now[u] = res[u];
+                        if (p.epi.residual && lm < nrows)
+                            res[u] = quad_residual(p.epi, p.N, n4, m0 + r0 + lm, p.c_vec4 != 0);
+                    }
+                }
                 for (int src = 0; src < S; ++src) {
                     const float* base = src == split ? sStage + r0 * kTileN : sRecv + src * rows_per * kTileN;
                     float4 v[kRows];
@@ -722,10 +743,10 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
                     const int lm = lm0 + u * kEpiWarps;
                     if (lm >= nrows) break;
                     if constexpr (kEpi == kEpiLinear) {
-                        store_quad(p.epi, p.N, n4, m0 + r0 + lm, acc[u], p.c, p.ldc, p.c_vec4 != 0);
+                        store_quad(p.epi, p.N, n4, m0 + r0 + lm, acc[u], b4, now[u], p.c, p.ldc, p.c_vec4 != 0);
                         continue;
                     } else if constexpr (kEpi == kEpiGated) {
-                        store_quad_gated(p.epi, n4, m0 + r0 + lm, acc[u], p.c, p.ldc, p.c_vec4 != 0);
+                        store_quad_gated(p.epi, b2, n4, m0 + r0 + lm, acc[u], p.c, p.ldc, p.c_vec4 != 0);
                         continue;
                     }
                     uint16_t* crow = p.c + static_cast<int64_t>(m0 + r0 + lm) * p.ldc;
@@ -797,6 +818,13 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
             tmem_dealloc(tmem_base, p.tmem_cols);
         }
         if (warp >= 3 && r1 > r0) {
+            [[maybe_unused]] TokenRun<4> own;      // what the epilogue adds, of the first rows
+            [[maybe_unused]] GatedBias own2;
+            if constexpr (kEpi != kEpiPlain) {
+                const int t = threadIdx.x - 96, row_n = n0 + (t & (kTileN - 1)), lm = t / kTileN * 4;
+                if constexpr (kEpi == kEpiLinear) load_run(p.epi, p.N, row_n, m0 + r0 + lm, r1 - r0 - lm, own);
+                else own2 = load_gated_bias(p.epi, 0, gated_feature(row_n));
+            }
             bool got = mbar_wait_cluster(red_bar, 0, lim);
             if (!got) fail(p, flags);
             if (kEpi == kEpiGated) got = __all_sync(0xffffffffu, got);   // one decision: see above
@@ -807,7 +835,6 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
             const int nrows = r1 - r0;
             const int cn = et & (kTileN - 1);
             const int nn = n0 + cn;
-            if (kEpi != kEpiPlain) pdl_wait_prior_grid();        // for the residual and the bias
             if (kEpi != kEpiPlain || nn < p.N) {
                 for (int lm = (et / kTileN) * 4; lm < nrows; lm += 4 * (kEpiThreads / kTileN)) {
                     float4 acc = *reinterpret_cast<const float4*>(sRecv + cn * stride + lm);
@@ -819,14 +846,15 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
                         acc.w += v.w;
                     }
                     if constexpr (kEpi == kEpiLinear) {
-                        float run[4] = {acc.x, acc.y, acc.z, acc.w};
-                        uint16_t res[4];
-                        residual_run(p.epi, p.N, nn, m0 + r0 + lm, min(4, nrows - lm), res);
-                        store_run(p.epi, p.N, nn, m0 + r0 + lm, min(4, nrows - lm), run, res, p.c, p.ldc);
+                        float sums[4] = {acc.x, acc.y, acc.z, acc.w};
+                        store_run(p.epi, p.N, nn, m0 + r0 + lm, min(4, nrows - lm), sums, own, p.c, p.ldc);
+                        lm += 4 * (kEpiThreads / kTileN);
+                        if (lm < nrows) load_run(p.epi, p.N, nn, m0 + r0 + lm, nrows - lm, own);
+                        lm -= 4 * (kEpiThreads / kTileN);
                         continue;
                     } else if constexpr (kEpi == kEpiGated) {
-                        const float run[4] = {acc.x, acc.y, acc.z, acc.w};
-                        store_run_gated(p.epi, 0, nn, m0 + r0 + lm, min(4, nrows - lm), run, p.c, p.ldc);
+                        const float sums[4] = {acc.x, acc.y, acc.z, acc.w};
+                        store_run_gated(p.epi, own2, nn, m0 + r0 + lm, min(4, nrows - lm), sums, p.c, p.ldc);
                         continue;
                     }
                     uint16_t* cp = p.c + static_cast<int64_t>(m0 + r0 + lm) * p.ldc + nn;
@@ -882,14 +910,29 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
         tmem_dealloc(tmem_base, p.tmem_cols);
     }
     if (warp >= 3) {
-        if (kEpi != kEpiPlain) pdl_wait_prior_grid();   // for the residual and the bias
         // owner: a thread sums 4 consecutive columns of one row over the sources in rank order
         const int et = threadIdx.x - 96;
         const int nrows = r1 - r0;
         const int nl4 = (et & 31) * 4;
         const int n4 = n0 + nl4;
         const bool v4 = p.c_vec4 && n4 + 3 < p.N;
+        [[maybe_unused]] float4 b4;
+        [[maybe_unused]] uint2 res;
+        [[maybe_unused]] GatedBias b2[2];
+        if constexpr (kEpi == kEpiLinear) {
+            b4 = quad_bias(p.epi, p.N, n4);
+            if (p.epi.residual && (et >> 5) < nrows) res = quad_residual(p.epi, p.N, n4, m0 + r0 + (et >> 5), p.c_vec4 != 0);
+        } else if constexpr (kEpi == kEpiGated) {
+            b2[0] = load_gated_bias(p.epi, 0, quad_feature(n4));
+            b2[1] = load_gated_bias(p.epi, 0, quad_feature(n4) + 1);
+        }
         for (int lm = et >> 5; lm < nrows; lm += kEpiWarps) {
+            [[maybe_unused]] uint2 now;
+            if constexpr (kEpi == kEpiLinear) {      // the next row's residual while this one is summed
+                now = res;
+                if (p.epi.residual && lm + kEpiWarps < nrows)
+                    res = quad_residual(p.epi, p.N, n4, m0 + r0 + lm + kEpiWarps, p.c_vec4 != 0);
+            }
             float4 acc = *reinterpret_cast<const float4*>(sRecv + lm * kTileN + nl4);
             for (int src = 1; src < S; ++src) {
                 const float4 v = *reinterpret_cast<const float4*>(sRecv + (src * rows_per + lm) * kTileN + nl4);
@@ -899,10 +942,10 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
                 acc.w += v.w;
             }
             if constexpr (kEpi == kEpiLinear) {
-                store_quad(p.epi, p.N, n4, m0 + r0 + lm, acc, p.c, p.ldc, p.c_vec4 != 0);
+                store_quad(p.epi, p.N, n4, m0 + r0 + lm, acc, b4, now, p.c, p.ldc, p.c_vec4 != 0);
                 continue;
             } else if constexpr (kEpi == kEpiGated) {
-                store_quad_gated(p.epi, n4, m0 + r0 + lm, acc, p.c, p.ldc, p.c_vec4 != 0);
+                store_quad_gated(p.epi, b2, n4, m0 + r0 + lm, acc, p.c, p.ldc, p.c_vec4 != 0);
                 continue;
             }
             uint16_t* crow = p.c + static_cast<int64_t>(m0 + r0 + lm) * p.ldc;

@@ -112,7 +112,7 @@ __device__ __forceinline__ void quantize_item(const AItem& it, const uint32_t (&
 // (plans that read A before the dependency wait); otherwise at most two, all loaded at once.
 // kEpi: what the sums go through before they are stored (epilogue.cuh).
 template <bool kMany, int kEpi>
-__global__ void __launch_bounds__(kResThreads, 1)
+__global__ void __launch_bounds__(kResThreads, kEpi == kEpiPlain ? 1 : 2)
 mxfp4_gemm_resident_kernel(const EpilogueArgs<ResidentArgs, kEpi> p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -358,6 +358,16 @@ mxfp4_gemm_resident_kernel(const EpilogueArgs<ResidentArgs, kEpi> p) {
     const bool sum_helpers = S > 1 && own_sums * G > 128;
     const int sum_threads = sum_helpers ? 256 : 128;
     auto owner_sum = [&](const int t0, const bool ok_in) {
+        [[maybe_unused]] TokenRun<4> run;             // what the epilogue adds, of the thread's first sum
+        [[maybe_unused]] GatedBias b2;
+        if constexpr (kEpi == kEpiLinear) {
+            if (t0 < own_sums * G) {
+                const int g = t0 / own_sums, n = n0 + own0 + t0 - g * own_sums;
+                load_run(p.epi, p.N, n, m0 + 4 * g, m_valid - 4 * g, run);
+            }
+        } else if constexpr (kEpi == kEpiGated) {
+            if (t0 < own_sums * G) b2 = load_gated_bias(p.epi, 0, ((n0 + own0) >> 1) + t0 % own_sums);
+        }
         const bool got = mbar_wait_cluster(red_bar, 0, lim);
         if (!got) res_fail(p, abort_flag);
         if (threadIdx.x == 128) RES_PHASE(9);
@@ -393,15 +403,15 @@ mxfp4_gemm_resident_kernel(const EpilogueArgs<ResidentArgs, kEpi> p) {
                         }
                     }
                 }
+                if (t != t0) b2 = load_gated_bias(p.epi, 0, f);
                 if (f < p.epi.features) {
-                    const float bg = bias_at(p.epi, f), bu = bias_at(p.epi, p.epi.features + f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) zg[i] += bg;
+                    for (int i = 0; i < 4; ++i) zg[i] += b2.gate;
                     activate(p.epi.act, zg);
                     uint16_t* cp = p.c + static_cast<int64_t>(m0 + 4 * g) * p.ldc + f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        if (4 * g + i < m_valid) *cp = to_bf16(zg[i] * (zu[i] + bu));
+                        if (4 * g + i < m_valid) *cp = to_bf16(zg[i] * (zu[i] + b2.up));
                         cp += p.ldc;
                     }
                 }
@@ -412,8 +422,8 @@ mxfp4_gemm_resident_kernel(const EpilogueArgs<ResidentArgs, kEpi> p) {
                 const int g = t / own_rows;
                 const int r = t - g * own_rows;
                 const int n = n0 + own0 + r;
-                uint16_t res[4];
-                if constexpr (kEpi == kEpiLinear) residual_run(p.epi, p.N, n, m0 + 4 * g, min(4, m_valid - 4 * g), res);
+                if constexpr (kEpi == kEpiLinear)
+                    if (t != t0) load_run(p.epi, p.N, n, m0 + 4 * g, m_valid - 4 * g, run);
                 float4 acc = rv[g * R + r];
                 for (int s0 = 1; s0 < S; s0 += 8) {
                     float4 x[8];
@@ -431,8 +441,8 @@ mxfp4_gemm_resident_kernel(const EpilogueArgs<ResidentArgs, kEpi> p) {
                     }
                 }
                 if constexpr (kEpi == kEpiLinear) {
-                    float run[4] = {acc.x, acc.y, acc.z, acc.w};
-                    store_run(p.epi, p.N, n, m0 + 4 * g, min(4, m_valid - 4 * g), run, res, p.c, p.ldc);
+                    float sums[4] = {acc.x, acc.y, acc.z, acc.w};
+                    store_run(p.epi, p.N, n, m0 + 4 * g, min(4, m_valid - 4 * g), sums, run, p.c, p.ldc);
                 } else if (n < p.N) {
                     uint16_t* cp = p.c + static_cast<int64_t>(m0 + 4 * g) * p.ldc + n;
                     const float vals[4] = {acc.x, acc.y, acc.z, acc.w};
@@ -476,12 +486,27 @@ mxfp4_gemm_resident_kernel(const EpilogueArgs<ResidentArgs, kEpi> p) {
         dst = map_to_rank(smem_addr(sRecv) + off, static_cast<uint32_t>(owner));
         bar = map_to_rank(smem_addr(red_bar), static_cast<uint32_t>(owner));
     }
+    // One K slice: what the epilogue adds is asked for while the MMAs run. (It may be the previous grid's, like A:
+    // these warps have waited for that.)
+    [[maybe_unused]] LaneStore<kEpi> lane_store;
+    if constexpr (kEpi != kEpiPlain)
+        if (S == 1) lane_store.load_first(p.epi, 0, p.N, n0 + nl, m0, m_valid, 0);
     const bool waited = mbar_wait(acc_full, 0, lim);
     tc_fence_after_sync();
     if (!waited) res_fail(p, abort_flag);
     if (threadIdx.x == 128) RES_PHASE(7);
     // one decision per warp (tcgen05.ld is warp-collective)
     const bool ok = !__any_sync(0xffffffffu, !waited || abort_flag[0] != 0u);
+    if constexpr (kEpi != kEpiPlain) {
+        if (S == 1) {
+            if (ok)
+                lane_store.store(p.epi, p.N, n0 + nl, m0, m_valid, 0, 16, tmem_base + (static_cast<uint32_t>(q * 32) << 16),
+                                 min(NI, na), static_cast<uint32_t>(p.m_tile), p.c, p.ldc);
+            tc_fence_before_sync();
+            named_barrier_arrive(2, 32 + 128);        // warp 1 may free tensor memory now
+            return;
+        }
+    }
     uint32_t v[32];
     if (ok) {
         // the two issuers' accumulators, added (the second holds data from two steps on)
@@ -512,14 +537,7 @@ mxfp4_gemm_resident_kernel(const EpilogueArgs<ResidentArgs, kEpi> p) {
 
     if (S == 1) {
         // one K slice: accumulator -> bf16 C, one output column per thread
-        // (the residual and the bias may be the previous grid's: every warp but 1 and 2 has waited for it)
-        if constexpr (kEpi == kEpiLinear) {
-            uint16_t res[32];
-            residual_run(p.epi, p.N, n0 + nl, m0, m_valid, res);
-            if (ok) store_run(p.epi, p.N, n0 + nl, m0, m_valid, reinterpret_cast<float(&)[32]>(v), res, p.c, p.ldc);
-        } else if constexpr (kEpi == kEpiGated) {
-            if (ok) store_run_gated(p.epi, 0, n0 + nl, m0, m_valid, reinterpret_cast<float(&)[32]>(v), p.c, p.ldc);
-        } else if (ok && n0 + nl < p.N) {
+        if (ok && n0 + nl < p.N) {
             uint16_t* cp = p.c + static_cast<int64_t>(m0) * p.ldc + n0 + nl;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {

@@ -38,7 +38,7 @@ int dense_plan(const DeviceInfo& di, int64_t M, int64_t N, int64_t K, int kind, 
     if (st != MXFP4_OK) return st;
     p.ws_bytes = p.gemm.ws_total;
     if (p.gemm.path == 2 && p.gemm.ctas > di.sm_count && M <= kMaxRows &&
-        make_stream_plan(M, 1, N, K, 1, di.sm_count, stream_clusters, &p.stream, equal_tiles(M, 192)) == 0) {
+        make_stream_plan(M, 1, N, K, 1, di.sm_count, stream_clusters, &p.stream, equal_tiles(M, 192), kind) == 0) {
         p.streams = true;
         p.ws_bytes = p.stream.ws_total;
     }
@@ -77,8 +77,9 @@ int run_dense(const void* x, int64_t M, int64_t K, int64_t ldx, const void* pack
     a.K = K;
     a.groups = 1;
     a.rows = static_cast<int>(M);
-    a.c_wide = aligned(out, 16) && ldo % 8 == 0 &&
-               (!epi.residual || (aligned(epi.residual, 16) && epi.ldr % 8 == 0)) ? 1 : 0;
+    // (a tensor map's rows are less than 2^40 bytes apart)
+    auto wide = [](const void* m, int64_t ld) { return aligned(m, 16) && ld % 8 == 0 && ld < int64_t(1) << 39; };
+    a.c_wide = wide(out, ldo) && (!epi.residual || wide(epi.residual, epi.ldr)) ? 1 : 0;
     a.epi = epi;
 #ifdef MXFP4_TEST_HOOKS
     a.test_give_up = {-1, 0, 0};

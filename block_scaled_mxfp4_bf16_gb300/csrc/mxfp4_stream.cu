@@ -316,7 +316,7 @@ __device__ __forceinline__ void write_step(const StreamArgs& p, const Walk& u, i
 // kEpi: what the sums go through before they are stored (epilogue.cuh).
 template <int kTermsPer, bool kFused, int kEpi>
 __global__ void __launch_bounds__(stream_threads(kTermsPer, kFused), 1)
-mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p) {
+mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p, const __grid_constant__ EpilogueMaps<kEpi> epi_maps) {
     constexpr int kThreads = stream_threads(kTermsPer, kFused);
     constexpr int kTokenWarps = token_warps(kTermsPer);
     extern __shared__ uint8_t smem_raw[];
@@ -324,16 +324,18 @@ mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p) {
     const uint32_t stage_bytes = kWBlock + p.a_block;
     uint8_t* sW = smem;                                          // [stages][kWBlock]
     uint8_t* sT = smem + static_cast<uint32_t>(p.stages) * kWBlock;   // [stages][a_block]
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + static_cast<uint32_t>(p.stages) * stage_bytes);
+    uint8_t* ring = smem + static_cast<uint32_t>(p.stages) * stage_bytes;
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + ring_bytes(kEpi));
     uint64_t* empty = full + kStreamMaxStages;
     uint64_t* acc_full = empty + kStreamMaxStages;               // [2]
     uint64_t* acc_empty = acc_full + 2;                          // [2]
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    uint64_t* ring_bars = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring_bars + ring_barrier_bytes(kEpi) / 8);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     volatile uint32_t* last_flag = tmem_slot + 4;                // [2] a slot
     int* warp_sum = reinterpret_cast<int*>(tmem_slot + 8);       // [16]
     uint8_t* epi_stage = reinterpret_cast<uint8_t*>(warp_sum + 16);   // [8 warps][kEpiStage]
-    int* prefix = reinterpret_cast<int*>(epi_stage + 8 * kEpiStage);  // [groups + 1] token tiles before a group
+    int* prefix = reinterpret_cast<int*>(epi_stage + epi_stage_bytes(kEpi));  // [groups + 1] token tiles before a group
     int* begins = prefix + p.groups + 1;                              // [groups + 1] first rows of the groups
     float* recv = reinterpret_cast<float*>(begins + p.groups + 1);    // [cluster][tokens][128], first CTA of a cluster
 
@@ -348,6 +350,9 @@ mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p) {
     } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
         mbar_init(&acc_full[threadIdx.x - 32], 1);
         mbar_init(&acc_empty[threadIdx.x - 32], kStreamEpiThreads / 32);
+        fence_mbar_init();
+    } else if (kEpi == kEpiLinear && threadIdx.x >= 96 && threadIdx.x < 96 + 8 * kRingSlots) {
+        mbar_init(&ring_bars[threadIdx.x - 96], 1);
         fence_mbar_init();
     } else if (threadIdx.x == 64) {
         *abort_flag = 0u;
@@ -557,8 +562,10 @@ mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p) {
         Walk u = start;
         int nshare = 0;
         bool live = true;
+        EpilogueRing<kEpi> pieces(epi_maps, ring, ring_bars, warp - 4, lane);
         while (next_share(p, prefix, u)) {
             const int b = nshare & 1;
+            if (live) pieces.begin(p, u, u.nt, half, warp);
             live = live && share_ready(p, &acc_full[b], (nshare >> 1) & 1, nshare, abort_flag);
             if (clustered && !live) break;
             tc_fence_after_sync();
@@ -587,13 +594,14 @@ mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p) {
                 }
             } else {
                 live = store_unit<kTermsPer, false, kEpi>(p, u, u.nt, acc, half, warp, lane, last_flag,
-                                                    epi_stage + (warp - 4) * kEpiStage, live);
+                                                    epi_stage + (warp - 4) * kEpiStage, live, pieces);
             }
             tc_fence_before_sync();
             __syncwarp();
             if (live && lane == 0) mbar_arrive(&acc_empty[b]);
             ++nshare;
         }
+        pieces.finish(p);
         if (clustered && nshare == 0) cluster_wait();   // failed: the handshake all the same
     }
     if (clustered && (warp < 4 || warp >= 12)) {
@@ -627,7 +635,7 @@ mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p) {
 // ------------------------------------------------------------------------ plan and launches
 
 int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count,
-                     int (*clusters_of)(int), StreamPlan* out, int m_tile) {
+                     int (*clusters_of)(int), StreamPlan* out, int m_tile, int epi) {
     StreamPlan p = {};
     p.k_atoms = static_cast<int>((K + kAtomK - 1) / kAtomK);
     p.n_tiles = static_cast<int>((N + kTileN - 1) / kTileN);
@@ -666,7 +674,7 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     p.pair = terms == 1 && p.m_tile > 128 && p.n_tiles > 1 && p.k_atoms >= kPairSteps;
     p.nmc = (p.m_tile + 127) / 128;
     p.a_block = static_cast<uint32_t>(p.m_tile) * 128u + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
-    size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 + 8 * kEpiStage +
+    size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 + epi_stage_bytes(epi) +
                          2 * (static_cast<size_t>(groups) + 1) * 4;
     const int64_t tiles = stream_tile_bound(rows, groups, p.m_tile);
     if (tiles * p.n_tiles > (int64_t(1) << 31) - 1) return -1;
@@ -682,12 +690,13 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
             }
     }
     const size_t recv = static_cast<size_t>(p.cluster > 1 ? p.cluster : 0) * (p.m_tile / terms) * kTileN * sizeof(float);
-    extra += recv;
+    extra += recv + ring_bytes(epi) + ring_barrier_bytes(epi);
     if (p.pair) extra += kStreamMaxStages * 8 + 64;   // a third set of barriers, more warps' sums
     const uint32_t t_stage =
         p.pair ? pair_code_bytes(p.m_tile) + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk : p.a_block;   // a CTA's part of a token block
     p.stages = static_cast<int>((kSmemLimit - extra) / (kWBlock + t_stage));
     if (p.stages > kStreamMaxStages) p.stages = kStreamMaxStages;
+    if (p.pair) p.stages = pair_stages(p.stages);
     // One share per CTA: one accumulator, and no more stages than it has steps, so that the next call's
     // CTAs fit beside this one's and ask for their weights while it ends.
     const int64_t steps = (terms > 1 ? all_units : tiles * p.n_tiles) * static_cast<int64_t>(p.k_atoms);
@@ -822,7 +831,10 @@ static cudaError_t launch_stream_as(const StreamPlan& plan, const EpilogueArgs<S
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = stream_config(dim3(plan.ctas), dim3(stream_threads(kTermsPer, kFused)),
                                                  plan.smem_bytes, s, plan.cluster, attr);
-    return cudaLaunchKernelEx(&cfg, mxfp4_stream_kernel<kTermsPer, kFused, kEpi>, args);
+    EpilogueMaps<kEpi> epi_maps = {};
+    if constexpr (kEpi == kEpiLinear)
+        if (args.c_wide && !encode_linear_maps(args, &epi_maps)) return cudaErrorInvalidValue;
+    return cudaLaunchKernelEx(&cfg, mxfp4_stream_kernel<kTermsPer, kFused, kEpi>, args, epi_maps);
 }
 
 cudaError_t launch_stream(const StreamPlan& plan, const StreamArgs& args, int terms, cudaStream_t s) {
@@ -839,6 +851,34 @@ cudaError_t launch_stream(const StreamPlan& plan, const WithEpilogue<StreamArgs>
     if (kind == kEpiLinear) return launch_stream_as<1, false, kEpiLinear>(plan, args, s);
     return plan.fused ? launch_stream_as<1, true, kEpiGated>(plan, args, s)
                       : launch_stream_as<1, false, kEpiGated>(plan, args, s);
+}
+
+TensorMapEncoder tensor_map_encoder() {
+    static std::atomic<TensorMapEncoder> known{nullptr};
+    TensorMapEncoder f = known.load(std::memory_order_acquire);
+    if (f) return f;
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+        return nullptr;
+    f = reinterpret_cast<TensorMapEncoder>(fn);
+    known.store(f, std::memory_order_release);
+    return f;
+}
+
+bool encode_linear_maps(const WithEpilogue<StreamArgs>& args, LinearMaps* maps) {
+    const TensorMapEncoder encode = tensor_map_encoder();
+    auto matrix = [&](CUtensorMap* map, const uint16_t* base, int64_t ld) {
+        const cuuint64_t dims[2] = {static_cast<cuuint64_t>(args.N), static_cast<cuuint64_t>(args.rows)};
+        const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * 2};
+        const cuuint32_t boxes[2] = {32, 16}, steps[2] = {1, 1};
+        return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<uint16_t*>(base), dims, strides, boxes, steps,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return encode && matrix(&maps->out, args.c, args.ldc) &&
+           (!args.epi.residual || matrix(&maps->residual, args.epi.residual, args.epi.ldr));
 }
 
 void fill_stream_args(const StreamPlan& plan, const DeviceInfo& di, uint8_t* ws, StreamArgs* out) {

@@ -85,24 +85,27 @@ struct PairMaps {
 
 template <int kEpi>
 __global__ void __launch_bounds__(kPairThreads, 1)
-mxfp4_stream_pair_kernel(const __grid_constant__ EpilogueArgs<StreamArgs, kEpi> p, const __grid_constant__ PairMaps maps) {
+mxfp4_stream_pair_kernel(const __grid_constant__ EpilogueArgs<StreamArgs, kEpi> p, const __grid_constant__ PairMaps maps,
+                         const __grid_constant__ EpilogueMaps<kEpi> epi_maps) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t t_rows = pair_code_bytes(p.m_tile);                         // half a tile's code rows, at most
     const uint32_t t_stage = t_rows + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
     uint8_t* sW = smem;                                                        // [stages][kWBlock]
     uint8_t* sT = smem + static_cast<uint32_t>(p.stages) * kWBlock;            // [stages][t_stage]
-    uint64_t* full = reinterpret_cast<uint64_t*>(sT + static_cast<uint32_t>(p.stages) * t_stage);   // a stage's scale factors
+    uint8_t* ring = sT + static_cast<uint32_t>(p.stages) * t_stage;
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + ring_bytes(kEpi));     // a stage's scale factors
     uint64_t* empty = full + kStreamMaxStages;
     uint64_t* ready = empty + kStreamMaxStages;    // first CTA: both CTAs' codes and scale factors of a stage
     uint64_t* acc_full = ready + kStreamMaxStages;                             // [2]
     uint64_t* acc_empty = acc_full + 2;                                        // [2] first CTA: both CTAs' epilogues
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
+    uint64_t* ring_bars = acc_empty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ring_bars + ring_barrier_bytes(kEpi) / 8);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     volatile uint32_t* last_flag = tmem_slot + 4;
     int* warp_sum = reinterpret_cast<int*>(tmem_slot + 8);
     uint8_t* epi_stage = reinterpret_cast<uint8_t*>(warp_sum + 32);
-    int* prefix = reinterpret_cast<int*>(epi_stage + 8 * kEpiStage);
+    int* prefix = reinterpret_cast<int*>(epi_stage + epi_stage_bytes(kEpi));
     int* begins = prefix + p.groups + 1;
 
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
@@ -118,6 +121,9 @@ mxfp4_stream_pair_kernel(const __grid_constant__ EpilogueArgs<StreamArgs, kEpi> 
     } else if (threadIdx.x >= 32 && threadIdx.x < 34) {
         mbar_init(&acc_full[threadIdx.x - 32], 1);
         mbar_init(&acc_empty[threadIdx.x - 32], 2 * kStreamEpiThreads / 32);
+        fence_mbar_init();
+    } else if (kEpi == kEpiLinear && threadIdx.x >= 96 && threadIdx.x < 96 + 8 * kRingSlots) {
+        mbar_init(&ring_bars[threadIdx.x - 96], 1);
         fence_mbar_init();
     } else if (threadIdx.x == 64) {
         *abort_flag = 0u;
@@ -318,17 +324,20 @@ mxfp4_stream_pair_kernel(const __grid_constant__ EpilogueArgs<StreamArgs, kEpi> 
         Walk u = start;
         int nshare = 0;
         bool live = true;
+        EpilogueRing<kEpi> pieces(epi_maps, ring, ring_bars, warp - 4, lane);
         while (next_share<true>(p, prefix, u)) {
             const int b = nshare & 1;
+            if (live) pieces.begin(p, u, 2 * u.nt + static_cast<int>(rank), half, warp);
             live = live && share_ready(p, &acc_full[b], (nshare >> 1) & 1, nshare, abort_flag);
             tc_fence_after_sync();
             live = store_unit<1, true, kEpi>(p, u, 2 * u.nt + static_cast<int>(rank), trow + static_cast<uint32_t>(b * p.m_tile), half,
-                                       warp, lane, last_flag, epi_stage + (warp - 4) * kEpiStage, live);
+                                       warp, lane, last_flag, epi_stage + (warp - 4) * kEpiStage, live, pieces);
             tc_fence_before_sync();
             __syncwarp();
             if (live && lane == 0) arrive_first(map_to_rank(smem_addr(&acc_empty[b]), 0u));
             ++nshare;
         }
+        pieces.finish(p);
     }
     // Neither CTA ends before the other's arrivals and MMAs (on both CTAs' memory) are over.
     tc_fence_before_sync();
@@ -339,22 +348,6 @@ mxfp4_stream_pair_kernel(const __grid_constant__ EpilogueArgs<StreamArgs, kEpi> 
         tmem_dealloc_pair(*tmem_slot, p.tmem_cols);
     }
     if (threadIdx.x == 128) arrive_unstored(p, last_flag);
-}
-
-// The driver's encoder of tensor maps, looked up once (the library does not link the driver).
-using TensorMapEncoder = decltype(&cuTensorMapEncodeTiled);
-static TensorMapEncoder tensor_map_encoder() {
-    static std::atomic<TensorMapEncoder> known{nullptr};
-    TensorMapEncoder f = known.load(std::memory_order_acquire);
-    if (f) return f;
-    void* fn = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-        return nullptr;
-    f = reinterpret_cast<TensorMapEncoder>(fn);
-    known.store(f, std::memory_order_release);
-    return f;
 }
 
 // `bytes` from `base` on as rows of 1 KB, copied `box` rows at a time.
@@ -403,7 +396,10 @@ static cudaError_t launch_pair_as(const StreamPlan& plan, const EpilogueArgs<Str
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, mxfp4_stream_pair_kernel<kEpi>, args, maps);
+    EpilogueMaps<kEpi> epi_maps = {};
+    if constexpr (kEpi == kEpiLinear)
+        if (args.c_wide && !encode_linear_maps(args, &epi_maps)) return cudaErrorInvalidValue;
+    return cudaLaunchKernelEx(&cfg, mxfp4_stream_pair_kernel<kEpi>, args, maps, epi_maps);
 }
 
 cudaError_t launch_stream_pair(const StreamPlan& plan, const StreamArgs& args, cudaStream_t s) {

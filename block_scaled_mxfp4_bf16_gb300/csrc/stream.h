@@ -15,10 +15,31 @@ constexpr int stream_threads(int terms, bool fused) { return kStreamThreads + (f
 constexpr int kSplitSteps = 8;            // 256-K steps that splitting a unit between CTAs has to save
 constexpr int kMergeSteps = 7;            // and that cutting a full wave together with the rest has to save
 constexpr int kStreamMaxStages = 10;
+// The linear epilogue's ring of shared memory, a slot for 16 tokens of a warp's 32 weight rows (64 bytes each), and its
+// barriers; the other epilogues have none.
+constexpr int kRingSlots = 4, kRingSlot = 1024;
+__host__ __device__ constexpr uint32_t ring_bytes(int epi) { return epi == kEpiLinear ? 8u * kRingSlots * kRingSlot : 0u; }
+__host__ __device__ constexpr uint32_t ring_barrier_bytes(int epi) { return epi == kEpiLinear ? 8u * kRingSlots * 8u : 0u; }
+// What the other epilogues' warps transpose through (kEpiStage each).
+__host__ __device__ constexpr uint32_t epi_stage_bytes(int epi) { return epi == kEpiLinear ? 0u : 8u * 1024u; }
+// C and the residual as the linear epilogue copies them: boxes of 16 rows x 32 columns, in 64-byte swizzled rows.
+struct LinearMaps {
+    CUtensorMap out, residual;
+};
+struct NoMaps {};
+template <int kEpi>
+using EpilogueMaps = std::conditional_t<kEpi == kEpiLinear, LinearMaps, NoMaps>;
 constexpr int kEpiStage = 1024;           // bytes of shared memory an epilogue warp transposes through
 constexpr int kPairThreads = 640;         // the pair kernel: warps 12-19 write scale factors
 constexpr int kPairSfSlots = 5;           // steps whose scale factors are in tensor memory at once
 constexpr uint32_t kPairSfCols = 24;      // columns of one step: 8 weights, 16 tokens
+// Of the stages that fit, those the pair kernel runs with. Its scale warps work in two sets, every other step each, so
+// with an odd number of stages a set meets every other fill of a stage only, and the parity of the stage's barrier does
+// not tell it a fill from the one before last. What keeps them apart is what the set waited for at its last step,
+// n - 2: that step n - 2 - kPairSfSlots was over. For that to be the stage's last fill or a later step, an odd number has
+// to be kPairSfSlots + 2 at least. (With five, late scale factors were taken from the fill before, and the next fill
+// announced to a barrier that still waited for them: wrong tiles, then a launch failure.)
+__host__ __device__ constexpr int pair_stages(int fit) { return fit % 2 && fit < kPairSfSlots + 2 ? fit - 1 : fit; }
 // Bytes of a stage that a CTA of a pair needs for its half of a tile's codes: boxes move 2 KB at a time.
 __host__ __device__ inline uint32_t pair_code_bytes(int m_tile) {
     return (static_cast<uint32_t>(m_tile) * 64u + 2047u) / 2048u * 2048u;
@@ -124,9 +145,14 @@ int stream_clusters(int size);
 
 // Plan for `rows` token-block rows in `groups` groups; terms: 1 (grouped) or kTerms; clusters_of:
 // stream_clusters, or a model of it.
-// m_tile: tokens per tile (a multiple of 16, up to 192) where the caller has chosen them, or 0.
+// m_tile: tokens per tile (a multiple of 16, up to 192) where the caller has chosen them, or 0; epi: the epilogue.
 int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count,
-                     int (*clusters_of)(int), StreamPlan* plan, int m_tile = 0);
+                     int (*clusters_of)(int), StreamPlan* plan, int m_tile = 0, int epi = kEpiPlain);
+// The driver's encoder of tensor maps, looked up once (the library does not link the driver); null if there is none.
+using TensorMapEncoder = decltype(&cuTensorMapEncodeTiled);
+TensorMapEncoder tensor_map_encoder();
+// The linear epilogue's maps of a call (C with N columns and `rows` rows); false where it cannot be had.
+bool encode_linear_maps(const WithEpilogue<StreamArgs>& args, LinearMaps* maps);
 
 // a [tokens, K] rows -> token blocks of the sorted rows: row r of the blocks is a[index ? index[r] : r].
 cudaError_t launch_quantize_groups(const uint16_t* a, int64_t tokens, int64_t K, int64_t lda, const int32_t* index,

@@ -328,6 +328,15 @@ __device__ __forceinline__ void tmem_load_frag16(uint32_t taddr, uint32_t (&v)[8
         : "r"(taddr)
         : "memory");
 }
+// Wait for the loads of two fragments. Until then their registers are not to be read, moved or given to other
+// values, so the wait names them; and no loop's edge lies between load and wait.
+__device__ __forceinline__ void tmem_frag16_wait(uint32_t (&a)[8], uint32_t (&b)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+                   "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7])
+                 :
+                 : "memory");
+}
 // Four 8x8 matrices of 16-bit values, stored transposed: lane 8m + r gives the address of row r
 // (a column of the fragments) of matrix m, eight values.
 __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -450,16 +459,8 @@ __device__ __forceinline__ void store_tile(const StreamArgs& p, uint32_t trow, i
     }
 }
 
-// Eight consecutive elements of a row of C or of the residual, of which those from column `from` up to `to`
-// exist: whole in one piece (16-byte aligned), else one by one.
-__device__ __forceinline__ uint4 load_piece(const uint16_t* at, int from, int to) {
-    if (from + 8 <= to) return __ldcg(reinterpret_cast<const uint4*>(at));
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int k = 0; k < 7; ++k)
-        if (from + k < to) w[k >> 1] |= static_cast<uint32_t>(__ldcg(at + k)) << (16 * (k & 1));
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
+// Up to eight elements of a row of C, of which those from column `from` up to `to` exist: whole in one piece (16-byte
+// aligned), else one by one.
 __device__ __forceinline__ void store_piece(uint16_t* at, const uint4& v, int from, int to) {
     if (from + 8 <= to) {
         *reinterpret_cast<uint4*>(at) = v;
@@ -471,130 +472,195 @@ __device__ __forceinline__ void store_piece(uint16_t* at, const uint4& v, int fr
         if (from + k < to) at[k] = static_cast<uint16_t>(w[k >> 1] >> (16 * (k & 1)));
 }
 
-// store_tile with an epilogue, 16 tokens at a time. n0: the warp's first weight row; bias0: the group's first bias
-// element (gated). Where rows are aligned to 16 bytes (the residual's too):
-//   linear: as store_tile; the residual takes the same way back, whole pieces to shared memory and from there as
-//           fragments, so that it is added before the one rounding.
-//   gated : a thread's fragments hold the gate's and the up projection's row of two features (lanes 0-15 and 16-31
-//           of the warp's) and two tokens; a token's 16 features are two pieces of shared memory, 32 bytes, the pieces of
-//           tokens 4-7 and 12-15 swapped, so that the eight rows a matrix is stored to touch all banks.
-template <int kEpi, bool kWide>
-__device__ __forceinline__ void store_tile_epi(const WithEpilogue<StreamArgs>& p, uint32_t trow, int tokens, int64_t row0, int n0,
-                                               int64_t bias0, int half, int lane, uint8_t* stage) {
-    if constexpr (!kWide) {
-        for (int cb = half * 16; cb < tokens; cb += 32) {
-            const int cnt = min(16, tokens - cb);
-            uint32_t r[16];
-            if constexpr (kEpi == kEpiLinear) {
-                uint16_t res[16];
-                residual_run(p.epi, p.N, n0 + lane, row0 + cb, cnt, res);
-                tmem_load_16(trow + static_cast<uint32_t>(cb), r);
-                tmem_load_wait();
-                store_run(p.epi, p.N, n0 + lane, row0 + cb, cnt, reinterpret_cast<float(&)[16]>(r), res, p.c, p.ldc);
-            } else {
-                tmem_load_16(trow + static_cast<uint32_t>(cb), r);
-                tmem_load_wait();
-                store_run_gated(p.epi, bias0, n0 + lane, row0 + cb, cnt, reinterpret_cast<float(&)[16]>(r), p.c, p.ldc);
-            }
-            __syncwarp();
+// The tokens [first, rows) of a tile that one of the two epilogue warps of 32 weight rows takes: whole sixteens.
+struct TokenShare {
+    int first, rows;
+};
+__device__ __forceinline__ TokenShare token_share(int tokens, int half) {
+    const int middle = (((tokens + 15) >> 4) + 1) / 2 * 16;
+    return {half ? middle : 0, half ? tokens : min(middle, tokens)};
+}
+
+__device__ __forceinline__ void tensor_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy) : "memory");
+}
+__device__ __forceinline__ void tensor_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the last kLeft stores of this thread have read their shared memory.
+template <int kLeft>
+__device__ __forceinline__ void stores_have_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
+
+// How a linear epilogue's warp moves 16 tokens of its 32 weight rows at a time (a piece): a ring of shared memory in the
+// swizzled layout of store_tile, tensor copies on both sides. The residual's pieces arrive two ahead, of a unit's
+// first pieces before its sums are waited for; a result takes the place of its residual, and a copy takes it to C.
+// Rows past the last token and columns past N are the maps' business: they read as zeros and are not written.
+// Through registers instead (16-byte loads a piece ahead, the transposed piece read back and stored by the lanes),
+// every 16 tokens waited for L2: 3648 x 4096 x 7168 45.6 us without and 58.7 with a residual, where the product alone
+// takes 7.8 of each unit's time.
+template <int kEpi>
+struct EpilogueRing {      // nothing for the other epilogues
+    __device__ __forceinline__ EpilogueRing(const EpilogueMaps<kEpi>&, uint8_t*, uint64_t*, int, int) {}
+    template <typename Args>
+    __device__ __forceinline__ void begin(const Args&, const Walk&, int, int, int) {}
+    template <typename Args>
+    __device__ __forceinline__ void finish(const Args&) {}
+};
+template <>
+struct EpilogueRing<kEpiLinear> {
+    const LinearMaps& maps;
+    uint32_t slots, bars;          // this warp's, in shared memory
+    uint64_t* bar0;
+    uint32_t put;                  // where a lane's matrix rows go in a slot
+    int lane;
+    uint32_t used = 0, asked = 0;  // pieces taken; pieces of the residual asked for
+    int x = 0, y = 0, end = 0;     // the next piece of the residual to ask for; the unit's end
+
+    __device__ __forceinline__ EpilogueRing(const LinearMaps& m, uint8_t* ring, uint64_t* barriers, int w, int l)
+        : maps(m), slots(smem_addr(ring) + static_cast<uint32_t>(w * kRingSlots * kRingSlot)),
+          bars(smem_addr(barriers + w * kRingSlots)), bar0(barriers + w * kRingSlots),
+          put(static_cast<uint32_t>((l & 7) * 64 + (((l >> 3) ^ ((l >> 1) & 3)) << 4))), lane(l) {}
+
+    __device__ __forceinline__ uint32_t slot(uint32_t piece) const { return slots + (piece % kRingSlots) * kRingSlot; }
+
+    // Ask for the next piece of the residual, if there is one: into the slot of the piece kRingSlots before it, whose
+    // store but one or earlier has read it.
+    __device__ __forceinline__ void ask() {
+        if (y >= end) return;
+        if (lane == 0) {
+            stores_have_read<1>();
+            const uint32_t bar = bars + (asked % kRingSlots) * 8u;
+            mbar_expect_if(1u, bar, kRingSlot);
+            tensor_load_2d(slot(asked), &maps.residual, x, y, bar, policy_evict_first());
         }
-        return;
+        ++asked;
+        y += 16;
     }
-    const int middle = (((tokens + 15) >> 4) + 1) / 2 * 16;    // the two warps of 32 weight rows
-    const int first = half ? middle : 0, rows = half ? tokens : min(middle, tokens);   // take [first, rows)
-    const int q = lane >> 2;
-    if constexpr (kEpi == kEpiLinear) {
-        const uint32_t put = smem_addr(stage) + static_cast<uint32_t>((lane & 7) * 64 + (((lane >> 3) ^ ((lane >> 1) & 3)) << 4));
-        uint8_t* get = stage + q * 64 + ((((lane & 3) ^ (q >> 1)) & 3) << 4);
-        const int n = n0 + (lane & 3) * 8;         // this lane's piece of row q, and 512 bytes on that of row q + 8
+    // A whole unit's first pieces.
+    __device__ __forceinline__ void begin(const WithEpilogue<StreamArgs>& p, const Walk& u, int nt, int half, int warp) {
+        x = nt * kTileN + (warp & 3) * 32;
+        y = end = 0;
+        if (!p.c_wide || !p.epi.residual || u.nk != p.k_atoms || x >= p.N) return;
+        const TokenShare t = token_share(u.rows, half);
+        y = static_cast<int>(u.row0) + t.first;
+        end = static_cast<int>(u.row0) + t.rows;
+        asked = used;
+        ask();
+        ask();
+        __syncwarp();
+    }
+    // The accumulator of the tokens of `t`, from tensor memory at trow, to C. Whether all went well.
+    __device__ __forceinline__ bool store(const WithEpilogue<StreamArgs>& p, uint32_t trow, const TokenShare& t, int64_t row0, int n0) {
+        if (n0 >= p.N) return true;
+        const int q = lane >> 2;
         float b[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) b[i] = n0 + q + 8 * i < p.N ? bias_at(p.epi, n0 + q + 8 * i) : 0.f;
         const bool res = p.epi.residual != nullptr;
-        const uint16_t* rp = p.epi.residual + (row0 + first + q) * p.epi.ldr + n;
-        uint16_t* cp = p.c + (row0 + first + q) * p.ldc + n;
-        for (int cb = first; cb < rows; cb += 16) {
-            const bool one = cb + q < rows, two = cb + q + 8 < rows;
-            uint4 r0 = make_uint4(0u, 0u, 0u, 0u), r1 = r0;
-            if (res && one) r0 = load_piece(rp, n, p.N);
-            if (res && two) r1 = load_piece(rp + 8 * p.epi.ldr, n, p.N);
+        for (int cb = t.first; cb < t.rows; cb += 16) {
             uint32_t lo[8], hi[8];
-            tmem_load_frag16(trow + static_cast<uint32_t>(cb), lo);
+            __syncwarp();                          // reads of tensor memory take the whole warp, and whole: lane 0 may
+            tmem_load_frag16(trow + static_cast<uint32_t>(cb), lo);                  // still be about its copies
             tmem_load_frag16(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
+            tmem_frag16_wait(lo, hi);
+            bool got = true;
             if (res) {
-                *reinterpret_cast<uint4*>(get) = r0;
-                *reinterpret_cast<uint4*>(get + 512) = r1;
-                __syncwarp();
+                ask();
+                got = mbar_wait(bar0 + used % kRingSlots, (used / kRingSlots) & 1u, p.wait_limit_ns);
+            } else if (lane == 0) {
+                stores_have_read<kRingSlots - 1>();
             }
-            tmem_load_wait();
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i)           // eight of the first 8 tokens, eight of the next
-                v[i] = __uint_as_float((i & 4) ? hi[(i >> 3) * 4 + (i & 3)] : lo[(i >> 3) * 4 + (i & 3)]) + b[(i >> 1) & 3];
-            activate(p.epi.act, v);
+            if (!__all_sync(0xffffffffu, got)) {
+                atomicOr(p.status, 1u);
+                return false;
+            }
+            __syncwarp();                          // as do matrix stores and loads
+            const uint32_t at = slot(used) + put;
+            // eight tokens at a time: sixteen leave no registers (of the pair kernel's 96) for the activations
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float* w = v + 8 * h;
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i < 4 ? lo[4 * h + i] : hi[4 * h + (i & 3)]) + b[i >> 1];
+                activate(p.epi.act, v);
                 if (res) {
                     uint32_t r[4];
-                    ldmatrix_x4_trans(put + static_cast<uint32_t>(h) * 512u, r);
+                    ldmatrix_x4_trans(at + static_cast<uint32_t>(h) * 512u, r);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        w[2 * i] += bf16_lo(r[i]);
-                        w[2 * i + 1] += bf16_hi(r[i]);
+                        v[2 * i] += bf16_lo(r[i]);
+                        v[2 * i + 1] += bf16_hi(r[i]);
                     }
                     __syncwarp();
                 }
-                stmatrix_x4_trans(put + static_cast<uint32_t>(h) * 512u, pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
-                                  pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
+                stmatrix_x4_trans(at + static_cast<uint32_t>(h) * 512u, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
             }
+            fence_proxy_async_smem();              // the copy reads the piece through the async proxy
             __syncwarp();
-            const uint4 v0 = *reinterpret_cast<const uint4*>(get), v1 = *reinterpret_cast<const uint4*>(get + 512);
-            if (one) store_piece(cp, v0, n, p.N);
-            if (two) store_piece(cp + 8 * p.ldc, v1, n, p.N);
-            rp += 16 * p.epi.ldr;
-            cp += 16 * p.ldc;
-            __syncwarp();
+            if (lane == 0) tensor_store_2d(&maps.out, n0, static_cast<int>(row0) + cb, slot(used));
+            ++used;
         }
-    } else {
-        const int f0 = n0 >> 1;                    // the warp's 16 features
-        const int I = p.epi.features;
-        // matrix lane / 8: tokens 0-7 or 8-15, features 0-7 or 8-15; row lane % 8: a token of them
-        const int tok = (lane >> 4) * 8 + (lane & 7);
-        const uint32_t put = smem_addr(stage) + static_cast<uint32_t>(tok * 32 + ((((lane >> 3) ^ (tok >> 2)) & 1) << 4));
-        const int t = lane >> 1, f = f0 + (lane & 1) * 8;      // this lane's piece: token t, features f .. f + 7
-        const uint8_t* get = stage + t * 32 + (((lane ^ (t >> 2)) & 1) << 4);
-        float bg[2], bu[2];
+        return true;
+    }
+    // No copy may be in flight when the CTA ends.
+    __device__ __forceinline__ void finish(const WithEpilogue<StreamArgs>& p) {
+        for (; used < asked; ++used) mbar_wait(bar0 + used % kRingSlots, (used / kRingSlots) & 1u, p.wait_limit_ns);
+        __syncwarp();
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+};
+
+// store_tile of a gated product, 16 tokens at a time. n0: the warp's first weight row; bias0: the group's first bias
+// element. Where C's rows are aligned to 16 bytes a thread's fragments hold the gate's and the up projection's row of
+// two features (lanes 0-15 and 16-31 of the warp's) and two tokens; a token's 16 features are two pieces of shared
+// memory, 32 bytes, the pieces of tokens 4-7 and 12-15 swapped, so that the eight rows a matrix is stored to touch all
+// banks.
+__device__ __forceinline__ void store_tile_gated(const WithEpilogue<StreamArgs>& p, uint32_t trow, const TokenShare& share,
+                                                 int64_t row0, int n0, int64_t bias0, int lane, uint8_t* stage) {
+    const int q = lane >> 2;
+    const int f0 = n0 >> 1;                        // the warp's 16 features
+    const int I = p.epi.features;
+    // matrix lane / 8: tokens 0-7 or 8-15, features 0-7 or 8-15; row lane % 8: a token of them
+    const int tok = (lane >> 4) * 8 + (lane & 7);
+    const uint32_t put = smem_addr(stage) + static_cast<uint32_t>(tok * 32 + ((((lane >> 3) ^ (tok >> 2)) & 1) << 4));
+    const int t = lane >> 1, f = f0 + (lane & 1) * 8;          // this lane's piece: token t, features f .. f + 7
+    const uint8_t* get = stage + t * 32 + (((lane ^ (t >> 2)) & 1) << 4);
+    GatedBias b[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = f0 + q + 8 * i;
-            bg[i] = at < I ? bias_at(p.epi, bias0 + at) : 0.f;
-            bu[i] = at < I ? bias_at(p.epi, bias0 + I + at) : 0.f;
+    for (int i = 0; i < 2; ++i) b[i] = load_gated_bias(p.epi, bias0, f0 + q + 8 * i);
+    uint16_t* cp = p.c + (row0 + share.first + t) * p.ldc + f;
+    for (int cb = share.first; cb < share.rows; cb += 16) {
+        uint32_t lo[8], hi[8];
+        __syncwarp();                              // reads of tensor memory take the whole warp, and whole
+        tmem_load_frag16(trow + static_cast<uint32_t>(cb), lo);
+        tmem_load_frag16(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
+        tmem_frag16_wait(lo, hi);
+        float g[8], u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {              // tokens 8 (i / 4), features 8 (i / 2 % 2)
+            const uint32_t* from = (i & 2) ? hi : lo;
+            g[i] = __uint_as_float(from[(i >> 2) * 4 + (i & 1)]) + b[(i >> 1) & 1].gate;
+            u[i] = __uint_as_float(from[(i >> 2) * 4 + 2 + (i & 1)]) + b[(i >> 1) & 1].up;
         }
-        uint16_t* cp = p.c + (row0 + first + t) * p.ldc + f;
-        for (int cb = first; cb < rows; cb += 16) {
-            uint32_t lo[8], hi[8];
-            tmem_load_frag16(trow + static_cast<uint32_t>(cb), lo);
-            tmem_load_frag16(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
-            tmem_load_wait();
-            float g[8], u[8];
+        activate(p.epi.act, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {          // tokens 8 (i / 4), features 8 (i / 2 % 2)
-                const uint32_t* from = (i & 2) ? hi : lo;
-                g[i] = __uint_as_float(from[(i >> 2) * 4 + (i & 1)]) + bg[(i >> 1) & 1];
-                u[i] = __uint_as_float(from[(i >> 2) * 4 + 2 + (i & 1)]) + bu[(i >> 1) & 1];
-            }
-            activate(p.epi.act, g);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] *= u[i];
-            stmatrix_x4_trans(put, pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
-                              pack_bf16x2(g[6], g[7]));
-            __syncwarp();
-            const uint4 v = *reinterpret_cast<const uint4*>(get);
-            if (cb + t < rows) store_piece(cp, v, f, I);
-            cp += 16 * p.ldc;
-            __syncwarp();
-        }
+        for (int i = 0; i < 8; ++i) g[i] *= u[i];
+        __syncwarp();
+        stmatrix_x4_trans(put, pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]),
+                          pack_bf16x2(g[6], g[7]));
+        __syncwarp();
+        const uint4 v = *reinterpret_cast<const uint4*>(get);
+        if (cb + t < share.rows) store_piece(cp, v, f, I);
+        cp += 16 * p.ldc;
+        __syncwarp();
     }
 }
 
@@ -651,6 +717,25 @@ __device__ __forceinline__ void arrive_unstored(const StreamArgs& p, const volat
     }
 }
 
+// A whole unit's accumulator to C, through an epilogue. kRun: tokens a lane stores at a time where C's (and the
+// residual's) rows are not aligned to 16 bytes. Whether all went well.
+template <int kEpi, int kRun>
+__device__ __forceinline__ bool store_tile_epi(const WithEpilogue<StreamArgs>& p, const Walk& u, int nt, uint32_t acc, int half,
+                                               int warp, int lane, uint8_t* stage, EpilogueRing<kEpi>& ring) {
+    const int n0 = nt * kTileN + (warp & 3) * 32;
+    const int64_t bias0 = kEpi == kEpiGated ? static_cast<int64_t>(u.group) * 2 * p.epi.features : 0;
+    if (p.c_wide) {
+        const TokenShare share = token_share(u.rows, half);
+        if constexpr (kEpi == kEpiLinear) return ring.store(p, acc, share, u.row0, n0);
+        else store_tile_gated(p, acc, share, u.row0, n0, bias0, lane, stage);
+    } else {
+        LaneStore<kEpi, kRun> run;
+        run.load_first(p.epi, bias0, p.N, n0 + lane, u.row0, u.rows, half * kRun);
+        run.store(p.epi, p.N, n0 + lane, u.row0, u.rows, half * kRun, 2 * kRun, acc, 1, 0u, p.c, p.ldc);
+    }
+    return true;
+}
+
 // A CTA's share of a unit from its accumulator (at acc in this warp's quarter of the lanes) to C:
 // the eight epilogue warps (warps 4 .. 11) call. Weight tile nt, 128 rows.
 // A whole unit goes straight out. Of a unit split between CTAs (or pairs), each but the last to
@@ -661,7 +746,8 @@ __device__ __forceinline__ void arrive_unstored(const StreamArgs& p, const volat
 // joint one (arrive_unstored makes up for the arrivals). Returns whether the warp is still live.
 template <int kTermsPer, bool kPair, int kEpi>
 __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>& p, const Walk& u, int nt, uint32_t acc, int half, int warp,
-                                           int lane, volatile uint32_t* last_flag, uint8_t* stage, bool live) {
+                                           int lane, volatile uint32_t* last_flag, uint8_t* stage, bool live,
+                                           EpilogueRing<kEpi>& ring) {
     constexpr int kTok = 16 / kTermsPer;         // tokens per 16 columns
     constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
     // The pair kernel has no registers for two: it spilled 136 bytes then, and 16384 rows took 218 us, not 210.
@@ -669,12 +755,11 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
     const bool split = u.nk != p.k_atoms;
     if (!split && !live) return false;
     if (kTermsPer == 1 && u.nk == p.k_atoms) {
-        const int n0 = nt * kTileN + (warp & 3) * 32;
         if constexpr (kEpi != kEpiPlain) {
-            const int64_t bias0 = static_cast<int64_t>(u.group) * 2 * p.epi.features;
-            if (p.c_wide) store_tile_epi<kEpi, true>(p, acc, u.rows, u.row0, n0, bias0, half, lane, stage);
-            else store_tile_epi<kEpi, false>(p, acc, u.rows, u.row0, n0, bias0, half, lane, stage);
-        } else if (p.c_wide) store_tile<true>(p, acc, u.rows, u.row0, n0, half, lane, stage);
+            return store_tile_epi<kEpi, kPair ? 8 : 16>(p, u, nt, acc, half, warp, lane, stage, ring);   // registers, as for kFlight
+        }
+        const int n0 = nt * kTileN + (warp & 3) * 32;
+        if (p.c_wide) store_tile<true>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         else store_tile<false>(p, acc, u.rows, u.row0, n0, half, lane, stage);
         return true;
     }
@@ -698,6 +783,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
         unsigned long long* counter = counter_of<kPair>(p, shared);
         if (threadIdx.x == 128)
             flag[0] = *reinterpret_cast<volatile unsigned long long*>(counter) == (p.tag << 8 | others) ? 1u : 0u;
+        if constexpr (kEpi != kEpiPlain) __syncwarp();
         if (named_barrier_any(2, kStreamEpiThreads, !live)) {
             if (threadIdx.x == 128) {
                 flag[1] = static_cast<uint32_t>(counter - p.counters);
@@ -710,6 +796,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
             float* mine = p.partial + (static_cast<size_t>(me * kRanks + rank) * 2 + slot) * slot_floats;
             for (int cb = half * 16; cb < u.rows; cb += 32) {
                 float v[kTok];
+                if constexpr (kEpi != kEpiPlain) __syncwarp();
                 load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
                 const int m0 = cb / kTermsPer;
 #pragma unroll
@@ -719,6 +806,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
             unsigned long long seen = 0ull;
             if (threadIdx.x == 128) seen = *reinterpret_cast<volatile unsigned long long*>(counter);
             __threadfence();
+            if constexpr (kEpi != kEpiPlain) __syncwarp();   // the barriers too take whole warps
             named_barrier(2, kStreamEpiThreads);
             if (threadIdx.x == 128) {
                 const unsigned long long was = arrive(counter, seen, p.tag, false);
@@ -726,6 +814,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
                 flag[1] = all && clean ? 1u : 0u;
                 if (all && !clean) *counter = 0ull;
             }
+            if constexpr (kEpi != kEpiPlain) __syncwarp();
             named_barrier(2, kStreamEpiThreads);
             last = flag[1] != 0u;
         }
@@ -733,9 +822,16 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
         if (last && threadIdx.x == 128) *counter = 0ull;   // as found by a replay of this launch
     }
     if (!last) return true;
+    [[maybe_unused]] GatedBias b2;
+    if constexpr (kEpi == kEpiGated) b2 = load_gated_bias(p.epi, static_cast<int64_t>(u.group) * 2 * p.epi.features, gated_feature(n));
     for (int cb = half * 16; cb < u.rows; cb += 32) {
         float own[kTok], v[kTok];
         const int m0 = cb / kTermsPer;
+        [[maybe_unused]] TokenRun<kTok> run;
+        if constexpr (kEpi == kEpiLinear && !kPair) load_run(p.epi, p.N, n, row0 + m0, tokens - m0, run);
+        // Thread 128 has just cleared the counter, lanes past N have skipped loads: reads of tensor memory take the whole
+        // warp, and whole.
+        if constexpr (kEpi != kEpiPlain) __syncwarp();
         load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), own);
         if (!split) {
 #pragma unroll
@@ -766,12 +862,10 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
             }
         }
         if constexpr (kEpi == kEpiLinear) {
-            uint16_t res[kTok];
-            residual_run(p.epi, p.N, n, row0 + m0, min(kTok, tokens - m0), res);
-            store_run(p.epi, p.N, n, row0 + m0, min(kTok, tokens - m0), v, res, p.c, p.ldc);
+            if (kPair) load_run(p.epi, p.N, n, row0 + m0, tokens - m0, run);   // no registers for it before
+            store_run(p.epi, p.N, n, row0 + m0, min(kTok, tokens - m0), v, run, p.c, p.ldc);
         } else if constexpr (kEpi == kEpiGated) {
-            store_run_gated(p.epi, static_cast<int64_t>(u.group) * 2 * p.epi.features, n, row0 + m0,
-                            min(kTok, tokens - m0), v, p.c, p.ldc);
+            store_run_gated(p.epi, b2, n, row0 + m0, min(kTok, tokens - m0), v, p.c, p.ldc);
         } else if (n < p.N) {
             uint16_t* cp = p.c + (row0 + m0) * p.ldc + n;
 #pragma unroll

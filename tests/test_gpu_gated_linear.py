@@ -21,7 +21,7 @@ SHAPES = [
     (37, 66, 2128), (36, 130, 1304), (5, 33, 16456), (84, 50, 9976), (51, 67, 1696), (39, 34, 776), (33, 2513, 4664),
     (33, 98, 1072), (64, 3584, 2048), (200, 2048, 512), (256, 500, 7168), (600, 130, 1000), (1024, 256, 600),
     (33, 10036, 8), (34, 10234, 312), (1, 10114, 2248), (19, 9967, 1056), (535, 3243, 8), (700, 3650, 1544), (2048, 2080, 2040),
-    (3000, 550, 4096), (1500, 2052, 1536),
+    (3000, 550, 4096), (1500, 2052, 1536), (2900, 1024, 4096), (1500, 2056, 7168),
 ]
 
 

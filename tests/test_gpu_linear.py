@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from block_scaled_mxfp4_bf16_gb300 import workloads
-from linear_testlib import ACTS, act64, linear
+from linear_testlib import ACT_EPS, ACTS, TINY, act64, linear
 from moe_testlib import assert_within, canary_out, outside_untouched, quantized, strided, weights
 
 pytestmark = pytest.mark.gpu
@@ -20,7 +20,7 @@ SHAPES = [
     (37, 130, 2128), (36, 260, 1304), (5, 66, 16456), (84, 100, 9976), (51, 132, 1696), (39, 68, 776), (33, 5025, 4664),
     (33, 196, 1072), (64, 7168, 2048), (200, 4096, 512), (256, 1000, 7168), (600, 260, 1000), (1024, 512, 600),
     (33, 20071, 8), (34, 20468, 312), (1, 20228, 2248), (19, 19933, 1056), (535, 6485, 8), (700, 7300, 1544), (2048, 4160, 2040),
-    (3000, 1100, 4096), (1500, 4104, 1536),
+    (3000, 1100, 4096), (1500, 4104, 1536), (2900, 2048, 4096), (1500, 4104, 7168), (4000, 4096, 5000),
 ]
 
 
@@ -141,7 +141,7 @@ def test_tails_of_the_activations():
     for act in ACTS:
         out = mx.mxfp4_linear(x, packed[0], N, bias=z, activation=act)[0]
         want = act64(act, z.double())
-        assert_within(out[None], want[None], (want.abs() * 2.0 ** -15 + 2.0 ** -120)[None], act)
+        assert_within(out[None], want[None], (want.abs() * ACT_EPS + TINY)[None], act)
 
 
 @pytest.mark.parametrize("M,N,K", [(4, 300, 1040), (700, 7300, 1544)])

@@ -187,6 +187,24 @@ int main() {
         }
         if ((int)seen.size() != 2 * I || gated_rows(I) % 16) return 3;
     }
+    // stages of the pair kernel: the scale warps of set n % 2 wait for fill n / stages of stage n % stages by its parity
+    // alone, having waited for step n - 2 - kPairSfSlots to be over at step n - 2; fills land in any order. Whatever fill
+    // of the stage is the last to have landed then, it must not be taken for this one.
+    for (int fit = 2; fit <= kStreamMaxStages; ++fit) {
+        const int stages = pair_stages(fit);
+        if (stages > fit || stages < fit - 1 || stages < 2) return 5;
+        for (int n = 0; n < 200; ++n) {
+            const int fill = n / stages, stage = n % stages, over = n - 2 - kPairSfSlots;
+            // the set itself has seen every fill of the stage that was its own; others' are sure only if they are over
+            int landed = 0;
+            for (int f = 0; f < fill; ++f) {
+                const int step = f * stages + stage;
+                if (step <= over || step % 2 == n % 2) landed = f + 1;
+            }
+            if (landed < fill) return 6;          // with one fill less landed, the parity is that of a fill that is in
+        }
+    }
+    if (pair_stages(5) != 4 || pair_stages(7) != 7 || pair_stages(6) != 6) return 7;
     // equal token tiles: the tiling of M by their own size is the same again
     for (int M = 1; M <= 20000; ++M) {
         int t = tile_rows(M, 192), n = 0;
