@@ -1,12 +1,15 @@
 """The products with an epilogue: mxfp4_linear (bias, activation, residual), mxfp4_gated_linear (two projections,
 the activation and the product of a gated feed-forward block) and its form for experts' groups of rows. As in the
-rest of the binding, the functions only check and marshal arguments; every step runs in the library's CUDA kernels."""
+rest of the binding, the functions only check and marshal arguments; every step runs in the library's CUDA kernels.
+
+A call of a few tokens takes the GPU 2 to 5 us and the host 8: it reads every tensor property once, keeps the
+sizes that the library answers by shape, and leaves the reports of what is wrong to slower helpers."""
 from __future__ import annotations
 
 import torch
 
-from . import Mxfp4Error, _check, _check_packed, _dev, _on, _stream, _writing, load_library
-from .moe import _BF16, _F32, _begin, _bf16_rows, _index, _need, _out, _scratch
+from . import (Mxfp4Error, _check, _dev, _on, _raw_stream, _stream, _writing, load_library, mxfp4_prepack_b_size)
+from .moe import _BF16, _F32, _bf16_rows, _device, _empty_strided, _index, _need, _out, _scratch
 
 # the C ABI's activations
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -14,20 +17,42 @@ _BIAS_TYPES = {_F32: 0, _BF16: 1}
 
 
 def _activation(name) -> int:
-    act = ACTIVATIONS.get(name)
-    if act is None:
-        raise ValueError(f"activation must be one of {', '.join(str(n) for n in ACTIVATIONS)}")
-    return act
+    """For a name that ACTIVATIONS does not have."""
+    raise ValueError(f"activation must be one of {', '.join(str(n) for n in ACTIVATIONS)}, not {name!r}")
 
 
-def _bias(bias: torch.Tensor | None, shape: tuple, like: torch.Tensor) -> tuple:
+def _bias(bias: torch.Tensor, shape: tuple, like: torch.Tensor) -> tuple:
     """(pointer, C type) of a dense fp32 or bf16 bias."""
-    if bias is None:
-        return None, 0
     dtype = _BIAS_TYPES.get(bias.dtype)
     if dtype is None:
         raise ValueError("bias must be an fp32 or bf16 tensor")
     return _index(bias, shape, like, "bias", bias.dtype), dtype
+
+
+# (bytes of one group's packed weights, bytes of workspace) by function, device and sizes; both depend on these only
+_SIZES: dict = {}
+
+
+def _sizes(key: tuple) -> tuple:
+    query, packed_size, device, *sizes = key
+    known = (packed_size(*sizes[-2:]), _need(query, device, *sizes))
+    if known[0]:
+        _SIZES[key] = known
+    return known
+
+
+def _too_small(name: str, what: str, need: int) -> None:
+    raise ValueError(f"{name} must be a CUDA buffer of at least {what} = {need} bytes on the device of the other operands")
+
+
+def _rows_and_stride(t: torch.Tensor, name: str) -> tuple:
+    """(rows, columns, row stride) of a bf16 matrix whose columns lie next to each other."""
+    if t.dtype is _BF16 and t.is_contiguous():
+        shape = t.shape
+        if len(shape) == 2:
+            return *shape, shape[1]
+    ld = _bf16_rows(t, name)
+    return *t.shape, ld
 
 
 def mxfp4_linear(x: torch.Tensor, packed_b: torch.Tensor, N: int, bias: torch.Tensor | None = None,
@@ -36,23 +61,38 @@ def mxfp4_linear(x: torch.Tensor, packed_b: torch.Tensor, N: int, bias: torch.Te
     """out [M, N] bf16 = act(MXFP4(x) . MXFP4(B)^T + bias) + residual, rounded once: mxfp4_gemm with what follows it.
     `packed_b`: mxfp4_prepack_b's; `bias` [N] fp32 or bf16; `activation`: none, relu, silu, gelu (by the normal
     distribution function) or gelu_tanh; `residual` [M, N] bf16 with any row stride, which `out` may be itself."""
-    st, device = _begin(x, "x", stream)
-    ldx = _bf16_rows(x, "x")
-    M, K = x.shape
-    act = _activation(activation)
+    device = x.get_device()
+    if device < 0 or device != _device():
+        _dev(x, "x")
+    st = _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+    M, K, ldx = _rows_and_stride(x, "x")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        _activation(activation)
     need = 0
     if M and N:
-        _check_packed(packed_b, N, K, x.device)
-        need = _need("mxfp4_linear_workspace_size", device, M, N, K)
-    bias_ptr, bias_type = _bias(bias, (N,), x)
+        key = ("mxfp4_linear_workspace_size", mxfp4_prepack_b_size, device, M, N, K)
+        known = _SIZES.get(key) or _sizes(key)
+        need = known[1]
+        if not known[0] or packed_b.nbytes < known[0] or packed_b.get_device() != device:
+            _too_small("packed_b", f"mxfp4_prepack_b_size({N}, {K})", known[0])
+    bias_ptr, bias_type = (None, 0) if bias is None else _bias(bias, (N,), x)
     res_ptr, ldr = None, 0
     if residual is not None:
-        _on(residual, x.device, "residual")
-        if tuple(residual.shape) != (M, N):
+        if residual.get_device() != device:
+            _on(residual, x.device, "residual")
+        rows, cols, ldr = _rows_and_stride(residual, "residual")
+        if rows != M or cols != N:
             raise ValueError(f"residual must be a [{M}, {N}] tensor")
-        res_ptr, ldr = residual.data_ptr(), _bf16_rows(residual, "residual")
-    out, ldo = _out(out, (M, N), x, "out", stream)
-    ws, ws_bytes, _held = _scratch(workspace, need, x, stream, st, device)
+        res_ptr = residual.data_ptr()
+    if out is None and stream is None and _empty_strided is not None:
+        out, ldo = _empty_strided((M, N), (N, 1), _BF16), N
+    else:
+        out, ldo = _out(out, (M, N), x, "out", stream)
+    if need or workspace is not None:
+        ws, ws_bytes, _held = _scratch(workspace, need, x, stream, st, device)
+    else:
+        ws, ws_bytes = None, 0
     status = load_library().mxfp4_linear(x.data_ptr(), M, K, ldx, packed_b.data_ptr(), N, bias_ptr, bias_type, act,
                                          res_ptr, ldr, out.data_ptr(), ldo, ws, ws_bytes, st)
     if status:
@@ -118,36 +158,36 @@ def mxfp4_prepack_gated_experts(bq: torch.Tensor, bs: torch.Tensor, stream=None)
     return packed
 
 
-_GATED_NEED: dict = {}
-
-
-def _check_gated(packed_gu: torch.Tensor, groups: int, I: int, K: int, device: torch.device) -> None:
-    """The packed weights must be as large as the kernel's reads of them."""
-    need = _GATED_NEED.get((I, K))
-    if need is None:
-        need = _GATED_NEED[(I, K)] = mxfp4_prepack_gated_size(I, K)
-    if need == 0 or packed_gu.nbytes < groups * need or not packed_gu.is_cuda or packed_gu.device != device:
-        raise ValueError(f"packed_gu must be a CUDA buffer of at least {groups} * mxfp4_prepack_gated_size({I}, {K}) = "
-                         f"{groups * need} bytes on the device of the other operands")
-
-
 def mxfp4_gated_linear(x: torch.Tensor, packed_gu: torch.Tensor, I: int, bias: torch.Tensor | None = None,
                        activation: str | None = "silu", out: torch.Tensor | None = None,
                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out [M, I] bf16 = act(MXFP4(x) . Wg^T + bias[:I]) * (MXFP4(x) . Wu^T + bias[I:]), rounded once: the first half
     of a gated feed-forward block in one product. `packed_gu`: mxfp4_prepack_gated's; `bias` [2I] fp32 or bf16;
     `activation` as for mxfp4_linear."""
-    st, device = _begin(x, "x", stream)
-    ldx = _bf16_rows(x, "x")
-    M, K = x.shape
-    act = _activation(activation)
+    device = x.get_device()
+    if device < 0 or device != _device():
+        _dev(x, "x")
+    st = _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+    M, K, ldx = _rows_and_stride(x, "x")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        _activation(activation)
     need = 0
     if M and I:
-        _check_gated(packed_gu, 1, I, K, x.device)
-        need = _need("mxfp4_gated_linear_workspace_size", device, M, I, K)
-    bias_ptr, bias_type = _bias(bias, (2 * I,), x)
-    out, ldo = _out(out, (M, I), x, "out", stream)
-    ws, ws_bytes, _held = _scratch(workspace, need, x, stream, st, device)
+        key = ("mxfp4_gated_linear_workspace_size", mxfp4_prepack_gated_size, device, M, I, K)
+        known = _SIZES.get(key) or _sizes(key)
+        need = known[1]
+        if not known[0] or packed_gu.nbytes < known[0] or packed_gu.get_device() != device:
+            _too_small("packed_gu", f"mxfp4_prepack_gated_size({I}, {K})", known[0])
+    bias_ptr, bias_type = (None, 0) if bias is None else _bias(bias, (2 * I,), x)
+    if out is None and stream is None and _empty_strided is not None:
+        out, ldo = _empty_strided((M, I), (I, 1), _BF16), I
+    else:
+        out, ldo = _out(out, (M, I), x, "out", stream)
+    if need or workspace is not None:
+        ws, ws_bytes, _held = _scratch(workspace, need, x, stream, st, device)
+    else:
+        ws, ws_bytes = None, 0
     status = load_library().mxfp4_gated_linear(x.data_ptr(), M, K, ldx, packed_gu.data_ptr(), I, bias_ptr, bias_type,
                                                act, out.data_ptr(), ldo, ws, ws_bytes, st)
     if status:
@@ -163,26 +203,35 @@ def mxfp4_grouped_gated_linear(a: torch.Tensor, packed_gu: torch.Tensor, offsets
     `bias` [E, 2I]) of the expert e with offsets[e] <= r < offsets[e+1]. `packed_gu`: mxfp4_prepack_gated_experts';
     `offsets` [E+1] and `rows` [R]: int32 on the device, as mxfp4_moe_route returns them (rows None: row r of `a`).
     Rows of out that belong to no expert are not written."""
-    st, device = _begin(a, "a", stream)
-    lda = _bf16_rows(a, "a")
-    tokens, K = a.shape
-    act = _activation(activation)
+    device = a.get_device()
+    if device < 0 or device != _device():
+        _dev(a, "a")
+    st = _raw_stream(device) if stream is None and _raw_stream is not None else _stream(stream)
+    tokens, K, lda = _rows_and_stride(a, "a")
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        _activation(activation)
     if packed_gu.dim() != 2 or not packed_gu.is_contiguous():
         raise ValueError("packed_gu must be a contiguous [E, bytes] buffer (mxfp4_prepack_gated_experts)")
     E = packed_gu.shape[0]
-    if E and I:
-        _check_gated(packed_gu, E, I, K, a.device)
-        if packed_gu.nbytes != E * _GATED_NEED[(I, K)]:
-            raise ValueError(f"packed_gu's rows must have mxfp4_prepack_gated_size({I}, {K}) bytes")
     offsets_ptr = _index(offsets, (E + 1,), a, "offsets")
     if rows is None:
         R, rows_ptr = tokens, None
     else:
         R = rows.shape[0] if rows.dim() == 1 else -1
         rows_ptr = _index(rows, (R,), a, "rows")
-    bias_ptr, bias_type = _bias(bias, (E, 2 * I), a)
-    out, ldo = _out(out, (R, I), a, "out", stream)
-    need = _need("mxfp4_grouped_gated_linear_workspace_size", device, R, E, I, K) if R and E and I else 0
+    need = 0
+    if R and E and I:
+        key = ("mxfp4_grouped_gated_linear_workspace_size", mxfp4_prepack_gated_size, device, R, E, I, K)
+        known = _SIZES.get(key) or _sizes(key)
+        need = known[1]
+        if not known[0] or packed_gu.nbytes != E * known[0] or packed_gu.get_device() != device:
+            _too_small("packed_gu", f"and exactly {E} * mxfp4_prepack_gated_size({I}, {K})", E * known[0])
+    bias_ptr, bias_type = (None, 0) if bias is None else _bias(bias, (E, 2 * I), a)
+    if out is None and stream is None and _empty_strided is not None:
+        out, ldo = _empty_strided((R, I), (I, 1), _BF16), I
+    else:
+        out, ldo = _out(out, (R, I), a, "out", stream)
     ws, ws_bytes, _held = _scratch(workspace, need, a, stream, st, device)
     status = load_library().mxfp4_grouped_gated_linear(a.data_ptr(), tokens, K, lda, rows_ptr, offsets_ptr, E,
                                                        packed_gu.data_ptr(), I, bias_ptr, bias_type, act,

@@ -88,6 +88,7 @@ def lib(monkeypatch):
         monkeypatch.setattr(module, "load_library", lambda: fake)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)   # a CPU tensor's get_device()
     monkeypatch.setattr(moe, "_NEED", {})
+    monkeypatch.setattr(linear, "_SIZES", {})
     return fake
 
 
