@@ -16,14 +16,6 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 bool sizes_ok(int64_t N, int64_t K) { return N >= 1 && N <= kMaxSize && K >= 1 && K % 8 == 0 && K <= (int64_t(1) << 30); }
 bool gated_sizes_ok(int64_t I, int64_t K) { return I >= 1 && I <= kMaxSize / 2 && sizes_ok(gated_rows(I), K); }
 
-// Tokens per tile of M tokens in equal tiles of at most `most`: the value that the streaming product's own tiling of M
-// by it gives again.
-int equal_tiles(int64_t M, int most) {
-    int m_tile = tile_rows(static_cast<int>(M), most);
-    while (tile_rows(static_cast<int>(M), m_tile) != m_tile) m_tile = tile_rows(static_cast<int>(M), m_tile);
-    return m_tile;
-}
-
 // How a dense product runs: on the GEMM's own plan, or as one group of the streaming product.
 struct DensePlan {
     bool streams;
@@ -32,28 +24,30 @@ struct DensePlan {
     size_t ws_bytes;
 };
 
-int dense_plan(const DeviceInfo& di, int64_t M, int64_t N, int64_t K, int kind, DensePlan* out) {
+int dense_plan(const DeviceInfo& di, int64_t M, int64_t N, int64_t K, int columns, int kind, DensePlan* out) {
     DensePlan p = {};
     const int st = cached_linear_plan(di, M, N, K, kind == kEpiGated ? 16 : 1, &p.gemm);
     if (st != MXFP4_OK) return st;
     p.ws_bytes = p.gemm.ws_total;
-    if (p.gemm.path == 2 && p.gemm.ctas > di.sm_count && M <= kMaxRows &&
-        make_stream_plan(M, 1, N, K, 1, di.sm_count, stream_clusters, &p.stream, equal_tiles(M, 192), kind) == 0) {
-        p.streams = true;
-        p.ws_bytes = p.stream.ws_total;
+    if (p.gemm.path == 2) {
+        const DenseChoice c = choose_dense(M, N, K, columns, p.gemm.ctas, p.gemm.splits, p.gemm.m_tile, di.sm_count);
+        if (c.streams && make_stream_plan(M, 1, N, K, 1, di.sm_count, stream_clusters, &p.stream, kind, c.m_tile, c.pair) == 0) {
+            p.streams = true;
+            p.ws_bytes = p.stream.ws_total;
+        }
     }
     *out = p;
     return MXFP4_OK;
 }
 
-// The operands of a call. N: weight rows; columns: of the output.
+// The operands of a call. N: weight rows.
 int run_dense(const void* x, int64_t M, int64_t K, int64_t ldx, const void* packed_b, int64_t N, int kind,
               const Epilogue& epi, void* out, int64_t ldo, void* workspace, size_t ws_bytes, void* stream) {
     DeviceInfo di;
     int st = device_info(&di);
     if (st != MXFP4_OK) return st;
     DensePlan plan;
-    st = dense_plan(di, M, N, K, kind, &plan);
+    st = dense_plan(di, M, N, K, kind == kEpiGated ? epi.features : static_cast<int>(N), kind, &plan);
     if (st != MXFP4_OK) return st;
     if (plan.ws_bytes) {
         if (!workspace || ws_bytes < plan.ws_bytes) return MXFP4_ERR_WORKSPACE;
@@ -77,9 +71,10 @@ int run_dense(const void* x, int64_t M, int64_t K, int64_t ldx, const void* pack
     a.K = K;
     a.groups = 1;
     a.rows = static_cast<int>(M);
-    // (a tensor map's rows are less than 2^40 bytes apart)
+    // The linear epilogue stores by tensor copies: rows less than 2^40 bytes apart, and whole 16-byte pieces, since a copy
+    // cuts a row at its end to those only (132 columns in rows of 136: all 136 were written).
     auto wide = [](const void* m, int64_t ld) { return aligned(m, 16) && ld % 8 == 0 && ld < int64_t(1) << 39; };
-    a.c_wide = wide(out, ldo) && (!epi.residual || wide(epi.residual, epi.ldr)) ? 1 : 0;
+    a.c_wide = wide(out, ldo) && (kind == kEpiGated || N % 8 == 0) && (!epi.residual || wide(epi.residual, epi.ldr)) ? 1 : 0;
     a.epi = epi;
 #ifdef MXFP4_TEST_HOOKS
     a.test_give_up = {-1, 0, 0};
@@ -106,7 +101,7 @@ size_t mxfp4_linear_workspace_size(int64_t M, int64_t N, int64_t K) {
     DeviceInfo di;
     DensePlan plan;
     if (M < 1 || M > kMaxSize || !sizes_ok(N, K) || device_info(&di) != MXFP4_OK) return 0;
-    return dense_plan(di, M, N, K, kEpiLinear, &plan) == MXFP4_OK ? plan.ws_bytes : 0;
+    return dense_plan(di, M, N, K, static_cast<int>(N), kEpiLinear, &plan) == MXFP4_OK ? plan.ws_bytes : 0;
 }
 
 int mxfp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx, const void* packed_b, int64_t N, const void* bias,
@@ -150,7 +145,7 @@ size_t mxfp4_gated_linear_workspace_size(int64_t M, int64_t I, int64_t K) {
     DeviceInfo di;
     DensePlan plan;
     if (M < 1 || M > kMaxSize || !gated_sizes_ok(I, K) || device_info(&di) != MXFP4_OK) return 0;
-    return dense_plan(di, M, gated_rows(I), K, kEpiGated, &plan) == MXFP4_OK ? plan.ws_bytes : 0;
+    return dense_plan(di, M, gated_rows(I), K, static_cast<int>(I), kEpiGated, &plan) == MXFP4_OK ? plan.ws_bytes : 0;
 }
 
 int mxfp4_gated_linear(const void* x, int64_t M, int64_t K, int64_t ldx, const void* packed_gu, int64_t I,

@@ -635,7 +635,7 @@ mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p, const __grid_constan
 // ------------------------------------------------------------------------ plan and launches
 
 int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count,
-                     int (*clusters_of)(int), StreamPlan* out, int m_tile, int epi) {
+                     int (*clusters_of)(int), StreamPlan* out, int epi, int m_tile, bool pair) {
     StreamPlan p = {};
     p.k_atoms = static_cast<int>((K + kAtomK - 1) / kAtomK);
     p.n_tiles = static_cast<int>((N + kTileN - 1) / kTileN);
@@ -672,6 +672,7 @@ int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int ter
     // 2048 62.8 against 62.6.
     constexpr int kPairSteps = 6;
     p.pair = terms == 1 && p.m_tile > 128 && p.n_tiles > 1 && p.k_atoms >= kPairSteps;
+    if (m_tile) p.pair = pair;
     p.nmc = (p.m_tile + 127) / 128;
     p.a_block = static_cast<uint32_t>(p.m_tile) * 128u + static_cast<uint32_t>(p.nmc) * 2u * kSfChunk;
     size_t extra = 1024 + (2 * kStreamMaxStages + 4) * 8 + 32 + 64 + epi_stage_bytes(epi) +

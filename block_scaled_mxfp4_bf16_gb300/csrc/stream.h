@@ -98,6 +98,70 @@ __host__ __device__ inline unsigned long long arrival_add(unsigned long long wor
 __host__ __device__ inline bool arrival_last(unsigned long long word, uint32_t others) { return (word & 0x7Full) == others; }
 __host__ __device__ inline bool arrival_clean(unsigned long long word) { return (word & kArrivalMark) == 0ull; }
 
+// ---- how a dense product with an epilogue runs: the choice between the GEMM's plan and one group of the streaming
+// product, and the latter's token tiles, by a model of the time that follows the operands' token blocks, in us.
+// A 256-K step takes as long as its bytes take into an SM (17 KB of weights, the CTA's token rows and their scales), 113 KB
+// a us, 120 of them a CTA working alone; a unit takes its steps or its epilogue, 3 us for 128 x 192 sums, whichever is more,
+// and 1.1 us; what is left after whole waves of units is cut along K where the walk does so (begin_walk), which
+// costs 9 us of sums through the workspace. Over 166 shapes (M 77 to 8192, N 1000 to 28672, K 1024 to 7168), every plan measured,
+// the one picked took 1.4 % more than the best (geometric mean; the largest equal tiles in pairs, and the GEMM wherever its CTAs
+// make one wave: 7.2 % more, 49 % at worst): 2048 x 14336 x 4096 gated 44.3 us in tiles of 176 against 50.6 of 192,
+// 1500 x 4096 x 7168 25.5 of 176 against 35.2 of 192, 300 x 14336 x 4096 gated 18.6 of 80 against 22.2 of 160.
+struct DenseChoice {
+    bool streams;
+    int m_tile;
+    bool pair;
+};
+inline double step_bytes(int token_bytes, int m_tile) { return 17408.0 + token_bytes + 1024.0 * ((m_tile + 127) / 128); }
+inline double stream_cost(int64_t M, int64_t N, int64_t K, int columns, int m_tile, bool pair, int sm_count) {
+    const int64_t k = (K + 255) / 256, n_tiles = (N + 127) / 128, tiles = (M + m_tile - 1) / m_tile;
+    const int64_t walkers = pair ? sm_count / 2 : sm_count, units = tiles * (pair ? (n_tiles + 1) / 2 : n_tiles);
+    const double step = pair ? step_bytes(static_cast<int>(pair_code_bytes(m_tile)), m_tile) / 113e3
+                             : step_bytes(m_tile * 128, m_tile) / 120e3;
+    const double epilogue = 3.0 * m_tile / 192, whole = k * step, unit = (whole > epilogue ? whole : epilogue) + 1.1;
+    // a pair's second CTA to wait for; rows that start off 16 bytes are stored element by element, with few registers
+    const double fixed = 2.0 + epilogue + (pair ? (columns % 8 ? 3.0 : 1.0) : 0.0);
+    const int64_t waves = units / walkers, rest = units - waves * walkers;
+    const int64_t even = (rest * k + walkers - 1) / walkers;
+    int64_t share = split_share(even, static_cast<int>(k));
+    if (rest == 0) return waves * unit + fixed;
+    const int64_t apart = share + kSplitSteps < k ? share + kSplitSteps : k;
+    if (waves > 0 && even + kMergeSteps < apart) {
+        share = ((rest + walkers) * k + walkers - 1) / walkers;
+        return (waves - 1) * unit + share * step + 9.0 + fixed;
+    }
+    return share >= k ? (waves + 1) * unit + fixed : waves * unit + share * step + 9.0 + fixed;
+}
+// The GEMM's plan in one wave of CTAs: a split tile's sums go through shared memory, which is cheap up to 128 tokens.
+inline double gemm_cost(int64_t K, int splits, int m_tile) {
+    const int64_t k = (K + 255) / 256, steps = (k + splits - 1) / splits;
+    const double end = splits == 1 ? 3.0 * m_tile / 192 : m_tile <= 128 ? 1.5 : 8.0;
+    return steps * step_bytes(m_tile * 128, m_tile) / 120e3 + 1.1 + end;
+}
+// gemm_*: the GEMM's plan on token blocks. N: weight rows; columns: of the output.
+inline DenseChoice choose_dense(int64_t M, int64_t N, int64_t K, int columns, int64_t gemm_ctas, int gemm_splits,
+                                int gemm_m_tile, int sm_count) {
+    DenseChoice best = {false, 0, false};
+    double least = gemm_ctas <= sm_count ? gemm_cost(K, gemm_splits, gemm_m_tile) : 1e30;
+    if (M > int64_t(1) << 30) return best;
+    // equal tiles whose own size tiles M the same way; smaller ones than 64 tokens only where M is
+    int tried = 0;
+    for (int64_t t = (M + 191) / 192; tried < 12; ++t, ++tried) {
+        const int m_tile = static_cast<int>(((M + t - 1) / t + 15) / 16 * 16);
+        if (m_tile < 64 && t > 1) break;
+        if (tile_rows(static_cast<int>(M), m_tile) != m_tile) continue;
+        // pairs from 12 steps on: 2048 x 7168 x 2048 22.2 us alone and 23.7 in pairs, 2048 x 14336 x 4096 51.1 and 44.3
+        for (int pair = 0; pair <= (K > 11 * 256 && N > 128 ? 1 : 0); ++pair) {
+            const double cost = stream_cost(M, N, K, columns, m_tile, pair != 0, sm_count);
+            if (cost < least) {
+                least = cost;
+                best = {true, m_tile, pair != 0};
+            }
+        }
+    }
+    return best;
+}
+
 struct StreamArgs {
     const uint8_t* tblk;      // token blocks [tile slot][k_atoms][a_block]
     const uint8_t* wblk;      // packed weights, group_bytes from one group to the next
@@ -145,9 +209,10 @@ int stream_clusters(int size);
 
 // Plan for `rows` token-block rows in `groups` groups; terms: 1 (grouped) or kTerms; clusters_of:
 // stream_clusters, or a model of it.
-// m_tile: tokens per tile (a multiple of 16, up to 192) where the caller has chosen them, or 0; epi: the epilogue.
+// m_tile: tokens per tile (a multiple of 16, up to 192) and pair: whether CTAs work in pairs, where the caller has
+// chosen them, or 0; epi: the epilogue.
 int make_stream_plan(int64_t rows, int64_t groups, int64_t N, int64_t K, int terms, int sm_count,
-                     int (*clusters_of)(int), StreamPlan* plan, int m_tile = 0, int epi = kEpiPlain);
+                     int (*clusters_of)(int), StreamPlan* plan, int epi = kEpiPlain, int m_tile = 0, bool pair = false);
 // The driver's encoder of tensor maps, looked up once (the library does not link the driver); null if there is none.
 using TensorMapEncoder = decltype(&cuTensorMapEncodeTiled);
 TensorMapEncoder tensor_map_encoder();

@@ -22,6 +22,7 @@ SHAPES = [
     (33, 98, 1072), (64, 3584, 2048), (200, 2048, 512), (256, 500, 7168), (600, 130, 1000), (1024, 256, 600),
     (33, 10036, 8), (34, 10234, 312), (1, 10114, 2248), (19, 9967, 1056), (535, 3243, 8), (700, 3650, 1544), (2048, 2080, 2040),
     (3000, 550, 4096), (1500, 2052, 1536), (2900, 1024, 4096), (1500, 2056, 7168),
+    (530, 1056, 7168), (600, 1440, 4096), (300, 4096, 4096), (512, 4100, 3584), (430, 4501, 3080), (768, 750, 3000), (150, 7168, 4096),
 ]
 
 

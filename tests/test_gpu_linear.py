@@ -21,6 +21,8 @@ SHAPES = [
     (33, 196, 1072), (64, 7168, 2048), (200, 4096, 512), (256, 1000, 7168), (600, 260, 1000), (1024, 512, 600),
     (33, 20071, 8), (34, 20468, 312), (1, 20228, 2248), (19, 19933, 1056), (535, 6485, 8), (700, 7300, 1544), (2048, 4160, 2040),
     (3000, 1100, 4096), (1500, 4104, 1536), (2900, 2048, 4096), (1500, 4104, 7168), (4000, 4096, 5000),
+    (530, 2112, 7168), (600, 2880, 4096), (300, 8192, 4096), (512, 8200, 3584), (430, 9000, 3080), (768, 1500, 3000), (150, 14336, 4096),
+    (1280, 4096, 4096),
 ]
 
 

@@ -168,7 +168,9 @@ def test_binding_prepack_gated(lib):
 
 
 HARNESS = r"""
+#include <cmath>
 #include <cstdio>
+#include <random>
 #include <set>
 #include "stream.h"
 using namespace mxfp4;
@@ -206,11 +208,20 @@ int main() {
         }
     }
     if (pair_stages(5) != 4 || pair_stages(7) != 7 || pair_stages(6) != 6) return 7;
-    // equal token tiles: the tiling of M by their own size is the same again
-    for (int M = 1; M <= 20000; ++M) {
-        int t = tile_rows(M, 192), n = 0;
-        while (tile_rows(M, t) != t && ++n < 10) t = tile_rows(M, t);
-        if (n == 10 || t > 192 || t % 16 || (tiles_of(M, t) - 1) * t >= M || tiles_of(M, t) * t < M) return 4;
+    // a dense product's token tiles: whole sixteens up to 192 that tile M the same way again, and cover it
+    std::mt19937 rng(1);
+    for (int i = 0; i < 200000; ++i) {
+        auto log_int = [&](double hi) { return (int64_t)std::exp2(std::generate_canonical<double, 53>(rng) * std::log2(hi)); };
+        const int64_t M = i < 5000 ? i + 1 : log_int(1 << 30), N = log_int(1 << 20), K = 8 * log_int(1 << 14);
+        const int splits = 1 + (int)(rng() % 5), m_tile = 16 * (1 + (int)(rng() % 16));
+        const DenseChoice c = choose_dense(M, N, K, (int)N, i % 3 ? 153 : 100, splits, m_tile, 152);
+        if (!c.streams) {
+            if (i % 3) return 4;      // the GEMM only where its CTAs make one wave
+            continue;
+        }
+        if (c.m_tile < 16 || c.m_tile > 192 || c.m_tile % 16 || tile_rows((int)M, c.m_tile) != c.m_tile) return 8;
+        const int64_t tiles = tiles_of((int)M, c.m_tile);
+        if ((tiles - 1) * c.m_tile >= M || tiles * c.m_tile < M || (c.pair && (N <= 128 || K <= 11 * 256))) return 9;
     }
     puts("ok");
     return 0;
