@@ -171,7 +171,10 @@ struct ResidentArgs {
 };
 
 // What happens to a product's sums before they are stored (epilogue.cuh).
-constexpr int kEpiPlain = 0, kEpiLinear = 1, kEpiGated = 2;
+// kEpiBias: linear without an activation, which the kernels of few tokens have instantiations of (their time goes into
+// fetching instructions, too: 1x4096x512 2.32 us with the activations' code in the kernel, 2.08 without).
+constexpr int kEpiPlain = 0, kEpiLinear = 1, kEpiGated = 2, kEpiBias = 3;
+constexpr bool linear_epilogue(int epi) { return epi == kEpiLinear || epi == kEpiBias; }
 constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3, kActGeluTanh = 4;
 struct Epilogue {
     const void* bias;          // bf16 or fp32, or null. Linear: [N]; gated: the gate's [features], then the up's

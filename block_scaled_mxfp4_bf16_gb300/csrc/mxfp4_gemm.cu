@@ -676,7 +676,7 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
         [[maybe_unused]] GatedBias b2[2];
         if constexpr (kEpi != kEpiPlain) {
             const int n4 = n0 + lane * 4, lm = warp - 3;
-            if constexpr (kEpi == kEpiLinear) {
+            if constexpr (linear_epilogue(kEpi)) {
                 if (owner) {
                     b4 = quad_bias(p.epi, p.N, n4);
 #pragma unroll
@@ -708,7 +708,7 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
             for (int lm0 = et >> 5; lm0 < nrows; lm0 += kRows * kEpiWarps) {
                 float4 acc[kRows];
                 [[maybe_unused]] uint2 now[kRows];
-                if constexpr (kEpi == kEpiLinear) {          // the next rows' residual while these are summed
+                if constexpr (linear_epilogue(kEpi)) {          // the next rows' residual while these are summed
 #pragma unroll
                     for (int u = 0; u < kRows; ++u) {
                         const int lm = lm0 + (kRows + u) * kEpiWarps;
@@ -742,8 +742,8 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
                 for (int u = 0; u < kRows; ++u) {
                     const int lm = lm0 + u * kEpiWarps;
                     if (lm >= nrows) break;
-                    if constexpr (kEpi == kEpiLinear) {
-                        store_quad(p.epi, p.N, n4, m0 + r0 + lm, acc[u], b4, now[u], p.c, p.ldc, p.c_vec4 != 0);
+                    if constexpr (linear_epilogue(kEpi)) {
+                        store_quad<kEpi>(p.epi, p.N, n4, m0 + r0 + lm, acc[u], b4, now[u], p.c, p.ldc, p.c_vec4 != 0);
                         continue;
                     } else if constexpr (kEpi == kEpiGated) {
                         store_quad_gated(p.epi, b2, n4, m0 + r0 + lm, acc[u], p.c, p.ldc, p.c_vec4 != 0);
@@ -822,7 +822,7 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
             [[maybe_unused]] GatedBias own2;
             if constexpr (kEpi != kEpiPlain) {
                 const int t = threadIdx.x - 96, row_n = n0 + (t & (kTileN - 1)), lm = t / kTileN * 4;
-                if constexpr (kEpi == kEpiLinear) load_run(p.epi, p.N, row_n, m0 + r0 + lm, r1 - r0 - lm, own);
+                if constexpr (linear_epilogue(kEpi)) load_run(p.epi, p.N, row_n, m0 + r0 + lm, r1 - r0 - lm, own);
                 else own2 = load_gated_bias(p.epi, 0, gated_feature(row_n));
             }
             bool got = mbar_wait_cluster(red_bar, 0, lim);
@@ -845,9 +845,9 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
                         acc.z += v.z;
                         acc.w += v.w;
                     }
-                    if constexpr (kEpi == kEpiLinear) {
+                    if constexpr (linear_epilogue(kEpi)) {
                         float sums[4] = {acc.x, acc.y, acc.z, acc.w};
-                        store_run(p.epi, p.N, nn, m0 + r0 + lm, min(4, nrows - lm), sums, own, p.c, p.ldc);
+                        store_run<kEpi>(p.epi, p.N, nn, m0 + r0 + lm, min(4, nrows - lm), sums, own, p.c, p.ldc);
                         lm += 4 * (kEpiThreads / kTileN);
                         if (lm < nrows) load_run(p.epi, p.N, nn, m0 + r0 + lm, nrows - lm, own);
                         lm -= 4 * (kEpiThreads / kTileN);
@@ -919,7 +919,7 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
         [[maybe_unused]] float4 b4;
         [[maybe_unused]] uint2 res;
         [[maybe_unused]] GatedBias b2[2];
-        if constexpr (kEpi == kEpiLinear) {
+        if constexpr (linear_epilogue(kEpi)) {
             b4 = quad_bias(p.epi, p.N, n4);
             if (p.epi.residual && (et >> 5) < nrows) res = quad_residual(p.epi, p.N, n4, m0 + r0 + (et >> 5), p.c_vec4 != 0);
         } else if constexpr (kEpi == kEpiGated) {
@@ -928,7 +928,7 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
         }
         for (int lm = et >> 5; lm < nrows; lm += kEpiWarps) {
             [[maybe_unused]] uint2 now;
-            if constexpr (kEpi == kEpiLinear) {      // the next row's residual while this one is summed
+            if constexpr (linear_epilogue(kEpi)) {      // the next row's residual while this one is summed
                 now = res;
                 if (p.epi.residual && lm + kEpiWarps < nrows)
                     res = quad_residual(p.epi, p.N, n4, m0 + r0 + lm + kEpiWarps, p.c_vec4 != 0);
@@ -941,8 +941,8 @@ mxfp4_gemm_kernel(const EpilogueArgs<GemmArgs, kEpi> p) {
                 acc.z += v.z;
                 acc.w += v.w;
             }
-            if constexpr (kEpi == kEpiLinear) {
-                store_quad(p.epi, p.N, n4, m0 + r0 + lm, acc, b4, now, p.c, p.ldc, p.c_vec4 != 0);
+            if constexpr (linear_epilogue(kEpi)) {
+                store_quad<kEpi>(p.epi, p.N, n4, m0 + r0 + lm, acc, b4, now, p.c, p.ldc, p.c_vec4 != 0);
                 continue;
             } else if constexpr (kEpi == kEpiGated) {
                 store_quad_gated(p.epi, b2, n4, m0 + r0 + lm, acc, p.c, p.ldc, p.c_vec4 != 0);
@@ -1067,7 +1067,8 @@ cudaError_t launch_gemm(const GemmPlan& plan, const GemmArgs& args, cudaStream_t
     return launch_gemm_as<kEpiPlain>(plan, args, s);
 }
 cudaError_t launch_gemm(const GemmPlan& plan, const WithEpilogue<GemmArgs>& args, int kind, cudaStream_t s) {
-    return kind == kEpiGated ? launch_gemm_as<kEpiGated>(plan, args, s) : launch_gemm_as<kEpiLinear>(plan, args, s);
+    if (kind == kEpiGated) return launch_gemm_as<kEpiGated>(plan, args, s);
+    return args.epi.act == kActNone ? launch_gemm_as<kEpiBias>(plan, args, s) : launch_gemm_as<kEpiLinear>(plan, args, s);
 }
 
 cudaError_t launch_timeout_selftest(uint32_t* status, uint64_t limit_ns, cudaStream_t s) {

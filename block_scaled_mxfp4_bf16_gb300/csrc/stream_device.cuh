@@ -564,23 +564,21 @@ struct EpilogueRing<kEpiLinear> {
         for (int i = 0; i < 4; ++i) b[i] = n0 + q + 8 * i < p.N ? bias_at(p.epi, n0 + q + 8 * i) : 0.f;
         const bool res = p.epi.residual != nullptr;
         for (int cb = t.first; cb < t.rows; cb += 16) {
-            uint32_t lo[8], hi[8];
-            __syncwarp();                          // reads of tensor memory take the whole warp, and whole: lane 0 may
-            tmem_load_frag16(trow + static_cast<uint32_t>(cb), lo);                  // still be about its copies
+            if (res) ask();
+            else if (lane == 0) stores_have_read<kRingSlots - 1>();
+            __syncwarp();                          // reads of tensor memory take the whole warp, and whole: lane 0 was
+            uint32_t lo[8], hi[8];                 // about its copies
+            tmem_load_frag16(trow + static_cast<uint32_t>(cb), lo);
             tmem_load_frag16(trow + (16u << 16) + static_cast<uint32_t>(cb), hi);
             tmem_frag16_wait(lo, hi);
-            bool got = true;
             if (res) {
-                ask();
-                got = mbar_wait(bar0 + used % kRingSlots, (used / kRingSlots) & 1u, p.wait_limit_ns);
-            } else if (lane == 0) {
-                stores_have_read<kRingSlots - 1>();
+                const bool got = mbar_wait(bar0 + used % kRingSlots, (used / kRingSlots) & 1u, p.wait_limit_ns);
+                if (!__all_sync(0xffffffffu, got)) {
+                    atomicOr(p.status, 1u);
+                    return false;
+                }
+                __syncwarp();                      // matrix loads and stores take the whole warp, too
             }
-            if (!__all_sync(0xffffffffu, got)) {
-                atomicOr(p.status, 1u);
-                return false;
-            }
-            __syncwarp();                          // as do matrix stores and loads
             const uint32_t at = slot(used) + put;
             // eight tokens at a time: sixteen leave no registers (of the pair kernel's 96) for the activations
 #pragma unroll
@@ -588,7 +586,7 @@ struct EpilogueRing<kEpiLinear> {
                 float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i < 4 ? lo[4 * h + i] : hi[4 * h + (i & 3)]) + b[i >> 1];
-                activate(p.epi.act, v);
+                activate<kEpiLinear>(p.epi.act, v);
                 if (res) {
                     uint32_t r[4];
                     ldmatrix_x4_trans(at + static_cast<uint32_t>(h) * 512u, r);
@@ -650,7 +648,7 @@ __device__ __forceinline__ void store_tile_gated(const WithEpilogue<StreamArgs>&
             g[i] = __uint_as_float(from[(i >> 2) * 4 + (i & 1)]) + b[(i >> 1) & 1].gate;
             u[i] = __uint_as_float(from[(i >> 2) * 4 + 2 + (i & 1)]) + b[(i >> 1) & 1].up;
         }
-        activate(p.epi.act, g);
+        activate<kEpiGated>(p.epi.act, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] *= u[i];
         __syncwarp();
@@ -863,7 +861,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
         }
         if constexpr (kEpi == kEpiLinear) {
             if (kPair) load_run(p.epi, p.N, n, row0 + m0, tokens - m0, run);   // no registers for it before
-            store_run(p.epi, p.N, n, row0 + m0, min(kTok, tokens - m0), v, run, p.c, p.ldc);
+            store_run<kEpi>(p.epi, p.N, n, row0 + m0, min(kTok, tokens - m0), v, run, p.c, p.ldc);
         } else if constexpr (kEpi == kEpiGated) {
             store_run_gated(p.epi, b2, n, row0 + m0, min(kTok, tokens - m0), v, p.c, p.ldc);
         } else if (n < p.N) {
