@@ -39,17 +39,8 @@ StreamArgs stream_args(const void* packed_b, int64_t N, int64_t K, void* c, int6
     return a;
 }
 
-#ifdef MXFP4_TEST_HOOKS
-decltype(StreamArgs::test_give_up) g_give_up = {-1, 0, 0};
-uint64_t g_tag = 0;
-#endif
-
 int run_stream(const StreamPlan& plan, const DeviceInfo& di, StreamArgs a, uint8_t* ws, int terms, cudaStream_t s) {
     fill_stream_args(plan, di, ws, &a);
-#ifdef MXFP4_TEST_HOOKS
-    a.test_give_up = g_give_up;
-    if (g_tag) a.tag = g_tag;
-#endif
     const cudaError_t e = launch_stream(plan, a, terms, s);
     return e == cudaSuccess ? MXFP4_OK : cuda_fail(e);
 }
@@ -204,9 +195,9 @@ int mxfp4_moe_combine(const void* y, int64_t R, int64_t N, int64_t ldy, const in
 // Test build only (-DMXFP4_TEST_HOOKS, never the product library): in the streaming products enqueued from
 // now on, one thread of one CTA takes the nth wait of its warp for run out (an epilogue warp's nth share,
 // the nth step of a warp that writes tokens or scale factors). cta -1 turns it off.
-void mxfp4_test_stream_give_up(int cta, int thread, int nth) { g_give_up = {cta, thread, nth}; }
+void mxfp4_test_stream_give_up(int cta, int thread, int nth) { stream_hooks().give_up = {cta, thread, nth}; }
 // And the tag that they all have, as the replays of one captured launch do (0: one each).
-void mxfp4_test_stream_tag(uint64_t tag) { g_tag = tag; }
+void mxfp4_test_stream_tag(uint64_t tag) { stream_hooks().tag = tag; }
 #endif
 
 }  // extern "C"

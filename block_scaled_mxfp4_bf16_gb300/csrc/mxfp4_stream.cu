@@ -902,6 +902,17 @@ void fill_stream_args(const StreamPlan& plan, const DeviceInfo& di, uint8_t* ws,
     a.a_block = plan.a_block;
     a.tmem_cols = plan.tmem_cols;
     a.wait_limit_ns = wait_limit_ns();
+#ifdef MXFP4_TEST_HOOKS
+    a.test_give_up = stream_hooks().give_up;
+    if (stream_hooks().tag) a.tag = stream_hooks().tag;
+#endif
 }
+
+#ifdef MXFP4_TEST_HOOKS
+StreamHooks& stream_hooks() {
+    static StreamHooks hooks = {{-1, 0, 0}, 0};
+    return hooks;
+}
+#endif
 
 }  // namespace mxfp4

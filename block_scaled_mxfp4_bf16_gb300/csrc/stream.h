@@ -234,6 +234,14 @@ cudaError_t launch_stream_pair(const StreamPlan& plan, const WithEpilogue<Stream
 cudaError_t launch_stream(const StreamPlan& plan, const WithEpilogue<StreamArgs>& args, int kind, cudaStream_t s);
 // The plan's part of the arguments, and the launch: the workspace holds token blocks, counters and partial sums.
 void fill_stream_args(const StreamPlan& plan, const DeviceInfo& di, uint8_t* ws, StreamArgs* a);
+#ifdef MXFP4_TEST_HOOKS
+// Test build only: what fill_stream_args gives every call (mxfp4_test_stream_give_up, mxfp4_test_stream_tag; tag 0: its own).
+struct StreamHooks {
+    decltype(StreamArgs::test_give_up) give_up;
+    uint64_t tag;
+};
+StreamHooks& stream_hooks();
+#endif
 
 // Routing and combination (moe.cu).
 struct RouteArgs {

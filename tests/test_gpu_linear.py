@@ -146,7 +146,7 @@ def test_tails_of_the_activations():
         assert_within(out[None], want[None], (want.abs() * ACT_EPS + TINY)[None], act)
 
 
-@pytest.mark.parametrize("M,N,K", [(4, 300, 1040), (700, 7300, 1544)])
+@pytest.mark.parametrize("M,N,K", [(4, 300, 1040), (60, 304, 1040), (700, 7300, 1544), (700, 7304, 3080)])
 def test_other_streams_graphs_and_an_empty_call(M, N, K):
     import block_scaled_mxfp4_bf16_gb300 as mx
     packed, w, x, b, r = operands(M, N, K, torch.float32, True, seed=9)
@@ -179,3 +179,43 @@ def test_other_streams_graphs_and_an_empty_call(M, N, K):
     assert mx.mxfp4_device_status() == 0
     assert mx.mxfp4_linear(x[:0], packed, N).shape == (0, N)
     assert mx.mxfp4_linear(x, packed, 0).shape == (M, 0)
+
+
+@pytest.mark.parametrize("M,N,K", [(2100, 200, 520), (700, 7304, 1544), (2100, 204, 520)])
+def test_rows_that_lie_past_2_to_the_31_elements(M, N, K):
+    # in place, on rows far apart: the last ones start behind 2^31 elements
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    packed, w, x, b, r = operands(M, N, K, torch.float32, True, seed=11)
+    stride = (2 ** 31 + 2 ** 27) // M // 8 * 8
+    store = torch.empty(M * stride, dtype=torch.bfloat16, device="cuda")
+    rows = store.view(M, stride)[:, 16:16 + N]
+    store.view(M, stride)[:, :N + 32] = -7.0
+    rows.copy_(r)
+    mx.mxfp4_linear(x, packed, N, bias=b, activation="silu", residual=rows, out=rows)
+    check(rows, x, w, bias=b, activation="silu", residual=r)
+    assert bool((store.view(M, stride)[:, :16] == -7).all()) and bool((store.view(M, stride)[:, 16 + N:N + 32] == -7).all())
+
+
+def test_two_threads_on_one_stream():
+    # calls of two kernels, enqueued with the interpreter's lock released between them
+    import threading
+
+    import block_scaled_mxfp4_bf16_gb300 as mx
+    cases = [operands(300, 520, 2056, torch.float32, True, seed=s) for s in (1, 2)]
+    want = [mx.mxfp4_linear(x, packed, 520, bias=b, residual=r) for packed, _, x, b, r in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        packed, _, x, b, r = cases[i]
+        for _ in range(200):
+            got[i].append(mx.mxfp4_linear(x, packed, 520, bias=b, residual=r))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o.view(torch.int16), want[i].view(torch.int16)) for o in got[i])
+    assert mx.mxfp4_device_status() == 0
