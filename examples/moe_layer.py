@@ -1,5 +1,5 @@
 """A mixture-of-experts feed-forward layer on MXFP4 weights, the way a model's layer uses the
-operators: route, the experts' first products (gate and up), the gated second products, combine.
+operators: route, the experts' first products (gate and up, gated in their epilogue), their second products, combine.
 
     python examples/moe_layer.py [tokens] [experts] [k] [hidden] [intermediate]
 
@@ -24,19 +24,19 @@ class MoeLayer:
     def __init__(self, router: torch.Tensor, w13: torch.Tensor, w2: torch.Tensor, k: int):
         self.router, self.k = router, k
         self.hidden, self.intermediate = w2.shape[1], w2.shape[2]
-        self.w13 = self._pack(w13)
-        self.w2 = self._pack(w2)
+        self.w13 = mx.mxfp4_prepack_gated_experts(*self._quantized(w13))
+        self.w2 = mx.mxfp4_prepack_experts(*self._quantized(w2))
 
     @staticmethod
-    def _pack(w: torch.Tensor) -> torch.Tensor:
+    def _quantized(w: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
         E, N, K = w.shape
         bq, bs = mx.mxfp4_quantize(w.reshape(E * N, K))
-        return mx.mxfp4_prepack_experts(bq.view(E, N, -1), bs.view(E, N, -1))
+        return bq.view(E, N, -1), bs.view(E, N, -1)
 
     def __call__(self, x: torch.Tensor) -> torch.Tensor:
         r = mx.mxfp4_moe_route((x @ self.router.T).float(), self.k)
-        gate_up = mx.mxfp4_grouped_gemm(x, self.w13, r.offsets, 2 * self.intermediate, rows=r.rows)
-        y = mx.mxfp4_grouped_gemm(gate_up, self.w2, r.offsets, self.hidden, gated=True)
+        h = mx.mxfp4_grouped_gated_linear(x, self.w13, r.offsets, self.intermediate, rows=r.rows)
+        y = mx.mxfp4_grouped_gemm(h, self.w2, r.offsets, self.hidden)
         return mx.mxfp4_moe_combine(y, r.slots, r.weights)
 
 
