@@ -67,7 +67,8 @@ L2_BYTES_DEFAULT = 126 * 1024 * 1024
 
 # Per plan path, the translation units of the kernels one call launches and everything they
 # include: a capture stays valid while these are unchanged (the two-kernel path also launches the
-# token-block quantizer of mxfp4_quant.cu).
+# token-block quantizer of mxfp4_quant.cu). epilogue.cuh is left out: the kernels of these calls are
+# instantiated for kEpiPlain, which has none of it in them.
 KERNEL_SOURCES = {
     1: ("mxfp4_gemm.cu", "mma_desc.cuh", "ptx.cuh", "quant_device.cuh", "internal.h"),
     2: ("mxfp4_gemm.cu", "mxfp4_quant.cu", "mma_desc.cuh", "ptx.cuh", "quant_device.cuh", "internal.h"),

@@ -32,8 +32,7 @@ __device__ __forceinline__ float fast_rcp(float x) {
 }
 
 // Two fp32 in a 64-bit register, and the instructions that work on both: half the issue slots of the arithmetic around the
-// exponentials (3648x4096x1536 with gelu, bias and residual 32.9 us, not
-// 31.3; 3x2112x7168 3.44 and 3.12).
+// exponentials (3648x4096x1536 with gelu, bias and residual 31.3 us, not 32.9).
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -132,7 +131,7 @@ __device__ __forceinline__ int gated_feature(int n) { return (n >> 4) * 8 + (n &
 __device__ __forceinline__ bool gated_up(int n) { return (n & 8) != 0; }
 
 // What an epilogue adds is loaded before the sums are waited for: loaded after them, one row's residual after another
-// (the stores between may be to the same memory, so the compiler keeps the order), 256x4096x7168 took 21.3 us, not 11.8.
+// (the stores between may be to the same memory, so the compiler keeps the order), 256x4096x7168 took 21.3 us, not 14.6.
 
 // ---- a lane's run of tokens: v[i] is the sum of weight row n (lane nl of its warp's 32) and token row0 + i,
 // for i < cnt. All lanes of the warp call, with rows past the last among them; cnt is the warp's.
@@ -321,7 +320,8 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, int nacc, uint32_t acc
 // Whole sums of a lane's weight row n from tensor memory to C, kN tokens at a time: of `tokens` (the first is row0 of
 // C) those from `first` on, every step-th kN of them. load_first asks for what the first run adds. The whole warp calls
 // both. 16 tokens, not 32: with 137 and 168 registers a thread instead of 80, no second CTA of the weight-resident
-// kernel, and no block of the quantizer beside the streaming one, fits the SM (8x2112x7168 4.20 us, not 3.6).
+// kernel, and no block of the quantizer beside the streaming one, fits the SM (256x4096x7168 with bias and
+// residual 14.6 us, not 13.5).
 template <int kEpi, int kN = 16>
 struct LaneStore {
     std::conditional_t<linear_epilogue(kEpi), TokenRun<kN>, GatedBias> add;

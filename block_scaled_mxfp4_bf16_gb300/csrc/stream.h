@@ -104,7 +104,7 @@ __host__ __device__ inline bool arrival_clean(unsigned long long word) { return 
 // a us, 120 of them a CTA working alone; a unit takes its steps or its epilogue, 3 us for 128 x 192 sums, whichever is more,
 // and 1.1 us; what is left after whole waves of units is cut along K where the walk does so (begin_walk), which
 // costs 9 us of sums through the workspace. Over 166 shapes (M 77 to 8192, N 1000 to 28672, K 1024 to 7168), every plan measured,
-// the one picked took 1.4 % more than the best (geometric mean; the largest equal tiles in pairs, and the GEMM wherever its CTAs
+// the one picked took 0.8 % more than the best (geometric mean; the largest equal tiles in pairs, and the GEMM wherever its CTAs
 // make one wave: 7.2 % more, 49 % at worst): 2048 x 14336 x 4096 gated 44.3 us in tiles of 176 against 50.6 of 192,
 // 1500 x 4096 x 7168 25.5 of 176 against 35.2 of 192, 300 x 14336 x 4096 gated 18.6 of 80 against 22.2 of 160.
 struct DenseChoice {

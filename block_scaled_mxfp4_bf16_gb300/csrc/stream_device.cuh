@@ -502,8 +502,7 @@ __device__ __forceinline__ void stores_have_read() {
 // first pieces before its sums are waited for; a result takes the place of its residual, and a copy takes it to C.
 // Rows past the last token and columns past N are the maps' business: they read as zeros and are not written.
 // Through registers instead (16-byte loads a piece ahead, the transposed piece read back and stored by the lanes),
-// every 16 tokens waited for L2: 3648 x 4096 x 7168 45.6 us without and 58.7 with a residual, where the product alone
-// takes 7.8 of each unit's time.
+// every 16 tokens waited for L2: 8192 x 4096 x 7168 with bias, gelu_tanh and residual 178 us, not 123.
 template <int kEpi>
 struct EpilogueRing {      // nothing for the other epilogues
     __device__ __forceinline__ EpilogueRing(const EpilogueMaps<kEpi>&, uint8_t*, uint64_t*, int, int) {}
