@@ -502,7 +502,7 @@ __device__ __forceinline__ void stores_have_read() {
 // first pieces before its sums are waited for; a result takes the place of its residual, and a copy takes it to C.
 // Rows past the last token and columns past N are the maps' business: they read as zeros and are not written.
 // Through registers instead (16-byte loads a piece ahead, the transposed piece read back and stored by the lanes),
-// every 16 tokens waited for L2: 8192 x 4096 x 7168 with bias, gelu_tanh and residual 178 us, not 123.
+// every 16 tokens waited for L2: 8192 x 4096 x 7168 with bias, gelu_tanh and residual 178 us, not 119.
 template <int kEpi>
 struct EpilogueRing {      // nothing for the other epilogues
     __device__ __forceinline__ EpilogueRing(const EpilogueMaps<kEpi>&, uint8_t*, uint64_t*, int, int) {}
@@ -554,7 +554,9 @@ struct EpilogueRing<kEpiLinear> {
         ask();
         __syncwarp();
     }
-    // The accumulator of the tokens of `t`, from tensor memory at trow, to C. Whether all went well.
+    // The accumulator of the tokens of `t`, from tensor memory at trow, to C. Whether all went well. (Two pieces a turn
+    // gained 7 % of 65536 x 2048 x 64 without an activation, and lost 6 to 10 % with gelu.)
+    template <int kAct>
     __device__ __forceinline__ bool store(const WithEpilogue<StreamArgs>& p, uint32_t trow, const TokenShare& t, int64_t row0, int n0) {
         if (n0 >= p.N) return true;
         const int q = lane >> 2;
@@ -585,7 +587,7 @@ struct EpilogueRing<kEpiLinear> {
                 float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i < 4 ? lo[4 * h + i] : hi[4 * h + (i & 3)]) + b[i >> 1];
-                activate<kEpiLinear>(p.epi.act, v);
+                activate_as<kAct>(v);
                 if (res) {
                     uint32_t r[4];
                     ldmatrix_x4_trans(at + static_cast<uint32_t>(h) * 512u, r);
@@ -620,6 +622,7 @@ struct EpilogueRing<kEpiLinear> {
 // two features (lanes 0-15 and 16-31 of the warp's) and two tokens; a token's 16 features are two pieces of shared
 // memory, 32 bytes, the pieces of tokens 4-7 and 12-15 swapped, so that the eight rows a matrix is stored to touch all
 // banks.
+template <int kAct>
 __device__ __forceinline__ void store_tile_gated(const WithEpilogue<StreamArgs>& p, uint32_t trow, const TokenShare& share,
                                                  int64_t row0, int n0, int64_t bias0, int lane, uint8_t* stage) {
     const int q = lane >> 2;
@@ -647,7 +650,7 @@ __device__ __forceinline__ void store_tile_gated(const WithEpilogue<StreamArgs>&
             g[i] = __uint_as_float(from[(i >> 2) * 4 + (i & 1)]) + b[(i >> 1) & 1].gate;
             u[i] = __uint_as_float(from[(i >> 2) * 4 + 2 + (i & 1)]) + b[(i >> 1) & 1].up;
         }
-        activate<kEpiGated>(p.epi.act, g);
+        activate_as<kAct>(g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) g[i] *= u[i];
         __syncwarp();
@@ -721,16 +724,24 @@ __device__ __forceinline__ bool store_tile_epi(const WithEpilogue<StreamArgs>& p
                                                int warp, int lane, uint8_t* stage, EpilogueRing<kEpi>& ring) {
     const int n0 = nt * kTileN + (warp & 3) * 32;
     const int64_t bias0 = kEpi == kEpiGated ? static_cast<int64_t>(u.group) * 2 * p.epi.features : 0;
-    if (p.c_wide) {
-        const TokenShare share = token_share(u.rows, half);
-        if constexpr (kEpi == kEpiLinear) return ring.store(p, acc, share, u.row0, n0);
-        else store_tile_gated(p, acc, share, u.row0, n0, bias0, lane, stage);
-    } else {
+    if (!p.c_wide) {
         LaneStore<kEpi, kRun> run;
         run.load_first(p.epi, bias0, p.N, n0 + lane, u.row0, u.rows, half * kRun);
         run.store(p.epi, p.N, n0 + lane, u.row0, u.rows, half * kRun, 2 * kRun, acc, 1, 0u, p.c, p.ldc);
+        return true;
     }
-    return true;
+    const TokenShare share = token_share(u.rows, half);
+    // A loop for each activation: with the choice inside it, fetching the instructions around it took longer than
+    // the work (3648 x 4096 x 1536 without an activation 21.2 us, not 19.0, with gelu_tanh, bias and residual 29.6 and
+    // 27.2; 4096 x 14336 x 4096 gated 89.5 and 86.8). Not so the runs of a lane below, whose five loops spill
+    // (3648 x 4097 x 1536 21.5 us with one loop, 33.3 with five).
+    bool ok = true;
+    with_activation(p.epi.act, [&](auto a) {
+        constexpr int kAct = decltype(a)::value;
+        if constexpr (kEpi == kEpiLinear) ok = ring.template store<kAct>(p, acc, share, u.row0, n0);
+        else store_tile_gated<kAct>(p, acc, share, u.row0, n0, bias0, lane, stage);
+    });
+    return ok;
 }
 
 // A CTA's share of a unit from its accumulator (at acc in this warp's quarter of the lanes) to C:
