@@ -101,11 +101,11 @@ __host__ __device__ inline bool arrival_clean(unsigned long long word) { return 
 // ---- how a dense product with an epilogue runs: the choice between the GEMM's plan and one group of the streaming
 // product, and the latter's token tiles, by a model of the time that follows the operands' token blocks, in us.
 // A 256-K step takes as long as its bytes take into an SM (17 KB of weights, the CTA's token rows and their scales), 113 KB
-// a us, 120 of them a CTA working alone; a unit takes its steps or its epilogue, 3 us for 128 x 192 sums, whichever is more,
+// a us, 120 of them a CTA working alone; a unit takes its steps or its epilogue, 2.4 us for 128 x 192 sums, whichever is more,
 // and 1.1 us; what is left after whole waves of units is cut along K where the walk does so (begin_walk), which
-// costs 9 us of sums through the workspace. Over 166 shapes (M 77 to 8192, N 1000 to 28672, K 1024 to 7168), every plan measured,
-// the one picked took 0.8 % more than the best (geometric mean; the largest equal tiles in pairs, and the GEMM wherever its CTAs
-// make one wave: 7.2 % more, 49 % at worst): 2048 x 14336 x 4096 gated 44.3 us in tiles of 176 against 50.6 of 192,
+// costs 9 us of sums through the workspace. Over 186 shapes (M 77 to 10000, N 1000 to 28672, K 256 to 7168), every plan measured,
+// the one picked took 0.8 % more than the best (geometric mean; 13 % at worst. The largest equal tiles in pairs, and the GEMM
+// wherever its CTAs make one wave, over 166 of them: 7.2 %, 49 %): 2048 x 14336 x 4096 gated 44.3 us in tiles of 176 against 50.6 of 192,
 // 1500 x 4096 x 7168 25.5 of 176 against 35.2 of 192, 300 x 14336 x 4096 gated 18.6 of 80 against 22.2 of 160.
 struct DenseChoice {
     bool streams;
@@ -118,9 +118,9 @@ inline double stream_cost(int64_t M, int64_t N, int64_t K, int columns, int m_ti
     const int64_t walkers = pair ? sm_count / 2 : sm_count, units = tiles * (pair ? (n_tiles + 1) / 2 : n_tiles);
     const double step = pair ? step_bytes(static_cast<int>(pair_code_bytes(m_tile)), m_tile) / 113e3
                              : step_bytes(m_tile * 128, m_tile) / 120e3;
-    const double epilogue = 3.0 * m_tile / 192, whole = k * step, unit = (whole > epilogue ? whole : epilogue) + 1.1;
+    const double epilogue = 2.4 * m_tile / 192, whole = k * step, unit = (whole > epilogue ? whole : epilogue) + 1.1;
     // a pair's second CTA to wait for; rows that start off 16 bytes are stored element by element, with few registers
-    const double fixed = 2.0 + epilogue + (pair ? (columns % 8 ? 3.0 : 1.0) : 0.0);
+    const double fixed = 2.0 + epilogue + (pair ? (columns % 8 ? 3.0 : 2.0) : 0.0);
     const int64_t waves = units / walkers, rest = units - waves * walkers;
     const int64_t even = (rest * k + walkers - 1) / walkers;
     int64_t share = split_share(even, static_cast<int>(k));
@@ -135,7 +135,7 @@ inline double stream_cost(int64_t M, int64_t N, int64_t K, int columns, int m_ti
 // The GEMM's plan in one wave of CTAs: a split tile's sums go through shared memory, which is cheap up to 128 tokens.
 inline double gemm_cost(int64_t K, int splits, int m_tile) {
     const int64_t k = (K + 255) / 256, steps = (k + splits - 1) / splits;
-    const double end = splits == 1 ? 3.0 * m_tile / 192 : m_tile <= 128 ? 1.5 : 8.0;
+    const double end = splits == 1 ? 2.0 * m_tile / 192 : m_tile <= 128 ? 1.5 : 8.0;
     return steps * step_bytes(m_tile * 128, m_tile) / 120e3 + 1.1 + end;
 }
 // gemm_*: the GEMM's plan on token blocks. N: weight rows; columns: of the output.
