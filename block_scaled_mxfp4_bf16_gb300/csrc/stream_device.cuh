@@ -760,6 +760,9 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
     constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
     // The pair kernel has no registers for two: it spilled 136 bytes then, and 16384 rows took 218 us, not 210.
     constexpr int kFlight = kPair ? 1 : 2;
+    // Nor, with an epilogue, for its own sums beside the others': it reads them when their turn comes.
+    constexpr bool kLate = kPair && kEpi != kEpiPlain;
+    static_assert(!kLate || (kTermsPer == 1 && kFlight == 1), "a unit that is not split has been stored above");
     const bool split = u.nk != p.k_atoms;
     if (!split && !live) return false;
     if (kTermsPer == 1 && u.nk == p.k_atoms) {
@@ -840,8 +843,8 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
         // Thread 128 has just cleared the counter, lanes past N have skipped loads: reads of tensor memory take the whole
         // warp, and whole.
         if constexpr (kEpi != kEpiPlain) __syncwarp();
-        load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), own);
-        if (!split) {
+        if constexpr (!kLate) load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), own);
+        if (!kLate && !split) {
 #pragma unroll
             for (int i = 0; i < kTok; ++i) v[i] = own[i];
         } else {
@@ -853,6 +856,13 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
 #pragma unroll
                 for (int q = 0; q < kFlight; ++q) {
                     const int c = c0 + q;
+                    if constexpr (kLate) {
+                        if (c == me) {
+                            __syncwarp();
+                            load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), theirs[q]);
+                            continue;
+                        }
+                    }
                     if (c > c_last || c == me) continue;
                     // the unit is the first of c's run unless the run began before it
                     const float* src = p.partial + (static_cast<size_t>(c * kRanks + rank) * 2 +
@@ -865,7 +875,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
                 for (int q = 0; q < kFlight; ++q) {
                     if (c0 + q > c_last) continue;
 #pragma unroll
-                    for (int i = 0; i < kTok; ++i) v[i] += c0 + q == me ? own[i] : theirs[q][i];
+                    for (int i = 0; i < kTok; ++i) v[i] += !kLate && c0 + q == me ? own[i] : theirs[q][i];
                 }
             }
         }
