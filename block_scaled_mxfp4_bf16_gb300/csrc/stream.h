@@ -104,7 +104,7 @@ __host__ __device__ inline bool arrival_clean(unsigned long long word) { return 
 // a us, 120 of them a CTA working alone; a unit takes its steps or its epilogue, 2.4 us for 128 x 192 sums, whichever is more,
 // and 1.1 us; what is left after whole waves of units is cut along K where the walk does so (begin_walk), which
 // costs 9 us of sums through the workspace. Over 186 shapes (M 77 to 10000, N 1000 to 28672, K 256 to 7168), every plan measured,
-// the one picked took 0.8 % more than the best (geometric mean; 13 % at worst. The largest equal tiles in pairs, and the GEMM
+// the one picked took 0.8 % more than the best (geometric mean; 9 % at worst. The largest equal tiles in pairs, and the GEMM
 // wherever its CTAs make one wave, over 166 of them: 7.2 %, 49 %): 2048 x 14336 x 4096 gated 44.3 us in tiles of 176 against 50.6 of 192,
 // 1500 x 4096 x 7168 25.5 of 176 against 35.2 of 192, 300 x 14336 x 4096 gated 18.6 of 80 against 22.2 of 160.
 struct DenseChoice {
@@ -150,8 +150,8 @@ inline DenseChoice choose_dense(int64_t M, int64_t N, int64_t K, int columns, in
         const int m_tile = static_cast<int>(((M + t - 1) / t + 15) / 16 * 16);
         if (m_tile < 64 && t > 1) break;
         if (tile_rows(static_cast<int>(M), m_tile) != m_tile) continue;
-        // pairs from 12 steps on: 2048 x 7168 x 2048 22.2 us alone and 23.7 in pairs, 2048 x 14336 x 4096 51.1 and 44.3
-        for (int pair = 0; pair <= (K > 11 * 256 && N > 128 ? 1 : 0); ++pair) {
+        // pairs from 8 steps on: 4000 x 28672 x 2048 gated 87.8 us alone and 82.3 in pairs; 4096 x 5120 x 1536 23.4 and 26.9
+        for (int pair = 0; pair <= (K > 7 * 256 && N > 128 ? 1 : 0); ++pair) {
             const double cost = stream_cost(M, N, K, columns, m_tile, pair != 0, sm_count);
             if (cost < least) {
                 least = cost;
