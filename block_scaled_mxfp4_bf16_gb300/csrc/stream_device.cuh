@@ -502,7 +502,7 @@ __device__ __forceinline__ void stores_have_read() {
 // first pieces before its sums are waited for; a result takes the place of its residual, and a copy takes it to C.
 // Rows past the last token and columns past N are the maps' business: they read as zeros and are not written.
 // Through registers instead (16-byte loads a piece ahead, the transposed piece read back and stored by the lanes),
-// every 16 tokens waited for L2: 8192 x 4096 x 7168 with bias, gelu_tanh and residual 178 us, not 119.
+// every 16 tokens waited for L2: 8192 x 4096 x 7168 with bias, gelu_tanh and residual 178 us, not 112.
 template <int kEpi>
 struct EpilogueRing {      // nothing for the other epilogues
     __device__ __forceinline__ EpilogueRing(const EpilogueMaps<kEpi>&, uint8_t*, uint64_t*, int, int) {}
@@ -760,7 +760,8 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
     constexpr int kRanks = kPair ? 2 : 1;        // CTAs that walk together, each with its own weight tile
     // The pair kernel has no registers for two: it spilled 136 bytes then, and 16384 rows took 218 us, not 210.
     constexpr int kFlight = kPair ? 1 : 2;
-    // Nor, with an epilogue, for its own sums beside the others': it reads them when their turn comes.
+    // Nor, with an epilogue, for its own sums beside the others': it reads them when their turn comes (held, they cost 250
+    // bytes of spills, not 32, and 8192 x 4096 x 7168 with bias, gelu_tanh and residual took 119 us, not 112).
     constexpr bool kLate = kPair && kEpi != kEpiPlain;
     static_assert(!kLate || (kTermsPer == 1 && kFlight == 1), "a unit that is not split has been stored above");
     const bool split = u.nk != p.k_atoms;

@@ -221,7 +221,7 @@ int main() {
         }
         if (c.m_tile < 16 || c.m_tile > 192 || c.m_tile % 16 || tile_rows((int)M, c.m_tile) != c.m_tile) return 8;
         const int64_t tiles = tiles_of((int)M, c.m_tile);
-        if ((tiles - 1) * c.m_tile >= M || tiles * c.m_tile < M || (c.pair && (N <= 128 || K <= 11 * 256))) return 9;
+        if ((tiles - 1) * c.m_tile >= M || tiles * c.m_tile < M || (c.pair && (N <= 128 || K <= 7 * 256))) return 9;
     }
     puts("ok");
     return 0;
