@@ -795,7 +795,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
         unsigned long long* counter = counter_of<kPair>(p, shared);
         if (threadIdx.x == 128)
             flag[0] = *reinterpret_cast<volatile unsigned long long*>(counter) == (p.tag << 8 | others) ? 1u : 0u;
-        if constexpr (kEpi != kEpiPlain) __syncwarp();
+        __syncwarp();              // thread 128 has been about the counter: barriers and reads of tensor memory take whole warps
         if (named_barrier_any(2, kStreamEpiThreads, !live)) {
             if (threadIdx.x == 128) {
                 flag[1] = static_cast<uint32_t>(counter - p.counters);
@@ -808,7 +808,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
             float* mine = p.partial + (static_cast<size_t>(me * kRanks + rank) * 2 + slot) * slot_floats;
             for (int cb = half * 16; cb < u.rows; cb += 32) {
                 float v[kTok];
-                if constexpr (kEpi != kEpiPlain) __syncwarp();
+                __syncwarp();
                 load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), v);
                 const int m0 = cb / kTermsPer;
 #pragma unroll
@@ -818,7 +818,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
             unsigned long long seen = 0ull;
             if (threadIdx.x == 128) seen = *reinterpret_cast<volatile unsigned long long*>(counter);
             __threadfence();
-            if constexpr (kEpi != kEpiPlain) __syncwarp();   // the barriers too take whole warps
+            __syncwarp();
             named_barrier(2, kStreamEpiThreads);
             if (threadIdx.x == 128) {
                 const unsigned long long was = arrive(counter, seen, p.tag, false);
@@ -826,7 +826,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
                 flag[1] = all && clean ? 1u : 0u;
                 if (all && !clean) *counter = 0ull;
             }
-            if constexpr (kEpi != kEpiPlain) __syncwarp();
+            __syncwarp();
             named_barrier(2, kStreamEpiThreads);
             last = flag[1] != 0u;
         }
@@ -843,7 +843,7 @@ __device__ __forceinline__ bool store_unit(const EpilogueArgs<StreamArgs, kEpi>&
         if constexpr (kEpi == kEpiLinear && !kPair) load_run(p.epi, p.N, n, row0 + m0, tokens - m0, run);
         // Thread 128 has just cleared the counter, lanes past N have skipped loads: reads of tensor memory take the whole
         // warp, and whole.
-        if constexpr (kEpi != kEpiPlain) __syncwarp();
+        __syncwarp();
         if constexpr (!kLate) load_tokens<kTermsPer>(acc + static_cast<uint32_t>(cb), own);
         if (!kLate && !split) {
 #pragma unroll
