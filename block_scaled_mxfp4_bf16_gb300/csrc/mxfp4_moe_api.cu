@@ -194,7 +194,8 @@ int mxfp4_moe_combine(const void* y, int64_t R, int64_t N, int64_t ldy, const in
 #ifdef MXFP4_TEST_HOOKS
 // Test build only (-DMXFP4_TEST_HOOKS, never the product library): in the streaming products enqueued from
 // now on, one thread of one CTA takes the nth wait of its warp for run out (an epilogue warp's nth share,
-// the nth step of a warp that writes tokens or scale factors). cta -1 turns it off.
+// its nth piece of the residual for nth from 2^20 on, the nth step of a warp that writes tokens or scale factors).
+// cta -1 turns it off.
 void mxfp4_test_stream_give_up(int cta, int thread, int nth) { stream_hooks().give_up = {cta, thread, nth}; }
 // And the tag that they all have, as the replays of one captured launch do (0: one each).
 void mxfp4_test_stream_tag(uint64_t tag) { stream_hooks().tag = tag; }

@@ -562,7 +562,7 @@ mxfp4_stream_kernel(const EpilogueArgs<StreamArgs, kEpi> p, const __grid_constan
         Walk u = start;
         int nshare = 0;
         bool live = true;
-        EpilogueRing<kEpi> pieces(epi_maps, ring, ring_bars, warp - 4, lane);
+        EpilogueRing<kEpi> pieces(epi_maps, ring, ring_bars, abort_flag, warp - 4, lane);
         while (next_share(p, prefix, u)) {
             const int b = nshare & 1;
             if (live) pieces.begin(p, u, u.nt, half, warp);

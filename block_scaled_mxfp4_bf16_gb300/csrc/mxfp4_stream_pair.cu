@@ -324,7 +324,7 @@ mxfp4_stream_pair_kernel(const __grid_constant__ EpilogueArgs<StreamArgs, kEpi> 
         Walk u = start;
         int nshare = 0;
         bool live = true;
-        EpilogueRing<kEpi> pieces(epi_maps, ring, ring_bars, warp - 4, lane);
+        EpilogueRing<kEpi> pieces(epi_maps, ring, ring_bars, abort_flag, warp - 4, lane);
         while (next_share<true>(p, prefix, u)) {
             const int b = nshare & 1;
             if (live) pieces.begin(p, u, 2 * u.nt + static_cast<int>(rank), half, warp);

@@ -258,6 +258,9 @@ __device__ __forceinline__ void stream_fail(const StreamArgs& p, volatile uint32
     *abort_flag = 1u;
 }
 
+// Waits of an epilogue's warp for pieces of the residual are numbered from here on, apart from those for its shares.
+constexpr int kPieceWaits = 1 << 20;
+
 // Whether all lanes of the warp got through their bounded waits, the nth time: one decision, since they may
 // run out of time apart and the warp goes on to instructions and barriers that take all of them.
 __device__ __forceinline__ bool warp_agrees(const StreamArgs& p, bool got, int nth) {
@@ -505,7 +508,7 @@ __device__ __forceinline__ void stores_have_read() {
 // every 16 tokens waited for L2: 8192 x 4096 x 7168 with bias, gelu_tanh and residual 178 us, not 112.
 template <int kEpi>
 struct EpilogueRing {      // nothing for the other epilogues
-    __device__ __forceinline__ EpilogueRing(const EpilogueMaps<kEpi>&, uint8_t*, uint64_t*, int, int) {}
+    __device__ __forceinline__ EpilogueRing(const EpilogueMaps<kEpi>&, uint8_t*, uint64_t*, volatile uint32_t*, int, int) {}
     template <typename Args>
     __device__ __forceinline__ void begin(const Args&, const Walk&, int, int, int) {}
     template <typename Args>
@@ -516,14 +519,16 @@ struct EpilogueRing<kEpiLinear> {
     const LinearMaps& maps;
     uint32_t slots, bars;          // this warp's, in shared memory
     uint64_t* bar0;
+    volatile uint32_t* abort_flag; // the CTA's
     uint32_t put;                  // where a lane's matrix rows go in a slot
     int lane;
     uint32_t used = 0, asked = 0;  // pieces taken; pieces of the residual asked for
     int x = 0, y = 0, end = 0;     // the next piece of the residual to ask for; the unit's end
 
-    __device__ __forceinline__ EpilogueRing(const LinearMaps& m, uint8_t* ring, uint64_t* barriers, int w, int l)
+    __device__ __forceinline__ EpilogueRing(const LinearMaps& m, uint8_t* ring, uint64_t* barriers, volatile uint32_t* abort,
+                                            int w, int l)
         : maps(m), slots(smem_addr(ring) + static_cast<uint32_t>(w * kRingSlots * kRingSlot)),
-          bars(smem_addr(barriers + w * kRingSlots)), bar0(barriers + w * kRingSlots),
+          bars(smem_addr(barriers + w * kRingSlots)), bar0(barriers + w * kRingSlots), abort_flag(abort),
           put(static_cast<uint32_t>((l & 7) * 64 + (((l >> 3) ^ ((l >> 1) & 3)) << 4))), lane(l) {}
 
     __device__ __forceinline__ uint32_t slot(uint32_t piece) const { return slots + (piece % kRingSlots) * kRingSlot; }
@@ -574,8 +579,8 @@ struct EpilogueRing<kEpiLinear> {
             tmem_frag16_wait(lo, hi);
             if (res) {
                 const bool got = mbar_wait(bar0 + used % kRingSlots, (used / kRingSlots) & 1u, p.wait_limit_ns);
-                if (!__all_sync(0xffffffffu, got)) {
-                    atomicOr(p.status, 1u);
+                if (!warp_agrees(p, got, kPieceWaits + static_cast<int>(used))) {
+                    stream_fail(p, abort_flag);    // the CTA's other warps take no further share
                     return false;
                 }
                 __syncwarp();                      // matrix loads and stores take the whole warp, too
