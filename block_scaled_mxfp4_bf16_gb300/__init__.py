@@ -367,15 +367,17 @@ _PACKED_NEED: dict = {}
 
 def _check_packed(packed_b: torch.Tensor, N: int, K: int, device: torch.device | None) -> None:
     """The packed weights must cover mxfp4_prepack_b_size(N, K) bytes on the GEMM's device: the
-    kernel streams that many bytes, so a smaller buffer would be read past its end. `device`
-    None checks only that the buffer is on a CUDA device (the per-step host call)."""
+    kernel streams that many bytes from the buffer's start, so a smaller buffer, or a view whose bytes
+    do not lie next to each other, would be read past its end. `device` None checks only that the
+    buffer is on a CUDA device (the per-step host call)."""
     need = _PACKED_NEED.get((N, K))
     if need is None:
         need = mxfp4_prepack_b_size(N, K)
         _PACKED_NEED[(N, K)] = need
-    if need == 0 or packed_b.nbytes < need or not packed_b.is_cuda or (device is not None and packed_b.device != device):
-        raise ValueError(f"packed_b must be a CUDA buffer of at least mxfp4_prepack_b_size({N}, {K}) = {need} bytes"
-                         " on the device of the other operands")
+    if (need == 0 or packed_b.nbytes < need or not packed_b.is_contiguous() or not packed_b.is_cuda
+            or (device is not None and packed_b.device != device)):
+        raise ValueError(f"packed_b must be a contiguous CUDA buffer of at least mxfp4_prepack_b_size({N}, {K}) = {need}"
+                         " bytes on the device of the other operands")
 
 
 def mxfp4_workspace_init(ws: torch.Tensor, stream=None) -> None:

@@ -42,7 +42,8 @@ def _sizes(key: tuple) -> tuple:
 
 
 def _too_small(name: str, what: str, need: int) -> None:
-    raise ValueError(f"{name} must be a CUDA buffer of at least {what} = {need} bytes on the device of the other operands")
+    raise ValueError(f"{name} must be a contiguous CUDA buffer of at least {what} = {need} bytes on the device of the"
+                     " other operands")
 
 
 def _rows_and_stride(t: torch.Tensor, name: str) -> tuple:
@@ -74,7 +75,7 @@ def mxfp4_linear(x: torch.Tensor, packed_b: torch.Tensor, N: int, bias: torch.Te
         key = ("mxfp4_linear_workspace_size", mxfp4_prepack_b_size, device, M, N, K)
         known = _SIZES.get(key) or _sizes(key)
         need = known[1]
-        if not known[0] or packed_b.nbytes < known[0] or packed_b.get_device() != device:
+        if not known[0] or packed_b.nbytes < known[0] or not packed_b.is_contiguous() or packed_b.get_device() != device:
             _too_small("packed_b", f"mxfp4_prepack_b_size({N}, {K})", known[0])
     bias_ptr, bias_type = (None, 0) if bias is None else _bias(bias, (N,), x)
     res_ptr, ldr = None, 0
@@ -177,7 +178,7 @@ def mxfp4_gated_linear(x: torch.Tensor, packed_gu: torch.Tensor, I: int, bias: t
         key = ("mxfp4_gated_linear_workspace_size", mxfp4_prepack_gated_size, device, M, I, K)
         known = _SIZES.get(key) or _sizes(key)
         need = known[1]
-        if not known[0] or packed_gu.nbytes < known[0] or packed_gu.get_device() != device:
+        if not known[0] or packed_gu.nbytes < known[0] or not packed_gu.is_contiguous() or packed_gu.get_device() != device:
             _too_small("packed_gu", f"mxfp4_prepack_gated_size({I}, {K})", known[0])
     bias_ptr, bias_type = (None, 0) if bias is None else _bias(bias, (2 * I,), x)
     if out is None and stream is None and _empty_strided is not None:
