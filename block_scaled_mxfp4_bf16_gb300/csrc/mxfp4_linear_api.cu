@@ -136,6 +136,7 @@ int mxfp4_linear(const void* x, int64_t M, int64_t K, int64_t ldx, const void* p
     if (!x || !packed_b || !out) return MXFP4_ERR_ARG;
     if (!aligned(x, 16) || ldx % 8 != 0 || !aligned(packed_b, 1024) || !aligned(out, 2) || !aligned(residual, 2))
         return MXFP4_ERR_ALIGN;
+    if (out == x) return MXFP4_ERR_ARG;   // in place on a residual that is x: rows stored while others still read them
     Epilogue epi = {};
     epi.bias = bias;
     epi.bias_bf16 = bias_dtype == MXFP4_BF16 ? 1 : 0;

@@ -61,7 +61,8 @@ def mxfp4_linear(x: torch.Tensor, packed_b: torch.Tensor, N: int, bias: torch.Te
                  workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out [M, N] bf16 = act(MXFP4(x) . MXFP4(B)^T + bias) + residual, rounded once: mxfp4_gemm with what follows it.
     `packed_b`: mxfp4_prepack_b's; `bias` [N] fp32 or bf16; `activation`: none, relu, silu, gelu (by the normal
-    distribution function) or gelu_tanh; `residual` [M, N] bf16 with any row stride, which `out` may be itself."""
+    distribution function) or gelu_tanh; `residual` [M, N] bf16 with any row stride of N or more, which `out` may be
+    itself (but not where the residual is x)."""
     device = x.get_device()
     if device < 0 or device != _device():
         _dev(x, "x")

@@ -555,8 +555,9 @@ int mxfp4_moe_combine(const void *y, int64_t R, int64_t N, int64_t ldy, const in
  *               z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2.
  *   residual  : bf16 [M, N], row stride ldr (ldr >= N), 2-byte aligned, or NULL (ldr is then not used).
  *   out       : bf16 [M, N], row stride ldo (ldo >= N), 2-byte aligned. It may be the residual itself (the
- *               same pointer and stride: every element is read by the thread that writes it); otherwise
- *               it must not overlap any input.
+ *               same pointer and stride: what is added to an element is read before the element is
+ *               written). It must not overlap any other input, nor a residual in any other way; out ==
+ *               x is refused (MXFP4_ERR_ARG), also where x is the residual.
  *   workspace : ws_bytes >= mxfp4_linear_workspace_size(M, N, K), 256-byte aligned; may be NULL when
  *               that size is 0. Its previous contents do not matter. Calls sharing it must be ordered.
  * M == 0 or N == 0 is a no-op. Ordering as mxfp4_gemm: x, bias and residual are read and out is written
