@@ -348,6 +348,17 @@ def mxfp4_gemm_workspace_size(M: int, N: int, K: int, path: int = 0, splits: int
     return int(load_library().mxfp4_gemm_workspace_size_ex(M, N, K, _opts(path, splits, m_tile)))
 
 
+# entries that a table of remembered sizes holds; a full one starts again, so that a process that meets ever new
+# lengths does not grow with them
+_REMEMBERED = 4096
+
+
+def _remember(table: dict, key: tuple, value) -> None:
+    if len(table) >= _REMEMBERED:
+        table.clear()
+    table[key] = value
+
+
 _WS_NEED: dict = {}
 
 
@@ -358,26 +369,27 @@ def _ws_need(device: torch.device, M: int, N: int, K: int, path: int = 0, splits
     need = _WS_NEED.get(key)
     if need is None:
         need = mxfp4_gemm_workspace_size(M, N, K, path, splits, m_tile) if M and N else 0
-        _WS_NEED[key] = need
+        _remember(_WS_NEED, key, need)
     return need
 
 
 _PACKED_NEED: dict = {}
 
 
-def _check_packed(packed_b: torch.Tensor, N: int, K: int, device: torch.device | None) -> None:
-    """The packed weights must cover mxfp4_prepack_b_size(N, K) bytes on the GEMM's device: the
+def _check_packed(packed_b: torch.Tensor, N: int, K: int, device: torch.device | None) -> int:
+    """mxfp4_prepack_b_size(N, K), checked: the packed weights must cover mxfp4_prepack_b_size(N, K) bytes on the GEMM's device: the
     kernel streams that many bytes from the buffer's start, so a smaller buffer, or a view whose bytes
     do not lie next to each other, would be read past its end. `device` None checks only that the
     buffer is on a CUDA device (the per-step host call)."""
     need = _PACKED_NEED.get((N, K))
     if need is None:
         need = mxfp4_prepack_b_size(N, K)
-        _PACKED_NEED[(N, K)] = need
+        _remember(_PACKED_NEED, (N, K), need)
     if (need == 0 or packed_b.nbytes < need or not packed_b.is_contiguous() or not packed_b.is_cuda
             or (device is not None and packed_b.device != device)):
         raise ValueError(f"packed_b must be a contiguous CUDA buffer of at least mxfp4_prepack_b_size({N}, {K}) = {need}"
                          " bytes on the device of the other operands")
+    return need
 
 
 def mxfp4_workspace_init(ws: torch.Tensor, stream=None) -> None:

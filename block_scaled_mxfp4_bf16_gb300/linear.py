@@ -8,8 +8,9 @@ from __future__ import annotations
 
 import torch
 
-from . import (Mxfp4Error, _check, _dev, _on, _raw_stream, _stream, _writing, load_library, mxfp4_prepack_b_size)
-from .moe import _BF16, _F32, _bf16_rows, _device, _empty_strided, _index, _need, _out, _scratch
+from . import (Mxfp4Error, _check, _dev, _on, _raw_stream, _remember, _stream, _writing, load_library,
+               mxfp4_prepack_b_size)
+from .moe import _BF16, _F32, _bf16_rows, _device, _empty_strided, _index, _out, _scratch
 
 # the C ABI's activations
 ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
@@ -35,9 +36,9 @@ _SIZES: dict = {}
 
 def _sizes(key: tuple) -> tuple:
     query, packed_size, device, *sizes = key
-    known = (packed_size(*sizes[-2:]), _need(query, device, *sizes))
+    known = (packed_size(*sizes[-2:]), getattr(load_library(), query)(*sizes))  # the current device is theirs
     if known[0]:
-        _SIZES[key] = known
+        _remember(_SIZES, key, known)
     return known
 
 

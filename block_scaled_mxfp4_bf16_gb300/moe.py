@@ -10,7 +10,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import (_PACKED_NEED, _WS, Mxfp4Error, _check, _check_packed, _current_capturing, _dev, _on, _raw_stream, _stream,
+from . import (_WS, Mxfp4Error, _check, _check_packed, _current_capturing, _dev, _on, _raw_stream, _remember, _stream,
                _workspace, _writing, load_library, mxfp4_prepack_b, mxfp4_prepack_b_size)
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
@@ -26,7 +26,7 @@ def _need(query: str, device: int, *sizes: int) -> int:
     if need is None:
         need = getattr(load_library(), query)(*sizes)
         if need:
-            _NEED[key] = need
+            _remember(_NEED, key, need)
     return need
 
 
@@ -163,8 +163,7 @@ def mxfp4_grouped_gemm(a: torch.Tensor, packed_b: torch.Tensor, offsets: torch.T
         raise ValueError("packed_b must be a contiguous [E, bytes] buffer (mxfp4_prepack_experts)")
     E = packed_b.shape[0]
     if E and N:
-        _check_packed(packed_b, N, K, a.device)
-        if packed_b.nbytes != E * _PACKED_NEED[(N, K)]:
+        if packed_b.nbytes != E * _check_packed(packed_b, N, K, a.device):
             raise ValueError(f"packed_b's rows must have mxfp4_prepack_b_size({N}, {K}) bytes")
     offsets_ptr = _index(offsets, (E + 1,), a, "offsets")
     if rows is None:
