@@ -66,9 +66,9 @@ __device__ __forceinline__ uint64_t rcp_pair(uint64_t x) {
     return pair_of(fast_rcp(a), fast_rcp(b));
 }
 
-// The activations, each within 2^-15 of its value (a bf16 rounding is 2^-8): what an exponential's argument
-// loses by rounding, a few 2^-24 of up to 127, and what follows.
-// z / (1 + e^-z): the exponential overflows to infinity below -88, whose reciprocal is 0.
+// The activations, each within 2^-15 of its value (a bf16 rounding is 2^-8) and 2^-119: what an exponential's argument
+// loses by rounding, a few 2^-24 of up to 127, and what follows; a factor of z below 2^-126 is a zero here.
+// z / (1 + e^-z): the factor is 0 below z = -87.33, where the value is -87.33 2^-126 and falls.
 __device__ __forceinline__ uint64_t act_silu(uint64_t z) {
     return mul_pair(z, rcp_pair(add_pair(both(1.f), exp2_pair(mul_pair(z, both(-1.4426950408889634f))))));
 }
@@ -80,8 +80,9 @@ __device__ __forceinline__ uint64_t act_gelu_tanh(uint64_t z) {
 }
 // z Phi(z), Phi the normal distribution function. Its tail h = Phi(-|z|) as t 2^(-z^2 log2(e) / 2 + Q(t)) with
 // t = 1 / (1 + 0.35 |z|), the form of Numerical Recipes' erfc (section 6.2). Q is a least-maximum fit of degree
-// five made for this form from the logarithm of Phi in 64 bits: h is within 1.1e-5 of its value wherever an fp32
-// holds it. No difference of near values: for negative z the result is z h itself.
+// five made for this form from the logarithm of Phi in 64 bits: h is within 1.4e-5 of its value up to |z| = 13.08, where
+// the exponential falls below 2^-126, and 0 from there on. No difference of near values: for negative z the result is
+// z h itself.
 __device__ __forceinline__ uint64_t act_gelu(uint64_t z) {
     float a, b, ha, hb;
     halves_of(z, a, b);

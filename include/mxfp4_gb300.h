@@ -552,7 +552,8 @@ int mxfp4_moe_combine(const void *y, int64_t R, int64_t N, int64_t ldy, const in
  *               NULL (bias_dtype is then not used).
  *   activation: MXFP4_ACT_NONE; MXFP4_ACT_RELU max(z, 0); MXFP4_ACT_SILU z / (1 + e^-z);
  *               MXFP4_ACT_GELU z Phi(z), Phi the normal distribution function; MXFP4_ACT_GELU_TANH
- *               z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2.
+ *               z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2. Each is within 2^-15 of its value and
+ *               2^-119 (z's factor counts as 0 below 2^-126: silu from z = -87.33 down).
  *   residual  : bf16 [M, N], row stride ldr (ldr >= N), 2-byte aligned, or NULL (ldr is then not used).
  *   out       : bf16 [M, N], row stride ldo (ldo >= N), 2-byte aligned. It may be the residual itself (the
  *               same pointer and stride: what is added to an element is read before the element is
