@@ -334,9 +334,9 @@ __device__ __forceinline__ void load_sums(uint32_t taddr, int nacc, uint32_t acc
 
 // Whole sums of a lane's weight row n from tensor memory to C, kN tokens at a time: of `tokens` (the first is row0 of
 // C) those from `first` on, every step-th kN of them. load_first asks for what the first run adds. The whole warp calls
-// both. 16 tokens, not 32: with 137 and 168 registers a thread instead of 80, no second CTA of the weight-resident
-// kernel, and no block of the quantizer beside the streaming one, fits the SM (256x4096x7168 with bias and
-// residual 14.6 us, not 13.5).
+// both. 16 tokens, not 32: with more than 80 registers a thread no second CTA of the weight-resident kernel, and no block
+// of the quantizer beside the GEMM on token blocks, fits the SM (256x4096x7168 with bias and residual 14.6 us, not 13.5).
+// The streaming kernel holds 168 a thread with 16 as well, so nothing fits beside it.
 template <int kEpi, int kN = 16>
 struct LaneStore {
     std::conditional_t<linear_epilogue(kEpi), TokenRun<kN>, GatedBias> add;

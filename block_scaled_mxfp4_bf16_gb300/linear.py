@@ -2,7 +2,7 @@
 the activation and the product of a gated feed-forward block) and its form for experts' groups of rows. As in the
 rest of the binding, the functions only check and marshal arguments; every step runs in the library's CUDA kernels.
 
-A call of a few tokens takes the GPU 2 to 5 us and the host 7 to 8: it reads every tensor property once, keeps the
+A call of a few tokens takes the GPU 2 to 5 us and the host 7 or more, half as much again on a busy one: it reads every tensor property once, keeps the
 sizes that the library answers by shape, and leaves the reports of what is wrong to slower helpers."""
 from __future__ import annotations
 
